@@ -32,6 +32,7 @@ GQA_ERR_DEVICE_BAD_INPUT = -7
 
 # name -> (restype, argtypes); every symbol include/gqa_attn.h declares.
 _P, _I, _F, _S = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
+_L = ctypes.c_int64
 _SIGNATURES = {
     "gqa_attn_decode": (_I, [_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _F, _I, _P]),
     "gqa_attn_decode_ws": (_I, [_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _F, _I, _P, _S,
@@ -49,6 +50,13 @@ _SIGNATURES = {
     "gqa_attn_prefill_ex": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _F, _P]),
     "gqa_attn_prefill_partial": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _I,
                                       _F, _P]),
+    "gqa_attn_prefill_packed": (_I, [_P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _L, _L,
+                                     _L, _L, _L, _L, _I, _F, _P]),
+    "gqa_attn_decode_tree": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I,
+                                  _I, _I, _L, _L, _L, _L, _L, _L, _F, _P, _S, _P]),
+    "gqa_attn_decode_tree_workspace_size": (_S, [_I, _I, _I, _I]),
+    "gqa_attn_cache_append": (_I, [_P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _L, _L,
+                                   _L, _L, _P]),
     "gqa_attn_pick_num_splits": (_I, [_I, _I, _I, _I]),
     "gqa_attn_pick_num_splits_q8": (_I, [_I, _I, _I, _I]),
     "gqa_attn_pick_num_splits_q4": (_I, [_I, _I, _I, _I]),
@@ -604,6 +612,235 @@ def prefill_partial(q, k, v, *, q_offset: int = 0, key_offset: int = 0, causal: 
     if rc != GQA_OK:
         raise GqaError(rc, "gqa_attn_prefill_partial")
     return out, lse
+
+
+# ---- ragged batches ---------------------------------------------------------
+
+
+def gqa_attn_prefill_packed(q, k, v, o, lse, cu_q, cu_k, B, H_q, H_kv, d, total_q, total_k,
+                            q_stride_t, q_stride_h, k_stride_t, k_stride_h, v_stride_t,
+                            v_stride_h, causal, scale, stream):
+    return lib().gqa_attn_prefill_packed(q, k, v, o, lse, cu_q, cu_k, B, H_q, H_kv, d, total_q,
+                                         total_k, q_stride_t, q_stride_h, k_stride_t, k_stride_h,
+                                         v_stride_t, v_stride_h, causal, scale, stream)
+
+
+def gqa_attn_decode_tree(q, k_new, v_new, k_cache, v_cache, o, lse, cu_seqlens, context_lens,
+                         tree_mask, mask_words, B, H_q, H_kv, d, total, max_tokens, S_max,
+                         q_stride_t, q_stride_h, k_stride_t, k_stride_h, v_stride_t, v_stride_h,
+                         scale, workspace, workspace_bytes, stream):
+    return lib().gqa_attn_decode_tree(q, k_new, v_new, k_cache, v_cache, o, lse, cu_seqlens,
+                                      context_lens, tree_mask, mask_words, B, H_q, H_kv, d, total,
+                                      max_tokens, S_max, q_stride_t, q_stride_h, k_stride_t,
+                                      k_stride_h, v_stride_t, v_stride_h, scale, workspace,
+                                      workspace_bytes, stream)
+
+
+def gqa_attn_decode_tree_workspace_size(H_q, H_kv, d, max_tokens):
+    return lib().gqa_attn_decode_tree_workspace_size(H_q, H_kv, d, max_tokens)
+
+
+def gqa_attn_cache_append(k_cache, v_cache, k_new, v_new, cu_seqlens, starts, index, B, H_kv, d,
+                          S_max, total, total_new, k_stride_t, k_stride_h, v_stride_t, v_stride_h,
+                          stream):
+    return lib().gqa_attn_cache_append(k_cache, v_cache, k_new, v_new, cu_seqlens, starts, index,
+                                       B, H_kv, d, S_max, total, total_new, k_stride_t, k_stride_h,
+                                       v_stride_t, v_stride_h, stream)
+
+
+def _packed(name, t, heads=None, d=None):
+    """Checks a packed [tokens, heads, d] bf16 tensor; returns its token and head strides."""
+    import torch
+
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be bfloat16, got {t.dtype}")
+    if t.dim() != 3 or (heads is not None and t.shape[1] != heads) or (
+            d is not None and t.shape[2] != d):
+        want = f"[tokens, {'heads' if heads is None else heads}, {'d' if d is None else d}]"
+        raise ValueError(f"{name} must be {want}, got {tuple(t.shape)}")
+    if t.stride(2) != 1:
+        raise ValueError(f"the last dimension of {name} must be contiguous")
+    # the stride of a dimension of size 1 says nothing: any valid one will do
+    st = t.stride(0) if t.shape[0] > 1 else 8
+    sh = t.stride(1) if t.shape[1] > 1 else 8
+    return st, sh
+
+
+def _ints(name, t, n, device):
+    import torch
+
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or not t.is_contiguous():
+        raise TypeError(f"{name} must be a contiguous int32 CUDA tensor")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}")
+    if t.numel() != n:
+        raise ValueError(f"{name} must have {n} elements, got {t.numel()}")
+
+
+def _outputs(q, out, lse):
+    import torch
+
+    if out is None:
+        out = torch.empty(tuple(q.shape), dtype=torch.bfloat16, device=q.device)
+    elif (out.dtype != torch.bfloat16 or out.shape != q.shape or not out.is_contiguous()
+          or out.device != q.device):
+        raise ValueError("out must be a contiguous bfloat16 tensor shaped like q on its device")
+    if lse is None:
+        lse = torch.empty(tuple(q.shape[:2]), dtype=torch.float32, device=q.device)
+    elif (lse.dtype != torch.float32 or lse.shape != q.shape[:2] or not lse.is_contiguous()
+          or lse.device != q.device):
+        raise ValueError("lse must be a contiguous float32 [tokens, H_q] tensor on q's device")
+    return out, lse
+
+
+def _same_device(q, **others):
+    for name, t in others.items():
+        if t is not None and t.device != q.device:
+            raise ValueError(f"{name} must be on {q.device}, got {t.device}")
+
+
+def prefill_packed(q, k, v, cu_seqlens, cu_seqlens_k=None, *, causal: bool = True,
+                   scale: float | None = None, out=None, lse=None, stream=None):
+    """Attention over packed sequences of different lengths. q [total_q,H_q,d], k/v
+    [total_k,H_kv,d] bf16 CUDA (any token and head strides that are multiples of 8, so slices of
+    a fused projection are taken as they are); cu_seqlens, cu_seqlens_k int32 [B+1] prefix sums
+    of the query and key counts (cu_seqlens_k None: the same). The queries of a sequence are its
+    last tokens: causal query t sees keys j <= n_k - n_q + t.
+
+    Returns (o [total_q,H_q,d] bf16, lse [total_q,H_q] fp32). Rows behind the last sequence are
+    not written. The call runs on ``stream`` (default: the current stream of q's device).
+    """
+    import torch
+
+    qs = _packed("q", q)
+    total_q, H_q, d = q.shape
+    ks = _packed("k", k, None, d)
+    vs = _packed("v", v, k.shape[1], d)
+    if v.shape != k.shape:
+        raise ValueError("k and v must have the same shape")
+    _same_device(q, k=k, v=v)
+    B = cu_seqlens.numel() - 1 if isinstance(cu_seqlens, torch.Tensor) else 0
+    if B < 0:
+        raise ValueError("cu_seqlens must have B + 1 elements")
+    _ints("cu_seqlens", cu_seqlens, B + 1, q.device)
+    if cu_seqlens_k is not None:
+        _ints("cu_seqlens_k", cu_seqlens_k, B + 1, q.device)
+    elif k.shape[0] != total_q:
+        raise ValueError("k and v must have q's tokens when cu_seqlens_k is not given")
+    sc = 1.0 / math.sqrt(d) if scale is None else float(scale)
+    with torch.cuda.device(q.device):
+        out, lse = _outputs(q, out, lse)
+        rc = gqa_attn_prefill_packed(_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse),
+                                     _ptr(cu_seqlens), _ptr(cu_seqlens_k), B, H_q, k.shape[1], d,
+                                     total_q, k.shape[0], *qs, *ks, *vs, 1 if causal else 0, sc,
+                                     _stream_ptr(stream))
+    if rc != GQA_OK:
+        raise GqaError(rc, "gqa_attn_prefill_packed")
+    return out, lse
+
+
+def _check_cache(k_cache, v_cache, H_kv, d):
+    _check_cuda_bf16("k_cache", k_cache, 4)
+    _check_cuda_bf16("v_cache", v_cache, 4)
+    if v_cache.shape != k_cache.shape or k_cache.shape[1] != H_kv or k_cache.shape[3] != d:
+        raise ValueError("k_cache, v_cache must be [B, H_kv, S_max, d] matching k_new, v_new")
+
+
+def decode_tree(q, k_new, v_new, k_cache, v_cache, context_lens, *, cu_seqlens=None,
+                max_tokens: int | None = None, tree_mask=None, scale: float | None = None,
+                out=None, lse=None, stream=None, workspace=None):
+    """Attention of drafted tokens over the cache: row b has context_lens[b] (int32 [B]) tokens in
+    k_cache/v_cache [B,H_kv,S_max,d] and its drafted tokens packed in q [total,H_q,d],
+    k_new/v_new [total,H_kv,d] (prefix sums cu_seqlens int32 [B+1]; None: total / B per row).
+    A drafted token sees its row's context and the drafted tokens whose bits are set in its row of
+    tree_mask (int32 [total, words], bit j for the row's token j), or with tree_mask None those
+    up to itself. max_tokens (at most 128) bounds a row's drafted tokens; it is needed with
+    cu_seqlens, whose values stay on the device.
+
+    Returns (o [total,H_q,d] bf16, lse [total,H_q] fp32). ``workspace``: a uint8 CUDA tensor of
+    gqa_attn_decode_tree_workspace_size bytes that no overlapping call uses; by default one is
+    allocated for the call.
+    """
+    import torch
+
+    qs = _packed("q", q)
+    total, H_q, d = q.shape
+    ks = _packed("k_new", k_new, None, d)
+    vs = _packed("v_new", v_new, k_new.shape[1], d)
+    H_kv = k_new.shape[1]
+    if v_new.shape != k_new.shape or k_new.shape[0] != total:
+        raise ValueError("k_new, v_new must be [total, H_kv, d] with q's tokens")
+    _check_cache(k_cache, v_cache, H_kv, d)
+    _same_device(q, k_new=k_new, v_new=v_new, k_cache=k_cache, v_cache=v_cache,
+                 tree_mask=tree_mask, workspace=workspace)
+    B, S_max = k_cache.shape[0], k_cache.shape[2]
+    _ints("context_lens", context_lens, B, q.device)
+    if cu_seqlens is not None:
+        _ints("cu_seqlens", cu_seqlens, B + 1, q.device)
+        if max_tokens is None:
+            raise ValueError("max_tokens is needed with cu_seqlens")
+    else:
+        if B == 0 or total % B:
+            raise ValueError("without cu_seqlens every row has total / B drafted tokens")
+        max_tokens = max(1, total // B) if max_tokens is None else max_tokens
+    words = 0
+    if tree_mask is not None:
+        if (tree_mask.dtype != torch.int32 or tree_mask.dim() != 2 or tree_mask.shape[0] != total
+                or not tree_mask.is_contiguous()):
+            raise ValueError("tree_mask must be a contiguous int32 [total, words] tensor")
+        words = tree_mask.shape[1]
+    sc = 1.0 / math.sqrt(d) if scale is None else float(scale)
+    with torch.cuda.device(q.device):
+        st = stream if stream is not None else torch.cuda.current_stream()
+        out, lse = _outputs(q, out, lse)
+        if workspace is None:
+            # from the launch stream's pool: its memory is reused only behind this call
+            n = gqa_attn_decode_tree_workspace_size(H_q, H_kv, d, max_tokens)
+            with torch.cuda.stream(st):
+                workspace = torch.empty(max(n, 256), dtype=torch.uint8, device=q.device)
+        rc = gqa_attn_decode_tree(_ptr(q), _ptr(k_new), _ptr(v_new), _ptr(k_cache), _ptr(v_cache),
+                                  _ptr(out), _ptr(lse), _ptr(cu_seqlens), _ptr(context_lens),
+                                  _ptr(tree_mask), words, B, H_q, H_kv, d, total, max_tokens,
+                                  S_max, *qs, *ks, *vs, sc, _ptr(workspace),
+                                  workspace.numel() * workspace.element_size(), st.cuda_stream)
+    if rc != GQA_OK:
+        raise GqaError(rc, "gqa_attn_decode_tree")
+    return out, lse
+
+
+def cache_append(k_cache, v_cache, k_new, v_new, starts, *, cu_seqlens=None, index=None,
+                 stream=None):
+    """Writes packed tokens into the cache k_cache/v_cache [B,H_kv,S_max,d]: entry i of row b (the
+    packed entry cu_seqlens[b] + i; cu_seqlens None: the same number for every row) goes to slot
+    starts[b] + i (int32 [B]). Entry e is token e of k_new/v_new [tokens,H_kv,d], or token
+    index[e] (int32) when index is given, such as the accepted path of a drafted tree."""
+    import torch
+
+    ks = _packed("k_new", k_new)
+    total_new, H_kv, d = k_new.shape
+    vs = _packed("v_new", v_new, H_kv, d)
+    if v_new.shape != k_new.shape:
+        raise ValueError("k_new and v_new must have the same shape")
+    _check_cache(k_cache, v_cache, H_kv, d)
+    _same_device(k_cache, v_cache=v_cache, k_new=k_new, v_new=v_new)
+    B, S_max = k_cache.shape[0], k_cache.shape[2]
+    _ints("starts", starts, B, k_cache.device)
+    total = total_new
+    if index is not None:
+        total = index.numel() if isinstance(index, torch.Tensor) else 0
+        _ints("index", index, total, k_cache.device)
+    if cu_seqlens is not None:
+        _ints("cu_seqlens", cu_seqlens, B + 1, k_cache.device)
+    elif B == 0 or total % B:
+        raise ValueError("without cu_seqlens every row has the same number of entries")
+    with torch.cuda.device(k_cache.device):
+        rc = gqa_attn_cache_append(_ptr(k_cache), _ptr(v_cache), _ptr(k_new), _ptr(v_new),
+                                   _ptr(cu_seqlens), _ptr(starts), _ptr(index), B, H_kv, d, S_max,
+                                   total, total_new, *ks, *vs, _stream_ptr(stream))
+    if rc != GQA_OK:
+        raise GqaError(rc, "gqa_attn_cache_append")
 
 
 def check(stream=None):

@@ -24,7 +24,7 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libgqa_attn.so")
 DEBUG_LIB = os.path.join(PKG, "libgqa_attn_debug.so")
 
-SOURCES = ["plan.cpp", "runtime.cu", "decode.cu", "prefill.cu"]
+SOURCES = ["plan.cpp", "runtime.cu", "decode.cu", "prefill.cu", "ragged.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 # Hidden visibility: only the C ABI (GQA_API in include/gqa_attn.h) is exported,
 # so two builds loaded in one process (the product and the -DGQA_DEBUG library)

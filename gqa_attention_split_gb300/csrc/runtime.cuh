@@ -52,6 +52,14 @@ cudaError_t encode_tmap_3d_bf16(CUtensorMap* map, const void* base, uint64_t inn
                                 uint64_t rows, uint64_t outer, uint32_t box_inner,
                                 uint32_t box_rows, CUtensorMapSwizzle swizzle);
 
+// 3-D bf16 tensor map over rows of `inner` elements with explicit strides (in
+// elements, multiples of 8) for the middle and the outer dimension; 128-byte
+// swizzle, box {64, box_mid, box_outer}.
+cudaError_t encode_tmap_3d_bf16_strided(CUtensorMap* map, const void* base, uint64_t inner,
+                                        uint64_t mid, uint64_t outer, uint64_t mid_stride,
+                                        uint64_t outer_stride, uint32_t box_mid,
+                                        uint32_t box_outer);
+
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 }  // namespace gqa

@@ -330,6 +330,99 @@ GQA_API int gqa_attn_prefill_partial(const uint16_t* q, const uint16_t* k, const
                                      int d, int T_q, int S_kv, int q_offset, int key_offset,
                                      int causal, float scale, cudaStream_t stream);
 
+/* -------------------------------------------------------- ragged batches --
+ * Sequences of different lengths packed one behind the other, and what a
+ * speculative decoding step does with them. No page has a counterpart; the
+ * mathematics is the one above: O = softmax(Q K^T * scale + mask) V and lse,
+ * per query, over the keys that the query sees. A query that sees no key gets
+ * O = 0 and lse = -inf. A key that a query does not see never reaches its
+ * result, whatever K and V hold there (NaN and infinities included): other
+ * sequences' tokens, later or masked-out tokens, cache slots behind the
+ * context.
+ *
+ * Packed tensors are [tokens, heads, d] bf16 with the last dimension
+ * contiguous. Their token and head strides are in elements, positive
+ * multiples of 8 (ignored for a dimension of size 1), so slices of a fused
+ * projection and head-major tensors are taken as they are. o is contiguous
+ * [tokens, H_q, d], lse contiguous fp32 [tokens, H_q] or NULL. Rows of o and
+ * lse that belong to no sequence are not written. q, k, v, o are 16-byte
+ * aligned.
+ *
+ * Prefix sums (cu_*): device int32 [B + 1], row b holds the packed tokens
+ * cu[b] .. cu[b + 1] - 1. Values that leave [0, total] or decrease are clamped
+ * and reported as GQA_ERR_DEVICE_BAD_INPUT by gqa_attn_check(). B <= 65535.
+ * scale > 0 (as gqa_attn_prefill). The calls allocate nothing, keep nothing
+ * and can be captured into graphs.
+ */
+
+/* Attention over packed sequences. Query t of a sequence with n_q queries and
+ * n_k keys sees its keys j <= n_k - n_q + t (causal != 0; the queries are the
+ * last n_q tokens) or all n_k of them (causal == 0).
+ *   cu_k : prefix sums of the keys, or NULL: the same as cu_q (and then
+ *          total_k == total_q).
+ * Any lengths, zero included. H_q / H_kv <= 128. */
+GQA_API int gqa_attn_prefill_packed(const uint16_t* q, const uint16_t* k, const uint16_t* v,
+                                    uint16_t* o, float* lse, const int32_t* cu_q,
+                                    const int32_t* cu_k, int B, int H_q, int H_kv, int d,
+                                    int total_q, int total_k, int64_t q_stride_t,
+                                    int64_t q_stride_h, int64_t k_stride_t, int64_t k_stride_h,
+                                    int64_t v_stride_t, int64_t v_stride_h, int causal,
+                                    float scale, cudaStream_t stream);
+
+/* Attention of drafted tokens over the cache (the verification step of
+ * speculative decoding). Row b has context_lens[b] tokens in the cache
+ * k_cache, v_cache [B, H_kv, S_max, d] (contiguous) and its drafted tokens in
+ * q, k_new, v_new, which are not in the cache yet. A drafted token sees the
+ * whole context, and
+ *   tree_mask != NULL: the drafted tokens j of its row whose bit is set, bit
+ *       j & 31 of word j >> 5 of its mask_words words (int32
+ *       [total, mask_words], mask_words * 32 >= max_tokens). A tree sets the
+ *       bits of a token's ancestors and its own; bits behind the row's last
+ *       token are ignored;
+ *   tree_mask == NULL: the drafted tokens up to itself (a line; one token per
+ *       row is ordinary decoding with the new token outside the cache).
+ *   cu_seqlens   : prefix sums of the drafted tokens, or NULL: total / B each.
+ *   max_tokens   : no row has more drafted tokens, 1..128. A longer row is cut
+ *                  there and reported as GQA_ERR_DEVICE_BAD_INPUT.
+ *   context_lens : device int32 [B]; values outside [0, S_max] are clamped
+ *                  and reported the same way.
+ *   workspace    : 256-byte aligned device memory of at least
+ *                  gqa_attn_decode_tree_workspace_size() bytes. It holds no
+ *                  state between calls; calls that overlap on the GPU must not
+ *                  share one.
+ * H_q / H_kv <= 16. The result does not depend on the other rows. */
+GQA_API int gqa_attn_decode_tree(const uint16_t* q, const uint16_t* k_new,
+                                 const uint16_t* v_new, const uint16_t* k_cache,
+                                 const uint16_t* v_cache, uint16_t* o, float* lse,
+                                 const int32_t* cu_seqlens, const int32_t* context_lens,
+                                 const int32_t* tree_mask, int mask_words, int B, int H_q,
+                                 int H_kv, int d, int total, int max_tokens, int S_max,
+                                 int64_t q_stride_t, int64_t q_stride_h, int64_t k_stride_t,
+                                 int64_t k_stride_h, int64_t v_stride_t, int64_t v_stride_h,
+                                 float scale, void* workspace, size_t workspace_bytes,
+                                 cudaStream_t stream);
+
+/* Bytes of workspace for gqa_attn_decode_tree (0 on invalid sizes). */
+GQA_API size_t gqa_attn_decode_tree_workspace_size(int H_q, int H_kv, int d, int max_tokens);
+
+/* Writes packed tokens into the cache [B, H_kv, S_max, d] (contiguous): entry
+ * i of row b, the packed entry e = cu_seqlens[b] + i, goes to slot
+ * starts[b] + i of row b. It is token e of k_new, v_new, or token index[e]
+ * (device int32 [total]) when index is given: the accepted path of a row's
+ * drafted tokens, say. Other slots are left as they are.
+ *   total        : entries; total_new: tokens in k_new, v_new (total_new >=
+ *                  total without index).
+ *   cu_seqlens   : prefix sums of the entries, or NULL: total / B per row.
+ * An entry whose slot lies outside [0, S_max) or whose index lies outside
+ * [0, total_new) is not written and reported as GQA_ERR_DEVICE_BAD_INPUT by
+ * gqa_attn_check(). k_new, v_new must not overlap the cache. */
+GQA_API int gqa_attn_cache_append(uint16_t* k_cache, uint16_t* v_cache, const uint16_t* k_new,
+                                  const uint16_t* v_new, const int32_t* cu_seqlens,
+                                  const int32_t* starts, const int32_t* index, int B, int H_kv,
+                                  int d, int S_max, int total, int total_new, int64_t k_stride_t,
+                                  int64_t k_stride_h, int64_t v_stride_t, int64_t v_stride_h,
+                                  cudaStream_t stream);
+
 /* ------------------------------------------------------ plan / scheduler --
  * Integer helpers the kernels use, exported so tests can compare them with
  * independent derivations bit for bit. Host-only; no GPU needed.
