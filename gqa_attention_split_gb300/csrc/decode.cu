@@ -126,13 +126,6 @@ struct SplitCfg {
     static_assert(kStageBytes % 1024 == 0, "stages stay aligned for the TMA swizzle");
 };
 
-__device__ __forceinline__ void pdl_launch_dependents() {
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-}
-__device__ __forceinline__ void pdl_wait_primary() {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-}
-
 __device__ __forceinline__ int load_seqlen(const int32_t* seqlens, int b, int S_max,
                                            unsigned* status, bool report, bool ring) {
     int sl = seqlens ? seqlens[b] : S_max;
@@ -209,7 +202,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1)
 
     // With more than one group per row the combine kernel follows: let it be
     // scheduled now (it waits for this grid before reading anything).
-    if (p.n_groups > 1) pdl_launch_dependents();
+    if (p.n_groups > 1) grid_launch_dependents();
 
     // ---- set-up that touches no global memory: it may overlap the previous
     // kernel in the stream (programmatic dependent launch).
@@ -270,7 +263,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1)
         }
     }
 
-    pdl_wait_primary();  // everything below may read what earlier kernels wrote
+    grid_wait_primary();  // everything below may read what earlier kernels wrote
     if (threadIdx.x == 0) GQA_TRACE_STAMP(blin, 1);
 
     const int seqlen = load_seqlen(p.seqlens, b, p.S_max, p.status,
@@ -842,7 +835,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1)
         // 9.04-9.07 with the trigger after the stream; 9-call graphs lose
         // ~1.5% (9.17-9.20 against 9.02-9.06 us).
         if (p.n_groups == 1 && !triggered && issued == my_n) {
-            pdl_launch_dependents();
+            grid_launch_dependents();
             triggered = true;
         }
     }
@@ -877,7 +870,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1)
     // A warp without tiles (or whose wait ran out) lets the next kernel
     // launch here. A combine kernel that follows was allowed to launch at the
     // start.
-    if (p.n_groups == 1 && !triggered) pdl_launch_dependents();
+    if (p.n_groups == 1 && !triggered) grid_launch_dependents();
 
     // ---- level 2a: the other warps hand their partials to warp 0, which
     // merges them fragment by fragment in registers (warp order fixed).
@@ -1044,8 +1037,8 @@ __global__ void __launch_bounds__(kCombineWarps * 32)
     constexpr int kPer = D / 32;  // dims per lane
     using VecT = typename std::conditional<kPer == 4, float4, float2>::type;
     if (threadIdx.x == 0) GQA_TRACE_STAMP(kTraceCombineBase + blockIdx.x, 0);
-    pdl_launch_dependents();      // the next kernel may start its own set-up
-    pdl_wait_primary();           // the split grid's partials are complete and visible
+    grid_launch_dependents();      // the next kernel may start its own set-up
+    grid_wait_primary();           // the split grid's partials are complete and visible
     if (threadIdx.x == 0) GQA_TRACE_STAMP(kTraceCombineBase + blockIdx.x, 1);
     const int lane = threadIdx.x & 31;
     const int row = blockIdx.x * kCombineWarps + (threadIdx.x >> 5);

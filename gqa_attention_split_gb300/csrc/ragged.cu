@@ -1,5 +1,6 @@
-// Attention over ragged batches: packed prompts, and drafted token trees on
-// top of the KV cache; and appending packed tokens to the cache.
+// Attention over ragged batches on the 5th-generation tensor cores: packed
+// prompts, and drafted token trees on top of the KV cache; and appending
+// packed tokens to the cache.
 //
 //   O = softmax(scale * Q K^T over the visible keys) V,   lse = ln sum exp(.)
 //
@@ -8,6 +9,20 @@
 // visible), then the row's own packed tokens (prefill_packed: a causal limit
 // or all of them; decode_tree: the bits of a mask, or a line). A key that a
 // query does not see never reaches its result, whatever K and V hold there.
+//
+// Layout of the work. The G query heads of a KV head are folded into the rows
+// of the matrix products: a group of rows is tok = floor(128 / G) consecutive
+// tokens x G heads (token-major, one TMA box {64, G, tok} per 64 columns), so
+// a causal diagonal is only tok tokens wide and a short prompt or a small
+// tree still fills rows. A work item is up to two groups that read the same
+// K/V tiles of 128 keys.
+//
+// Roles of a CTA (one per SM, persistent): warp 0 TMA, warp 1 issues every
+// tcgen05.mma, warp 2 finds the work items from the prefix sums on the device
+// and passes them on through a ring in shared memory, warp 3 repairs V tiles
+// whose keys not every row may see, two warpgroups run the online softmax,
+// one query row per thread. S and O live in tensor memory, P is written over
+// its S columns and read from there by the P V product.
 
 #include <cuda_runtime.h>
 #include <math.h>
@@ -16,32 +31,77 @@
 #include "plan.cuh"
 #include "ptx.cuh"
 #include "runtime.cuh"
+#include "tcgen05.cuh"
 
 namespace gqa {
 namespace ragged {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr int kMaxTreeTokens = 128;
+constexpr int kMaxTreeTokens = 128;  // drafted tokens of a row: one tile of keys
+constexpr int BM = kPrefillBlockM;   // rows of a group
+constexpr int BN = kPrefillBlockN;   // keys of a tile
+constexpr int kThreads = 384;
+constexpr int kRingSlots = 4;        // K/V tiles in flight
+constexpr int kItemSlots = 4;        // work items known ahead
+constexpr int kSchedSeqs = 1024;     // sequences whose schedule is kept in shared memory
+constexpr int kTreeCtas = 152;       // most CTAs of a decode_tree launch (workspace size)
+constexpr uint32_t kBoxBytes = BM * 128;       // 128 rows x 64 bf16
+constexpr uint32_t kStageBytes = 32 * 64;      // a warp's output stage: 32 rows x 64 B
+constexpr uint32_t kTmemCols = 512;            // S_0, S_1, O_0, O_1
+// rescale O only when the running maximum (base 2) grew by more than this: P <= 2^8
+constexpr float kRescaleThreshold = 8.f;
+
+// kPrompts: items are blocks of 2 * tok tokens of a sequence, all of its keys.
+// kTreePair: items are blocks of 2 * tok drafted tokens, a range of the keys.
+// kTreeAlt: all drafted tokens of a row fit in one group; the two softmax
+// groups take alternate K/V tiles and are merged in the epilogue.
+enum Mode { kPrompts, kTreePair, kTreeAlt };
 
 struct Params {
-    const uint16_t *q, *k, *v;    // packed [total, heads, d], strides below
-    const uint16_t *kc, *vc;      // cache [B, H_kv, S_max, d] (decode_tree)
+    const uint16_t* v;            // packed V, read again only for values that are not finite
     uint16_t* o;                  // [total_q, H_q, d]
     float* lse;                   // [total_q, H_q] or null
+    float *part_o, *part_lse;     // decode_tree: [slot][part_rows][d], [slot][part_rows]
     const int32_t *cu_q, *cu_k, *ctx;
     const uint32_t* mask;         // [total_q, mask_words] or null
     unsigned* status;
-    int64_t q_st, q_sh, k_st, k_sh, v_st, v_sh;
-    int B, H_q, H_kv, G, total_q, total_k, S_max, max_tokens, mask_words, causal, tree;
+    int64_t v_st, v_sh;
+    int B, H_q, H_kv, G, total_q, total_k, S_max, max_tokens, mask_words, causal;
+    int tok;          // tokens of a group
+    int head_group;   // kPrompts: KV heads whose items are scheduled together
+    int team;         // decode_tree: CTAs that share a range of keys, one per token block
+    int n_teams, min_tiles, part_rows;
     float scale_log2;
+    int inject_timeout;  // test hook: block 0 withholds its first Q copy
 };
 
+// One work item: tiles j0 .. j0 + n - 1 of a row's tile list (the context's
+// tiles, c_t of them, then its own tokens') against one or two groups of rows.
+struct __align__(16) Item {
+    int n;       // tiles, the larger of n0 and n1; -1: no more items
+    int n0, n1;  // tiles of group 0 and 1 (kTreeAlt: unused)
+    int j0;
+    int kvh, b;
+    int dst;     // partial slot, or -1: the item is the whole row, write O and lse
+    int ctx;     // context length
+    int q_row;   // packed index of the row's first token
+    int tok0;    // first token of group 0, counted in the row
+    int T;       // tokens of the row
+    int c_t;     // context tiles
+    int k_row;   // packed index of the row's first own key
+    int off;     // own key of token 0 (keys minus queries)
+    int n_own;   // own keys
+    int pad;
+};
+static_assert(sizeof(Item) == 64, "four 16-byte copies");
+
 __device__ __forceinline__ int clampi(int x, int lo, int hi) { return min(max(x, lo), hi); }
+__device__ __forceinline__ int cdiv(int a, int b) { return (a + b - 1) / b; }
 
 // First packed token and token count of row b under prefix sums cu (null:
 // every row has total / B tokens). Bad prefix sums are clamped: the row stays
-// inside [0, total), and *bad is set.
+// inside [0, total), and bad is set.
 __device__ __forceinline__ void row_range(const int32_t* cu, int B, int total, int b, int& first,
                                           int& count, bool& bad) {
     if (!cu) {
@@ -56,75 +116,1114 @@ __device__ __forceinline__ void row_range(const int32_t* cu, int B, int total, i
     bad = bad || first != a || last != e;
 }
 
-__device__ __forceinline__ int context_of(const Params& p, int b, bool& bad) {
-    const int c = p.ctx[b], n = clampi(c, 0, p.S_max);
-    bad = bad || n != c;
-    return n;
+__device__ __forceinline__ void tree_row(const Params& p, int b, int& first, int& T, int& ctx,
+                                         bool& bad) {
+    row_range(p.cu_q, p.B, p.total_q, b, first, T, bad);
+    if (T > p.max_tokens) {
+        T = p.max_tokens;
+        bad = true;
+    }
+    const int c = p.ctx[b];
+    ctx = clampi(c, 0, p.S_max);
+    bad = bad || ctx != c;
 }
 
-// One warp per (packed token, query head).
+// Tiles that each block of a row's drafted tokens runs: the context's and one
+// for the drafted tokens.
+__device__ __forceinline__ int tree_tiles(int T, int ctx) {
+    return T > 0 ? cdiv(ctx, BN) + 1 : 0;
+}
+
+// ---- limits of an item, as every role needs them
+
+// Own keys visible to token t (kPrompts).
+__device__ __forceinline__ int token_limit(const Params& p, const Item& w, int t) {
+    return p.causal ? clampi(w.off + t + 1, 0, w.n_own) : w.n_own;
+}
+// Own keys that every row of group g sees / that some row of it sees.
+template <int kMode>
+__device__ __forceinline__ int group_first(const Params& p, const Item& w, int g) {
+    return kMode == kPrompts ? token_limit(p, w, w.tok0 + g * p.tok) : 0;
+}
+template <int kMode>
+__device__ __forceinline__ int group_last(const Params& p, const Item& w, int g) {
+    return kMode == kPrompts ? token_limit(p, w, min(w.T, w.tok0 + (g + 1) * p.tok) - 1) : w.n_own;
+}
+// Keys of tile jj that some row of group g sees (1..128).
+template <int kMode>
+__device__ __forceinline__ int tile_keys(const Params& p, const Item& w, int jj, int g) {
+    if (kMode != kPrompts && jj < w.c_t) return min(BN, w.ctx - jj * BN);
+    return clampi(group_last<kMode>(p, w, g) - (jj - w.c_t) * BN, 0, BN);
+}
+// The keys of V tile jj that the P V products read are [0, end). Those from
+// `seen` on are not visible to every row, those from `keys` on to none.
+struct Repair {
+    int seen, keys, end;
+    __device__ bool needed() const { return seen < end; }
+};
+template <int kMode>
+__device__ __forceinline__ Repair repair_of(const Params& p, const Item& w, int jj) {
+    const int last = kMode == kPrompts && w.n1 > 0 ? 1 : 0;  // the group that sees more
+    Repair r;
+    r.keys = tile_keys<kMode>(p, w, jj, last);
+    r.end = (r.keys + 15) & ~15;
+    r.seen = kMode != kPrompts && jj < w.c_t
+                 ? r.keys
+                 : clampi(group_first<kMode>(p, w, 0) - (jj - w.c_t) * BN, 0, r.keys);
+    return r;
+}
+
+// ---- shared memory
+
 template <int D>
-__global__ void __launch_bounds__(256) rows_kernel(const Params p) {
-    constexpr int kPer = D / 32;
-    const int lane = threadIdx.x & 31;
-    const int64_t w = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5);
-    if (w >= int64_t(p.total_q) * p.H_q) return;
-    const int tok = int(w / p.H_q), h = int(w % p.H_q), hk = h / p.G;
-    int b = 0, q0 = 0, T = 0;
+struct Geo {
+    static_assert(D == 64 || D == 128, "head dim");
+    static constexpr int kBoxes = D / 64;
+    static constexpr uint32_t kTileBytes = kBoxes * kBoxBytes;
+    static constexpr uint32_t kQOff = 0;  // two groups
+    static constexpr uint32_t kRingOff = 2 * kTileBytes;
+    static constexpr uint32_t kStageOff = kRingOff + kRingSlots * kTileBytes;  // 8 warps
+    static constexpr uint32_t kXchOff = kStageOff + 8 * kStageBytes;  // float4 [2][128]
+    static constexpr uint32_t kSeqOff = kXchOff + 2 * BM * 16;        // int2 [kSchedSeqs]
+    static constexpr uint32_t kItemOff = kSeqOff + kSchedSeqs * 8;
+    static constexpr uint32_t kBarOff = kItemOff + kItemSlots * 64;
+    static constexpr int kSmemBytes = 1024 + kBarOff + 512;
+    static_assert(kSmemBytes <= 232448, "more dynamic shared memory than one CTA may have");
+};
+__device__ __forceinline__ uint32_t col_s_of(int g) { return uint32_t(g) * 128u; }
+__device__ __forceinline__ uint32_t col_o_of(int g) { return 256u + uint32_t(g) * 128u; }
+
+enum Bar {
+    bQFull = 0,                            // Q of an item landed
+    bQEmpty,                               // the item's last S products completed
+    bSlotFull,                             // x kRingSlots
+    bSlotEmpty = bSlotFull + kRingSlots,   // x kRingSlots
+    bSFull = bSlotEmpty + kRingSlots,      // x2: S_g ready
+    bPFull = bSFull + 2,                   // x2: P_g ready (4 warps)
+    bODone = bPFull + 2,                   // x2: O_g final
+    bItemFull = bODone + 2,                // x kItemSlots
+    bItemEmpty = bItemFull + kItemSlots,   // x kItemSlots (kItemReaders)
+    bFixAsk = bItemEmpty + kItemSlots,     // x2: the repair warp may start on a tile
+    bFixDone = bFixAsk + 2,                // x2
+    bXch = bFixDone + 2,                   // kTreeAlt: m, l of both groups written (8 warps)
+    bXchDone,                              // kTreeAlt: both O read (8 warps)
+    bDrain,
+    kNumBars
+};
+static_assert(kNumBars * 8 + 8 <= 512, "barrier area");
+constexpr int kItemReaders = 3 + 8;  // TMA, MMA and repair warps, 8 softmax warps
+
+// ---- the scheduling warp
+
+struct Publisher {
+    uint8_t* items;
+    uint64_t* bars;
+    unsigned* status;
+    int count = 0;
+    __device__ bool put(const Item& w, int lane) {
+        const int s = count % kItemSlots;
+        if (count >= kItemSlots &&
+            !__all_sync(0xffffffffu,
+                        mbar_wait_bounded(smem_u32(&bars[bItemEmpty + s]),
+                                          ((count / kItemSlots) - 1) & 1, status)))
+            return false;
+        if (lane == 0) {
+            *reinterpret_cast<Item*>(items + s * sizeof(Item)) = w;
+            mbar_arrive(smem_u32(&bars[bItemFull + s]));
+        }
+        __syncwarp();
+        ++count;
+        return true;
+    }
+};
+
+// kPrompts. A block's cost is the number of keys it sees, so a sequence's
+// blocks are numbered by levels (key position of the block / block length) and
+// the launch runs the levels from the highest down over all sequences, in
+// snake order over the CTAs: heaviest first, found from the prefix sums by
+// counting, without sorting, so that every CTA finds its own items alone.
+// KV heads are taken in groups whose K and V fit in L2 together.
+__device__ __forceinline__ void schedule_prompts(const Params& p, int2* seqs, Publisher& pub,
+                                                 int lane) {
+    const int block = 2 * p.tok;
     bool bad = false;
-    for (; b < p.B; ++b) {
+    auto levels = [&](int b) {  // x: lowest level, y: blocks
+        int q0, T, k0, n;
         row_range(p.cu_q, p.B, p.total_q, b, q0, T, bad);
-        if (p.tree && T > p.max_tokens) {
-            T = p.max_tokens;
-            bad = true;
+        if (p.cu_k) row_range(p.cu_k, p.B, p.total_k, b, k0, n, bad);
+        else n = T;
+        return make_int2((p.causal ? max(n - T, 0) : n) / block, cdiv(T, block));
+    };
+    int top = 0, blocks = 0;
+    for (int b = lane; b < p.B; b += 32) {
+        const int2 s = levels(b);
+        if (b < kSchedSeqs) seqs[b] = s;
+        blocks += s.y;
+        if (s.y > 0) top = max(top, p.causal ? s.x + s.y - 1 : s.x);
+    }
+    if (bad && blockIdx.x == 0) atomicOr(p.status, kStatusBadSeqlen);
+    top = __reduce_max_sync(0xffffffffu, top);
+    blocks = __reduce_add_sync(0xffffffffu, blocks);
+    __syncwarp();
+    auto get = [&](int b) { return b < kSchedSeqs ? seqs[b] : levels(b); };
+    auto above = [&](int l) {  // blocks on levels > l
+        int c = 0;
+        for (int b = lane; b < p.B; b += 32) {
+            const int2 s = get(b);
+            c += p.causal ? clampi(s.x + s.y - 1 - l, 0, s.y) : (s.x > l ? s.y : 0);
         }
-        if (tok >= q0 && tok < q0 + T) break;
-    }
-    if (bad && lane == 0) atomicOr(p.status, kStatusBadSeqlen);
-    if (b == p.B) return;  // behind the last sequence
-    const int t = tok - q0;
-    int k0 = q0, n_own = T, ctx = 0;
-    if (p.cu_k) row_range(p.cu_k, p.B, p.total_k, b, k0, n_own, bad);
-    if (p.tree) ctx = context_of(p, b, bad);
-    if (bad && lane == 0) atomicOr(p.status, kStatusBadSeqlen);
-    const int lim = p.causal ? clampi(n_own - T + t + 1, 0, n_own) : n_own;
-    float qv[kPer], acc[kPer], m = -INFINITY, l = 0.f;
-    for (int i = 0; i < kPer; ++i) {
-        qv[i] = __uint_as_float(uint32_t(p.q[tok * p.q_st + h * p.q_sh + lane * kPer + i]) << 16);
-        acc[i] = 0.f;
-    }
-    for (int j = 0; j < ctx + n_own; ++j) {
-        const uint16_t *kr, *vr;
-        if (j < ctx) {
-            const size_t at = ((size_t(b) * p.H_kv + hk) * p.S_max + j) * D;
-            kr = p.kc + at;
-            vr = p.vc + at;
-        } else {
-            const int i = j - ctx;
-            const bool seen = p.mask ? (p.mask[size_t(tok) * p.mask_words + (i >> 5)] >> (i & 31)) & 1
-                                     : i < lim;
-            if (!seen) continue;
-            kr = p.k + (k0 + i) * p.k_st + hk * p.k_sh;
-            vr = p.v + (k0 + i) * p.v_st + hk * p.v_sh;
+        return __reduce_add_sync(0xffffffffu, c);
+    };
+    const int64_t total = int64_t(blocks) * p.H_kv;
+    const int ctas = gridDim.x;
+    int hint = top, hint_group = 0;
+    for (int it = 0;; ++it) {
+        const int64_t R = int64_t(it) * ctas + ((it & 1) ? ctas - 1 - int(blockIdx.x) : blockIdx.x);
+        if (R >= total) break;
+        const int64_t per_group = int64_t(blocks) * p.head_group;
+        const int hg = int(R / per_group), heads = min(p.head_group, p.H_kv - hg * p.head_group);
+        const int64_t in_group = R - hg * per_group;
+        const int rank = int(in_group / heads);
+        if (hg != hint_group) {
+            hint = top;
+            hint_group = hg;
         }
-        float s = 0.f;
-        for (int i = 0; i < kPer; ++i)
-            s += qv[i] * __uint_as_float(uint32_t(kr[lane * kPer + i]) << 16);
-        for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-        s *= p.scale_log2;
-        const float mn = fmaxf(m, s);
-        if (mn == -INFINITY) continue;
-        const float corr = exp2f(m - mn), e = exp2f(s - mn);
-        m = mn;
-        l = l * corr + e;
-        for (int i = 0; i < kPer; ++i)
-            acc[i] = acc[i] * corr + e * __uint_as_float(uint32_t(vr[lane * kPer + i]) << 16);
+        int lo = 0, hi = hint;  // the lowest level with at most `rank` blocks above it
+        while (lo < hi) {
+            const int mid = (lo + hi) >> 1;
+            if (above(mid) <= rank) hi = mid;
+            else lo = mid + 1;
+        }
+        hint = lo;
+        int k = rank - above(lo);  // the k-th block of this level
+        int b = 0, i = 0;
+        for (int b0 = 0; b0 < p.B; b0 += 32) {
+            int c = 0;
+            int2 s = make_int2(0, 0);
+            if (b0 + lane < p.B) {
+                s = get(b0 + lane);
+                c = p.causal ? (lo >= s.x && lo < s.x + s.y) : (s.x == lo ? s.y : 0);
+            }
+            int sum = c;
+            for (int o = 1; o < 32; o <<= 1) {
+                const int x = __shfl_up_sync(0xffffffffu, sum, o);
+                if (lane >= o) sum += x;
+            }
+            const unsigned hit = __ballot_sync(0xffffffffu, sum > k);
+            if (hit) {
+                const int src = __ffs(hit) - 1;
+                b = b0 + src;
+                i = __shfl_sync(0xffffffffu, p.causal ? lo - s.x : k - (sum - c), src);
+                break;
+            }
+            k -= __shfl_sync(0xffffffffu, sum, 31);
+        }
+        Item w{};
+        w.kvh = hg * p.head_group + int(in_group % heads);
+        w.b = b;
+        w.dst = -1;
+        row_range(p.cu_q, p.B, p.total_q, b, w.q_row, w.T, bad);
+        w.k_row = w.q_row;
+        w.n_own = w.T;
+        if (p.cu_k) row_range(p.cu_k, p.B, p.total_k, b, w.k_row, w.n_own, bad);
+        w.off = w.n_own - w.T;
+        w.tok0 = i * block;
+        w.n0 = cdiv(group_last<kPrompts>(p, w, 0), BN);
+        w.n1 = w.tok0 + p.tok < w.T ? cdiv(group_last<kPrompts>(p, w, 1), BN) : 0;
+        w.n = max(w.n0, w.n1);
+        if (!pub.put(w, lane)) return;
     }
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    for (int i = 0; i < kPer; ++i)
-        p.o[size_t(w) * D + lane * kPer + i] =
-            __bfloat16_as_ushort(__float2bfloat16_rn(acc[i] * inv));
-    if (lane == 0 && p.lse) p.lse[w] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+    Item end{};
+    end.n = -1;
+    pub.put(end, lane);
+}
+
+// decode_tree. The tiles of all rows and KV heads in one line, cut into equal
+// ranges, one per team of CTAs: however ragged the contexts are, every CTA
+// streams the same number of keys. The members of a team take the token blocks
+// of the same keys at the same time (K and V come from L2 for all but one). A
+// (row, head) that is cut leaves partial results for the merge.
+struct TreeSplit {
+    int total, per;  // tiles, tiles of a team
+};
+__device__ __forceinline__ TreeSplit tree_split(const Params& p, int lane, bool& bad) {
+    int t = 0;
+    for (int b = lane; b < p.B; b += 32) {
+        int q0, T, ctx;
+        tree_row(p, b, q0, T, ctx, bad);
+        t += tree_tiles(T, ctx) * p.H_kv;
+    }
+    TreeSplit s;
+    s.total = __reduce_add_sync(0xffffffffu, t);
+    s.per = max(p.min_tiles, cdiv(s.total, p.n_teams));
+    return s;
+}
+
+template <int kMode>
+__device__ __forceinline__ void schedule_tree(const Params& p, Publisher& pub, int lane) {
+    bool bad = false;
+    const TreeSplit sp = tree_split(p, lane, bad);
+    if (bad && blockIdx.x == 0) atomicOr(p.status, kStatusBadSeqlen);
+    const int team = blockIdx.x / p.team, member = blockIdx.x % p.team;
+    const int64_t begin = int64_t(team) * sp.per;
+    const int end = int(min(int64_t(sp.total), begin + sp.per));
+    int before = 0;  // tiles of the rows before b0
+    int x = int(min(begin, int64_t(end)));
+    for (int b0 = 0; b0 < p.B && x < end; b0 += 32) {
+        int q0 = 0, T = 0, ctx = 0, tiles = 0;
+        if (b0 + lane < p.B) {
+            tree_row(p, b0 + lane, q0, T, ctx, bad);
+            tiles = tree_tiles(T, ctx);
+        }
+        int sum = tiles * p.H_kv;  // inclusive prefix sum over the lanes
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, sum, o);
+            if (lane >= o) sum += y;
+        }
+        const int all = __shfl_sync(0xffffffffu, sum, 31);
+        while (x < end && x < before + all) {
+            const int src = __ffs(__ballot_sync(0xffffffffu, before + sum > x)) - 1;
+            const int row_tiles = __shfl_sync(0xffffffffu, tiles, src);
+            const int row_begin =
+                before + __shfl_sync(0xffffffffu, sum, src) - row_tiles * p.H_kv;
+            Item w{};
+            w.b = b0 + src;
+            w.kvh = (x - row_begin) / row_tiles;
+            w.j0 = (x - row_begin) % row_tiles;
+            w.n = min(row_tiles - w.j0, end - x);
+            w.q_row = w.k_row = __shfl_sync(0xffffffffu, q0, src);
+            w.T = w.n_own = __shfl_sync(0xffffffffu, T, src);
+            w.ctx = __shfl_sync(0xffffffffu, ctx, src);
+            w.c_t = row_tiles - 1;
+            w.tok0 = member * 2 * p.tok;
+            w.n0 = w.n;
+            w.n1 = w.tok0 + p.tok < w.T ? w.n : 0;
+            // slot 2c: the range begins inside the (row, head); 2c + 1: it ends inside
+            w.dst = w.n == row_tiles ? -1 : 2 * int(blockIdx.x) + (w.j0 == 0);
+            x += w.n;
+            if (w.tok0 < w.T && !pub.put(w, lane)) return;
+        }
+        before += all;
+    }
+    Item stop{};
+    stop.n = -1;
+    pub.put(stop, lane);
+}
+
+// ---- softmax of one tile of scores
+
+struct RowState {
+    float m, l, lb;  // running maximum (base 2), sums of p and of bf16(p)
+};
+
+// P = 2^(s - m) over the tile, written as bf16 pairs over S; returns the factor
+// that O has to be scaled by (1: left as it is).
+__device__ __forceinline__ float softmax_tile(const float (&sv)[BN], RowState& st,
+                                              float scale_log2, uint64_t c2, uint32_t s_addr) {
+    float mm[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) mm[i] = fmaxf(sv[i], sv[8 + i]);
+#pragma unroll
+    for (int c = 16; c < BN; c += 16)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) mm[i] = fmax3(mm[i], sv[c + i], sv[c + 8 + i]);
+    const float mx = fmax3(fmax3(mm[0], mm[1], mm[2]), fmax3(mm[3], mm[4], mm[5]),
+                           fmaxf(mm[6], mm[7]));
+    const float m_new = fmaxf(st.m, mx * scale_log2);
+    const bool need = m_new > st.m + kRescaleThreshold;
+    const float corr = need ? fast_exp2(st.m - m_new) : 1.f;
+    if (need) st.m = m_new;
+    // a row that has seen no key yet keeps m = -inf and p = 0
+    const float m_sub = st.m == -INFINITY ? 0.f : st.m;
+    const uint64_t n2 = f2pack(-m_sub, -m_sub);
+    uint64_t s2[4];
+    float bl[4], bh[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+        s2[u] = 0ull;
+        bl[u] = bh[u] = 0.f;
+    }
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+        uint32_t pk[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+            const int c = half * 64 + 2 * i;
+            float x0, x1;
+            f2unpack(ffma2(f2pack(sv[c], sv[c + 1]), c2, n2), x0, x1);
+            const float e0 = fast_exp2(x0), e1 = fast_exp2(x1);
+            s2[i & 3] = fadd2(s2[i & 3], f2pack(e0, e1));
+            pk[i] = pack_bf16x2(e0, e1);  // P in bf16: the operand type of the P V product
+            bl[i & 3] = add_f32_bf16_lo(bl[i & 3], pk[i]);
+            bh[i & 3] = add_f32_bf16_hi(bh[i & 3], pk[i]);
+        }
+        tc::tmem_st32(s_addr + half * 32, pk);
+    }
+    float t[8], tb[8];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+        f2unpack(s2[u], t[2 * u], t[2 * u + 1]);
+        tb[2 * u] = bl[u];
+        tb[2 * u + 1] = bh[u];
+    }
+    st.l = st.l * corr + (((t[0] + t[1]) + (t[2] + t[3])) + ((t[4] + t[5]) + (t[6] + t[7])));
+    st.lb = st.lb * corr +
+            (((tb[0] + tb[1]) + (tb[2] + tb[3])) + ((tb[4] + tb[5]) + (tb[6] + tb[7])));
+    return corr;
+}
+
+// ---- output: 64 bytes of each of a warp's 32 rows, through shared memory so
+// that four neighbouring lanes write one row's 64 bytes.
+struct RowPtrs {
+    uint8_t* p[4];  // rows lane / 4 + 8 * i of the warp (null: not written)
+    __device__ RowPtrs(uint8_t* own, int lane) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            p[i] = reinterpret_cast<uint8_t*>(
+                __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(own),
+                            i * 8 + (lane >> 2)));
+    }
+};
+__device__ __forceinline__ void store_rows(uint32_t stage, int lane, const uint4 (&v)[4],
+                                           const RowPtrs& rows, int byte) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        st_shared_v4(stage + lane * 64 + ((i ^ ((lane >> 1) & 3)) << 4), v[i]);
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = i * 8 + (lane >> 2);
+        const uint4 x = ld_shared_v4(stage + r * 64 + (((lane & 3) ^ ((r >> 1) & 3)) << 4));
+        if (rows.p[i]) *reinterpret_cast<uint4*>(rows.p[i] + byte + (lane & 3) * 16) = x;
+    }
+    __syncwarp();
+}
+
+template <int D, int kMode>
+__global__ void __launch_bounds__(kThreads, 1)
+    ragged_kernel(const __grid_constant__ CUtensorMap tmap_q,
+                  const __grid_constant__ CUtensorMap tmap_k,
+                  const __grid_constant__ CUtensorMap tmap_v,
+                  const __grid_constant__ CUtensorMap tmap_kc,
+                  const __grid_constant__ CUtensorMap tmap_vc, const Params p) {
+    using Gm = Geo<D>;
+    constexpr uint32_t kTileBytes = Gm::kTileBytes;
+    constexpr bool kTree = kMode != kPrompts, kAlt = kMode == kTreeAlt;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                               ~uintptr_t(1023));
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Gm::kBarOff);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + kNumBars);
+    // set once a repaired V tile held a value that is not finite; never cleared
+    volatile uint32_t* odd_values = tmem_slot + 1;
+    auto bar = [&](int i) { return smem_u32(&bars[i]); };
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 0) {
+        mbar_init(bar(bQFull), 1);
+        mbar_init(bar(bQEmpty), 1);
+        for (int s = 0; s < kRingSlots; ++s) {
+            mbar_init(bar(bSlotFull + s), 1);
+            mbar_init(bar(bSlotEmpty + s), 1);
+        }
+        for (int g = 0; g < 2; ++g) {
+            mbar_init(bar(bSFull + g), 1);
+            mbar_init(bar(bPFull + g), 4);
+            mbar_init(bar(bODone + g), 1);
+            mbar_init(bar(bFixAsk + g), 1);
+            mbar_init(bar(bFixDone + g), 1);
+        }
+        for (int s = 0; s < kItemSlots; ++s) {
+            mbar_init(bar(bItemFull + s), 1);
+            mbar_init(bar(bItemEmpty + s), kItemReaders);
+        }
+        mbar_init(bar(bXch), 8);
+        mbar_init(bar(bXchDone), 8);
+        mbar_init(bar(bDrain), 1);
+        *odd_values = 0;
+        fence_mbar_init();
+    }
+    if (warp == 1) {
+        tc::tmem_alloc(smem_u32(tmem_slot), kTmemCols);
+        tc::tmem_relinquish();
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    // Nothing above touches global memory: it overlaps the previous kernel.
+    grid_launch_dependents();
+    grid_wait_primary();
+    const uint32_t tmem = *tmem_slot;
+    const int wg = warp >> 2;
+
+    // Item number `it`, read by one lane or by a whole warp.
+    auto take = [&](int it, Item& w) {
+        const int s = it % kItemSlots;
+        if (!mbar_wait_bounded(bar(bItemFull + s), (it / kItemSlots) & 1, p.status)) return false;
+        w = *reinterpret_cast<const Item*>(smem + Gm::kItemOff + s * sizeof(Item));
+        return true;
+    };
+    auto release = [&](int it) { mbar_arrive(bar(bItemEmpty + it % kItemSlots)); };
+    auto ring_wait = [&](int r) {
+        return mbar_wait_bounded(bar(bSlotFull + r % kRingSlots), (r / kRingSlots) & 1, p.status);
+    };
+
+    if (wg == 0) {
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 104;" ::: "memory");
+      if (warp == 0) {
+        if (lane == 0) {
+        // ------------------------------------------------------ TMA producer
+        tma_prefetch_desc(&tmap_q);
+        tma_prefetch_desc(&tmap_k);
+        tma_prefetch_desc(&tmap_v);
+        if (kTree) {
+            tma_prefetch_desc(&tmap_kc);
+            tma_prefetch_desc(&tmap_vc);
+        }
+        Item w{};
+        bool alive = true, withheld = false;
+        int r = 0, q_loads = 0;
+        for (int it = 0; alive; ++it) {
+            alive = take(it, w);
+            if (!alive || w.n < 0) break;
+            release(it);
+            if (w.n == 0) continue;  // no key: nothing to load
+            if (q_loads > 0) alive = mbar_wait_bounded(bar(bQEmpty), (q_loads - 1) & 1, p.status);
+            if (!alive) break;
+            // Test hook: block 0 withholds its first Q copy, so every wait on
+            // it runs out and reports kStatusTimeout (nothing faults or hangs).
+            withheld = p.inject_timeout && blockIdx.x == 0 && q_loads == 0;
+            if (!withheld) {
+                const int groups = !kAlt && w.tok0 + p.tok < w.T ? 2 : 1;
+                mbar_arrive_expect_tx(bar(bQFull), groups * Gm::kBoxes * p.G * p.tok * 128);
+                for (int g = 0; g < groups; ++g)
+                    for (int hh = 0; hh < Gm::kBoxes; ++hh)
+                        tma_load(smem_u32(smem + Gm::kQOff + g * kTileBytes) + hh * kBoxBytes,
+                                 &tmap_q, hh * 64, w.kvh * p.G, w.q_row + w.tok0 + g * p.tok,
+                                 bar(bQFull));
+                ++q_loads;
+            }
+            for (int i = 0; i < 2 * w.n; ++i, ++r) {  // K_0, V_0, K_1, V_1, ...
+                const int s = r % kRingSlots;
+                if (r >= kRingSlots)
+                    alive = mbar_wait_bounded(bar(bSlotEmpty + s), ((r / kRingSlots) - 1) & 1,
+                                              p.status);
+                if (!alive) break;
+                const int jj = w.j0 + (i >> 1);
+                const uint32_t dst = smem_u32(smem + Gm::kRingOff + s * kTileBytes);
+                mbar_arrive_expect_tx(bar(bSlotFull + s), kTileBytes);
+                for (int hh = 0; hh < Gm::kBoxes; ++hh) {
+                    if (kTree && jj < w.c_t)
+                        tma_load(dst + hh * kBoxBytes, (i & 1) ? &tmap_vc : &tmap_kc, hh * 64,
+                                 jj * BN, w.b * p.H_kv + w.kvh, bar(bSlotFull + s));
+                    else
+                        tma_load(dst + hh * kBoxBytes, (i & 1) ? &tmap_v : &tmap_k, hh * 64,
+                                 w.kvh, w.k_row + (jj - w.c_t) * BN, bar(bSlotFull + s));
+                }
+            }
+            if (withheld) break;
+        }
+        // Every copy still in flight lands before the CTA exits.
+        if (q_loads > 0) mbar_wait_bounded(bar(bQFull), (q_loads - 1) & 1, p.status);
+        for (int i = max(0, r - kRingSlots); i < r; ++i) ring_wait(i);
+        }
+      } else if (warp == 1) {
+        if (lane == 0) {
+        // -------------------------------------------------------- MMA issuer
+        const uint32_t idesc_s = tc::idesc_bf16_f32(BM, BN, false);
+        const uint32_t idesc_pv = tc::idesc_bf16_f32(BM, D, true);
+        auto slot_addr = [&](int i) {
+            return smem_u32(smem + Gm::kRingOff + (i % kRingSlots) * kTileBytes);
+        };
+        const uint64_t qdesc0 = tc::sdesc_sw128(smem_u32(smem + Gm::kQOff), 16, 1024);
+        const uint64_t qdesc1 = tc::sdesc_sw128(smem_u32(smem + Gm::kQOff + kTileBytes), 16, 1024);
+        // S_g = Q K^T with K in ring item ri (kTreeAlt: both groups hold the same rows)
+        auto issue_s = [&](int g, int ri) {
+            const uint64_t qdesc = !kAlt && g ? qdesc1 : qdesc0;
+            const uint64_t kdesc = tc::sdesc_sw128(slot_addr(ri), 16, 1024);
+            const uint32_t qlo = uint32_t(qdesc), qhi = uint32_t(qdesc >> 32);
+            const uint32_t klo = uint32_t(kdesc), khi = uint32_t(kdesc >> 32);
+            const uint32_t dst = tmem + col_s_of(g);
+            tc::mma_ss_lo<0>(dst, qlo, qhi, klo, khi, idesc_s);
+#pragma unroll
+            for (int kk = 1; kk < D / 16; ++kk) {
+                const uint32_t o = ((kk >> 2) * kBoxBytes + (kk & 3) * 32) >> 4;
+                tc::mma_ss_lo<1>(dst, qlo + o, qhi, klo + o, khi, idesc_s);
+            }
+            tc::commit(bar(bSFull + g));
+        };
+        // O_g (+)= P_g V over the first `keys` keys, V in ring item ri
+        auto issue_pv = [&](int g, int ri, bool first, int keys) {
+            const uint64_t vdesc = tc::sdesc_sw128(slot_addr(ri), kBoxBytes, 1024);
+            const uint32_t vlo = uint32_t(vdesc), vhi = uint32_t(vdesc >> 32);
+            const uint32_t dst = tmem + col_o_of(g), src = tmem + col_s_of(g);
+            tc::mma_ts_lo(dst, src, vlo, vhi, idesc_pv, first ? 0u : 1u);
+            if (keys > BN - 16) {
+#pragma unroll
+                for (int ks = 1; ks < BN / 16; ++ks)
+                    tc::mma_ts_lo(dst, src + ks * 8, vlo + uint32_t((ks * 2048) >> 4), vhi,
+                                  idesc_pv, 1u);
+            } else {
+                for (int ks = 1; ks * 16 < keys; ++ks)
+                    tc::mma_ts_lo(dst, src + ks * 8, vlo + uint32_t((ks * 2048) >> 4), vhi,
+                                  idesc_pv, 1u);
+            }
+        };
+        Item w{};
+        bool alive = true;
+        int r = 0, qi = 0;   // ring items consumed, items with tiles
+        int t0 = 0, t1 = 0;  // tiles group 0 and 1 finished (their S and P phases)
+        int asked = 0, fixed = 0;
+        // The repair of V tile j starts when the previous tile's products are
+        // issued: only then has its ring slot's earlier use been seen here.
+        auto ask = [&](int j) {
+            if (repair_of<kMode>(p, w, w.j0 + j).needed()) mbar_arrive(bar(bFixAsk + (asked++ & 1)));
+        };
+        auto repaired = [&](int j) {
+            if (!repair_of<kMode>(p, w, w.j0 + j).needed()) return true;
+            const int f = fixed++;
+            return mbar_wait_bounded(bar(bFixDone + (f & 1)), (f >> 1) & 1, p.status);
+        };
+        for (int it = 0; alive; ++it) {
+            alive = take(it, w);
+            if (!alive || w.n < 0) break;
+            release(it);
+            const int n = w.n;
+            if (n == 0) continue;
+            ask(0);
+            alive = mbar_wait_bounded(bar(bQFull), qi & 1, p.status) && ring_wait(r);
+            if (!alive) break;
+            ++qi;
+            tc::fence_after_sync();
+            if constexpr (kAlt) {
+                issue_s(0, r);
+                tc::commit(bar(bSlotEmpty + r % kRingSlots));
+                if (n > 1) {
+                    alive = ring_wait(r + 2);
+                    if (!alive) break;
+                    tc::fence_after_sync();
+                    issue_s(1, r + 2);
+                    tc::commit(bar(bSlotEmpty + (r + 2) % kRingSlots));
+                }
+                if (n <= 2) tc::commit(bar(bQEmpty));
+                for (int j = 0; j < n && alive; ++j) {
+                    const int g = j & 1, rv = r + 2 * j + 1;
+                    if (j + 1 < n) ask(j + 1);
+                    alive = ring_wait(rv) && repaired(j) &&
+                            mbar_wait_bounded(bar(bPFull + g), (g ? t1 : t0) & 1, p.status);
+                    if (!alive) break;
+                    (g ? t1 : t0) += 1;
+                    tc::fence_after_sync();
+                    issue_pv(g, rv, j < 2, tile_keys<kMode>(p, w, w.j0 + j, 0));
+                    tc::commit(bar(bSlotEmpty + rv % kRingSlots));
+                    if (j + 2 < n) {
+                        alive = ring_wait(rv + 3);
+                        if (!alive) break;
+                        tc::fence_after_sync();
+                        issue_s(g, rv + 3);  // K_{j+2}
+                        tc::commit(bar(bSlotEmpty + (rv + 3) % kRingSlots));
+                        if (j + 3 == n) tc::commit(bar(bQEmpty));
+                    } else {
+                        tc::commit(bar(bODone + g));
+                    }
+                }
+            } else {
+                // The last group that reads K_t / V_t is group 1 while it has tiles.
+                auto last_user = [&](int t) { return t < w.n1 ? 1 : 0; };
+                if (w.n0 > 0) issue_s(0, r);
+                if (w.n1 > 0) issue_s(1, r);
+                tc::commit(bar(bSlotEmpty + r % kRingSlots));
+                if (n == 1) tc::commit(bar(bQEmpty));
+                for (int j = 0; j < n && alive; ++j) {
+                    const int rv = r + 2 * j + 1;  // V_j; K_{j+1} follows it
+                    if (j + 1 < n) ask(j + 1);
+                    alive = ring_wait(rv) && (j + 1 == n || ring_wait(rv + 1)) && repaired(j);
+#pragma unroll
+                    for (int g = 0; g < 2; ++g) {
+                        if (!alive) break;
+                        const int n_g = g ? w.n1 : w.n0;
+                        if (j >= n_g) continue;
+                        alive = mbar_wait_bounded(bar(bPFull + g), ((g ? t1 : t0) + j) & 1,
+                                                  p.status);
+                        if (!alive) break;
+                        tc::fence_after_sync();
+                        issue_pv(g, rv, j == 0, tile_keys<kMode>(p, w, w.j0 + j, g));
+                        if (g == last_user(j)) tc::commit(bar(bSlotEmpty + rv % kRingSlots));
+                        if (j + 1 < n_g) {
+                            issue_s(g, rv + 1);
+                            if (g == last_user(j + 1)) {
+                                tc::commit(bar(bSlotEmpty + (rv + 1) % kRingSlots));
+                                if (j + 2 == n) tc::commit(bar(bQEmpty));
+                            }
+                        } else {
+                            tc::commit(bar(bODone + g));
+                        }
+                    }
+                }
+                t0 += w.n0;
+                t1 += w.n1;
+            }
+            r += 2 * n;
+        }
+        // No product may still run when the tensor memory is freed.
+        tc::commit(bar(bDrain));
+        mbar_wait_bounded(bar(bDrain), 0, p.status);
+        }
+      } else if (warp == 2) {
+        // --------------------------------------------------------- scheduler
+        Publisher pub{smem + Gm::kItemOff, bars, p.status};
+        if constexpr (kTree)
+            schedule_tree<kMode>(p, pub, lane);
+        else
+            schedule_prompts(p, reinterpret_cast<int2*>(smem + Gm::kSeqOff), pub, lane);
+      } else {
+        // ------------------------------------------------------------ repair
+        // P is 0 at a key that a row does not see, but 0 * NaN is not: in the
+        // tiles that reach past the first row's last key, V rows that nobody
+        // sees are set to 0, and values that are not finite among the others
+        // are too; the rows that do see those add them in the epilogue.
+        Item w{};
+        bool alive = true;
+        int r = 0, f = 0;
+        for (int it = 0; alive; ++it) {
+            alive = __all_sync(0xffffffffu, take(it, w));
+            __syncwarp();
+            if (!alive || w.n < 0) break;
+            if (lane == 0) release(it);
+            for (int j = 0; j < w.n && alive; ++j) {
+                const Repair fix = repair_of<kMode>(p, w, w.j0 + j);
+                if (!fix.needed()) continue;
+                const int ri = r + 2 * j + 1;
+                alive = __all_sync(0xffffffffu,
+                                   mbar_wait_bounded(bar(bFixAsk + (f & 1)), (f >> 1) & 1,
+                                                     p.status)) &&
+                        __all_sync(0xffffffffu, ring_wait(ri));
+                if (!alive) break;
+                const uint32_t tile = smem_u32(smem + Gm::kRingOff + (ri % kRingSlots) * kTileBytes);
+                constexpr int kPieces = Gm::kBoxes * 8;  // 16-byte pieces of a row
+                bool odd = false;
+                for (int i = fix.seen * kPieces + lane; i < fix.end * kPieces; i += 32) {
+                    const int row = i / kPieces, piece = i % kPieces;
+                    const uint32_t at = tile + (piece >> 3) * kBoxBytes + row * 128 + (piece & 7) * 16;
+                    if (row >= fix.keys) {
+                        st_shared_v4(at, make_uint4(0, 0, 0, 0));
+                        continue;
+                    }
+                    uint4 x = ld_shared_v4(at);
+                    uint32_t* u = reinterpret_cast<uint32_t*>(&x);
+                    bool here = false;
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        if ((u[c] & 0x7f80u) == 0x7f80u) {
+                            u[c] &= 0xffff0000u;
+                            here = true;
+                        }
+                        if ((u[c] & 0x7f800000u) == 0x7f800000u) {
+                            u[c] &= 0xffffu;
+                            here = true;
+                        }
+                    }
+                    if (here) {
+                        st_shared_v4(at, x);
+                        odd = true;
+                    }
+                }
+                if (odd) *odd_values = 1;
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(bFixDone + (f & 1)));
+                ++f;
+            }
+            r += 2 * w.n;
+        }
+      }
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 200;" ::: "memory");
+        // ------------------------------------------------ softmax warpgroups
+        const int g = wg - 1;
+        const int quad = warp & 3;  // tensor-memory lanes 32 * quad .. + 31
+        const int row = quad * 32 + lane;
+        const int row_tok = row / p.G, row_head = row % p.G;
+        const uint32_t lane_base = tmem + (uint32_t(quad * 32) << 16);
+        const uint32_t col_s = col_s_of(g), col_o = col_o_of(g);
+        const uint32_t stage = smem_u32(smem + Gm::kStageOff + (g * 4 + quad) * kStageBytes);
+        float4* xch = reinterpret_cast<float4*>(smem + Gm::kXchOff);
+        const uint64_t c2 = f2pack(p.scale_log2, p.scale_log2);
+        Item w{};
+        bool alive = true;
+        int tt = 0;              // tiles this group finished: its S phases
+        int done0 = 0, done1 = 0;  // O_0, O_1 phases (kTreeAlt reads both, else its own)
+        int xk = 0;
+        auto wait_all = [&](int b, int phase) {
+            return bool(__all_sync(0xffffffffu, mbar_wait_bounded(bar(b), phase & 1, p.status)));
+        };
+        for (int it = 0; alive; ++it) {
+            alive = __all_sync(0xffffffffu, take(it, w));
+            __syncwarp();
+            if (!alive || w.n < 0) break;
+            if (lane == 0) release(it);
+            const int tok0 = kAlt ? w.tok0 : w.tok0 + g * p.tok;
+            const int count = min(p.tok, w.T - tok0);  // tokens of this group
+            if (count <= 0) continue;
+            const int t = tok0 + row_tok;
+            const bool valid = row_tok < count;
+            const bool act = quad * 32 < count * p.G;  // some row of this warp is valid
+            const int ng = kAlt ? (w.n + 1 - g) >> 1 : (g ? w.n1 : w.n0);
+            const size_t orow = (size_t(w.q_row) + t) * p.H_q + w.kvh * p.G + row_head;
+            if (kMode == kPrompts && ng == 0) {  // queries that see no key
+                if (valid) {
+                    uint4* dst = reinterpret_cast<uint4*>(p.o + orow * D);
+                    for (int i = 0; i < D / 8; ++i) dst[i] = make_uint4(0, 0, 0, 0);
+                    if (p.lse) p.lse[orow] = -INFINITY;
+                }
+                continue;
+            }
+            const int lim = kTree ? 0 : token_limit(p, w, t);
+            const int lim_first = group_first<kMode>(p, w, g);
+            uint32_t bits[4] = {0, 0, 0, 0};  // drafted tokens this row sees
+            const bool own = w.j0 + w.n > w.c_t;  // the item has the row's own tokens
+            if (kTree && own && valid) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int rest = w.T - 32 * i;  // tokens from this word on
+                    if (rest <= 0) break;
+                    const uint32_t live = rest >= 32 ? 0xffffffffu : (1u << rest) - 1u;
+                    const int upto = t + 1 - 32 * i;
+                    bits[i] = live & (p.mask ? p.mask[(size_t(w.q_row) + t) * p.mask_words + i]
+                                      : upto >= 32 ? 0xffffffffu
+                                      : upto <= 0  ? 0u
+                                                   : (1u << upto) - 1u);
+                }
+            }
+            RowState st{-INFINITY, 0.f, 0.f};
+            for (int i = 0; i < ng && alive; ++i) {
+                alive = wait_all(bSFull + g, tt + i);
+                if (!alive) break;
+                if (act) {
+                    tc::fence_after_sync();
+                    float sv[BN];
+#pragma unroll
+                    for (int c = 0; c < BN / 32; ++c) {
+                        uint32_t x[32];
+                        tc::tmem_ld32(lane_base + col_s + c * 32, x);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) sv[c * 32 + e] = __uint_as_float(x[e]);
+                    }
+                    tc::tmem_wait_ld();
+                    const int jj = w.j0 + (kAlt ? 2 * i + g : i);
+                    if (kTree) {
+                        if (jj >= w.c_t) {
+#pragma unroll
+                            for (int c = 0; c < BN; ++c)
+                                sv[c] = (bits[c >> 5] >> (c & 31)) & 1 ? sv[c] : -INFINITY;
+                        } else if (w.ctx - jj * BN < BN) {
+                            const int last = w.ctx - jj * BN;
+#pragma unroll
+                            for (int c = 0; c < BN; ++c) sv[c] = c < last ? sv[c] : -INFINITY;
+                        }
+                    } else if (lim_first - jj * BN < BN) {
+                        const int last = lim - jj * BN;
+#pragma unroll
+                        for (int c = 0; c < BN; ++c) sv[c] = c < last ? sv[c] : -INFINITY;
+                    }
+                    const float corr = softmax_tile(sv, st, p.scale_log2, c2, lane_base + col_s);
+                    // O is complete here: this tile's S product was issued after
+                    // the previous P V of the group, and they complete in order.
+                    if (i > 0 && __any_sync(0xffffffffu, corr != 1.f)) {
+                        const uint64_t corr2 = f2pack(corr, corr);
+#pragma unroll
+                        for (int c = 0; c < D / 32; ++c) {
+                            uint32_t x[32];
+                            tc::tmem_ld32(lane_base + col_o + c * 32, x);
+                            tc::tmem_wait_ld();
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) {
+                                float a0, a1;
+                                f2unpack(fmul2(f2pack(__uint_as_float(x[2 * e]),
+                                                      __uint_as_float(x[2 * e + 1])),
+                                               corr2),
+                                         a0, a1);
+                                x[2 * e] = __float_as_uint(a0);
+                                x[2 * e + 1] = __float_as_uint(a1);
+                            }
+                            tc::tmem_st32(lane_base + col_o + c * 32, x);
+                        }
+                    }
+                    tc::tmem_wait_st();
+                    tc::fence_before_sync();
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(bPFull + g));
+            }
+            if (!alive) break;
+            tt += ng;
+
+            // ---- epilogue. Every read of O completes before this warp's next
+            // P arrive, which is what lets the next item overwrite O.
+            float f0 = 1.f, f1 = 0.f;  // weights of O_0 and O_1 (kTreeAlt)
+            const bool two = kAlt && w.n > 1;
+            if constexpr (kAlt) {
+                xch[g * BM + row] = make_float4(st.m, st.l, st.lb, 0.f);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(bXch));
+                alive = wait_all(bODone, done0) && (!two || wait_all(bODone + 1, done1)) &&
+                        wait_all(bXch, xk);
+                if (!alive) break;
+                done0 += 1;
+                done1 += two;
+                const float4 a = xch[row], b = xch[BM + row];  // group 1 without tiles: -inf, 0, 0
+                const float m = fmaxf(a.x, b.x), ms = m == -INFINITY ? 0.f : m;
+                f0 = fast_exp2(a.x - ms);
+                f1 = fast_exp2(b.x - ms);
+                st.m = m;
+                st.l = f0 * a.y + f1 * b.y;
+                st.lb = f0 * a.z + f1 * b.z;
+            } else {
+                alive = wait_all(bODone + g, done0);
+                if (!alive) break;
+                done0 += 1;
+            }
+            if (act) {
+                tc::fence_after_sync();
+                const bool direct = !kTree || w.dst < 0;
+                const size_t prow = kTree ? size_t(w.dst) * p.part_rows + (t - w.tok0) * p.G + row_head
+                                          : 0;
+                uint8_t* own_row =
+                    !valid ? nullptr
+                    : direct ? reinterpret_cast<uint8_t*>(p.o + orow * D)
+                             : reinterpret_cast<uint8_t*>(p.part_o + prow * D);
+                const RowPtrs rows(own_row, lane);
+                // l is 0 only for a row that saw no key (and NaN stays NaN)
+                const float inv = st.lb == 0.f ? 0.f : 1.f / st.lb;
+                const bool odd = *odd_values != 0 && own;
+                const int c_begin = kAlt ? g * (D / 64) : 0;
+                const int c_end = kAlt ? (g + 1) * (D / 64) : D / 32;
+                for (int c = c_begin; c < c_end; ++c) {
+                    uint32_t x[32];
+                    tc::tmem_ld32(lane_base + (kAlt ? col_o_of(0) : col_o) + c * 32, x);
+                    if constexpr (kAlt) {
+                        if (two) {
+                            uint32_t y[32];
+                            tc::tmem_ld32(lane_base + col_o_of(1) + c * 32, y);
+                            tc::tmem_wait_ld();
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                x[e] = __float_as_uint(f0 * __uint_as_float(x[e]) +
+                                                       f1 * __uint_as_float(y[e]));
+                        }
+                    }
+                    tc::tmem_wait_ld();
+                    if (odd && valid) {
+                        // values that are not finite among the keys that not every
+                        // row sees: those that this row sees are added here
+                        const int k_end = kTree ? w.n_own : lim;
+                        for (int k = kTree ? 0 : group_first<kMode>(p, w, 0); k < k_end; ++k) {
+                            if (kTree) {
+                                const uint32_t word = k < 32 ? bits[0] : k < 64 ? bits[1]
+                                                    : k < 96 ? bits[2] : bits[3];
+                                if (!((word >> (k & 31)) & 1)) continue;
+                            }
+                            const uint16_t* vr = p.v + (int64_t(w.k_row) + k) * p.v_st +
+                                                 w.kvh * p.v_sh + c * 32;
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) {
+                                const uint32_t bf = vr[e];
+                                if ((bf & 0x7f80u) == 0x7f80u)
+                                    x[e] = __float_as_uint(__uint_as_float(x[e]) +
+                                                           __uint_as_float(bf << 16));
+                            }
+                        }
+                    }
+                    if (direct) {
+                        uint4 v[4];
+                        uint32_t* u = reinterpret_cast<uint32_t*>(v);
+#pragma unroll
+                        for (int e = 0; e < 16; ++e)
+                            u[e] = pack_bf16x2(__uint_as_float(x[2 * e]) * inv,
+                                               __uint_as_float(x[2 * e + 1]) * inv);
+                        store_rows(stage, lane, v, rows, c * 64);
+                    } else {
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            uint4 v[4];
+                            uint32_t* u = reinterpret_cast<uint32_t*>(v);
+#pragma unroll
+                            for (int e = 0; e < 16; ++e)
+                                u[e] = __float_as_uint(__uint_as_float(x[h * 16 + e]) * inv);
+                            store_rows(stage, lane, v, rows, c * 128 + h * 64);
+                        }
+                    }
+                }
+                if (valid && (!kAlt || g == 0)) {
+                    const float lse = st.l == 0.f ? -INFINITY : (st.m + log2f(st.l)) * kLn2;
+                    if (!direct)
+                        p.part_lse[prow] = lse;
+                    else if (p.lse)
+                        p.lse[orow] = lse;
+                }
+            }
+            if constexpr (kAlt) {
+                // both groups have read O_0, O_1 and xch
+                tc::fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(bXchDone));
+                alive = wait_all(bXchDone, xk);
+                ++xk;
+            }
+        }
+    }
+
+    tc::fence_before_sync();
+    __syncthreads();
+    if (warp == 1) {
+        tc::fence_after_sync();
+        tc::tmem_dealloc(tmem, kTmemCols);
+    }
+}
+
+// Folds the partial results of every (row, KV head, token block) that more
+// than one range of keys covers, in key order:
+//   lse = ln sum_i exp(lse_i),  O = sum_i exp(lse_i - lse) O_i.
+// One warp per query row; nothing to do for a block that one item covered.
+constexpr int kMergeWarps = 8;
+
+template <int D>
+__global__ void __launch_bounds__(kMergeWarps * 32) merge_kernel(const Params p) {
+    constexpr int kPer = D / 32;
+    grid_launch_dependents();
+    grid_wait_primary();
+    const int lane = threadIdx.x & 31;
+    const int chunks = cdiv(p.part_rows, kMergeWarps);
+    const int unit = blockIdx.x / chunks;  // (row, KV head, block), block innermost
+    const int r = (blockIdx.x % chunks) * kMergeWarps + (threadIdx.x >> 5);
+    const int member = unit % p.team, kvh = (unit / p.team) % p.H_kv, b = unit / p.team / p.H_kv;
+    bool bad = false;
+    int q0, T, ctx;
+    tree_row(p, b, q0, T, ctx, bad);
+    const int tok = member * 2 * p.tok + r / p.G;
+    if (r >= p.part_rows || tok >= T) return;
+    const TreeSplit sp = tree_split(p, lane, bad);
+    int before = 0;  // tiles of the rows before b
+    for (int i = lane; i < b; i += 32) {
+        int a, t, c;
+        tree_row(p, i, a, t, c, bad);
+        before += tree_tiles(t, c) * p.H_kv;
+    }
+    const int tiles = tree_tiles(T, ctx);
+    const int x0 = __reduce_add_sync(0xffffffffu, before) + kvh * tiles;
+    const int first = x0 / sp.per, last = (x0 + tiles - 1) / sp.per;  // teams
+    if (first == last) return;
+    // part i comes from team first + i: slot 2c + 1 of its first CTA, 2c of the others
+    auto slot = [&](int i) {
+        const int c = (first + i) * p.team + member;
+        return size_t(2 * c + (i == 0)) * p.part_rows + r;
+    };
+    const int parts = last - first + 1;
+    float mx = -INFINITY;
+    for (int i = lane; i < parts; i += 32) mx = fmaxf(mx, p.part_lse[slot(i)]);
+    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    const float ms = mx == -INFINITY ? 0.f : mx;
+    float acc[kPer], sum = 0.f;
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) acc[e] = 0.f;
+    for (int base = 0; base < parts; base += 32) {
+        const int cnt = min(32, parts - base);
+        const float wt = lane < cnt ? exp2f((p.part_lse[slot(base + lane)] - ms) * kLog2e) : 0.f;
+        sum += wt;
+#pragma unroll 4
+        for (int i = 0; i < cnt; ++i) {
+            const float wi = __shfl_sync(0xffffffffu, wt, i);
+            const float* src = p.part_o + slot(base + i) * D + lane * kPer;
+            float f[kPer];
+            if constexpr (kPer == 4)
+                *reinterpret_cast<float4*>(f) = *reinterpret_cast<const float4*>(src);
+            else
+                *reinterpret_cast<float2*>(f) = *reinterpret_cast<const float2*>(src);
+#pragma unroll
+            for (int e = 0; e < kPer; ++e) acc[e] += wi * f[e];
+        }
+    }
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    const size_t orow = (size_t(q0) + tok) * p.H_q + kvh * p.G + r % p.G;
+    uint32_t* out = reinterpret_cast<uint32_t*>(p.o + orow * D) + lane * (kPer / 2);
+#pragma unroll
+    for (int e = 0; e < kPer / 2; ++e) out[e] = pack_bf16x2(acc[2 * e] * inv, acc[2 * e + 1] * inv);
+    if (lane == 0 && p.lse) p.lse[orow] = sum == 0.f ? -INFINITY : ms + logf(sum);
+}
+
+// ------------------------------------------------------------------ host side
+
+template <typename... A>
+cudaError_t launch(void (*kern)(A...), unsigned grid, int threads, size_t smem,
+                   cudaStream_t stream, A... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    // The grid may start while the previous kernel of the stream finishes; it
+    // reads no global memory before griddepcontrol.wait.
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
+struct Maps {
+    CUtensorMap q, k, v, kc, vc;
+};
+
+template <int D, int kMode>
+int launch_ragged(const Maps& m, const Params& p, int ctas, cudaStream_t stream) {
+    auto kern = ragged_kernel<D, kMode>;
+    static std::atomic<uint64_t> attr_done{0};
+    const int dev = current_device();
+    if (device_attrs_pending(attr_done, dev)) {
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 Geo<D>::kSmemBytes) != cudaSuccess)
+            return GQA_ERR_CUDA;
+        device_attrs_mark(attr_done, dev);
+    }
+    return launch(kern, unsigned(ctas), kThreads, Geo<D>::kSmemBytes, stream, m.q, m.k, m.v, m.kc,
+                  m.vc, p) == cudaSuccess
+               ? GQA_OK
+               : GQA_ERR_CUDA;
+}
+
+// Tensor maps of the packed operands: Q in boxes of tok tokens x G heads, K
+// and V in boxes of 128 tokens of one head.
+bool packed_maps(Maps& m, const Params& p, const uint16_t* q, const uint16_t* k, const uint16_t* v,
+                 int d, int64_t q_st, int64_t q_sh, int64_t k_st, int64_t k_sh, int64_t v_st,
+                 int64_t v_sh) {
+    // a dimension of size 1 has no stride of its own
+    auto fix = [](int64_t s, int64_t n) { return n > 1 ? uint64_t(s) : uint64_t(8); };
+    if (encode_tmap_3d_bf16_strided(&m.q, q, d, p.H_q, p.total_q, fix(q_sh, p.H_q),
+                                    fix(q_st, p.total_q), p.G, p.tok) != cudaSuccess)
+        return false;
+    m.k = m.v = m.kc = m.vc = m.q;  // never read unless set
+    if (p.total_k == 0) return true;
+    return encode_tmap_3d_bf16_strided(&m.k, k, d, p.H_kv, p.total_k, fix(k_sh, p.H_kv),
+                                       fix(k_st, p.total_k), 1, BN) == cudaSuccess &&
+           encode_tmap_3d_bf16_strided(&m.v, v, d, p.H_kv, p.total_k, fix(v_sh, p.H_kv),
+                                       fix(v_st, p.total_k), 1, BN) == cudaSuccess;
+}
+
+// CTAs of a decode_tree launch work in teams of one per block of 2 * tok
+// drafted tokens.
+struct TreePlan {
+    int tok, team, part_rows;
+    bool alt;
+};
+TreePlan tree_plan(int G, int max_tokens) {
+    TreePlan t;
+    t.tok = BM / G;
+    t.alt = max_tokens <= t.tok;
+    t.team = t.alt ? 1 : (max_tokens + 2 * t.tok - 1) / (2 * t.tok);
+    t.part_rows = (max_tokens < 2 * t.tok ? max_tokens : 2 * t.tok) * G;
+    return t;
 }
 
 bool bad_strides(int64_t st, int64_t sh, int64_t tokens, int heads) {
@@ -145,16 +1244,6 @@ int check_common(const void* q, const void* k, const void* v, const void* o, con
         (reinterpret_cast<uintptr_t>(lse) & 3u))
         return GQA_ERR_MISALIGNED;
     return GQA_OK;
-}
-
-int launch_rows(const Params& p, int d, cudaStream_t stream) {
-    const int64_t warps = int64_t(p.total_q) * p.H_q;
-    const unsigned grid = unsigned((warps + 7) / 8);
-    if (d == 128)
-        rows_kernel<128><<<grid, 256, 0, stream>>>(p);
-    else
-        rows_kernel<64><<<grid, 256, 0, stream>>>(p);
-    return cudaGetLastError() == cudaSuccess ? GQA_OK : GQA_ERR_CUDA;
 }
 
 // ------------------------------------------------------------ cache append
@@ -227,24 +1316,41 @@ extern "C" int gqa_attn_prefill_packed(const uint16_t* q, const uint16_t* k, con
         (reinterpret_cast<uintptr_t>(cu_k) & 3u))
         return GQA_ERR_MISALIGNED;
     if (B == 0 || total_q == 0) return GQA_OK;
+    const int sms = num_sms();
     Params p{};
-    p.q = q; p.k = k; p.v = v; p.o = o; p.lse = lse;
+    p.v = v; p.o = o; p.lse = lse;
     p.cu_q = cu_q; p.cu_k = cu_k;
     p.status = status_word();
-    if (!p.status) return GQA_ERR_CUDA;
-    p.q_st = q_stride_t; p.q_sh = q_stride_h; p.k_st = k_stride_t; p.k_sh = k_stride_h;
+    if (!p.status || sms <= 0) return GQA_ERR_CUDA;
     p.v_st = v_stride_t; p.v_sh = v_stride_h;
     p.B = B; p.H_q = H_q; p.H_kv = H_kv; p.G = H_q / H_kv; p.total_q = total_q; p.total_k = total_k;
     p.causal = causal != 0;
+    p.tok = BM / p.G;
     p.scale_log2 = scale * kLog2e;
-    return launch_rows(p, d, stream);
+    p.inject_timeout = take_injected_timeout() ? 1 : 0;
+    // KV heads whose K and V together fit in the L2 budget run at the same time
+    const int64_t head_bytes = int64_t(total_k) * d * 4;
+    p.head_group = int(head_bytes * H_kv <= kPrefillL2Budget
+                           ? H_kv
+                           : kPrefillL2Budget / head_bytes > 1 ? kPrefillL2Budget / head_bytes : 1);
+    // at most this many blocks, however the tokens are spread over the rows
+    const int64_t blocks = int64_t(total_q) / (2 * p.tok) + (B < total_q ? B : total_q);
+    const int ctas = int(blocks * H_kv < sms ? blocks * H_kv : sms);
+    Maps m;
+    if (!packed_maps(m, p, q, k, v, d, q_stride_t, q_stride_h, k_stride_t, k_stride_h, v_stride_t,
+                     v_stride_h))
+        return GQA_ERR_CUDA;
+    return d == 128 ? launch_ragged<128, kPrompts>(m, p, ctas, stream)
+                    : launch_ragged<64, kPrompts>(m, p, ctas, stream);
 }
 
 extern "C" size_t gqa_attn_decode_tree_workspace_size(int H_q, int H_kv, int d, int max_tokens) {
     if (H_q <= 0 || H_kv <= 0 || H_q % H_kv || (d != 64 && d != 128) || max_tokens < 1 ||
         max_tokens > ragged::kMaxTreeTokens || H_q / H_kv > 16)
         return 0;
-    return 256;
+    const ragged::TreePlan t = ragged::tree_plan(H_q / H_kv, max_tokens);
+    // two slots per CTA: fp32 O and lse of part_rows rows
+    return size_t(2) * ragged::kTreeCtas * t.part_rows * (d + 1) * 4;
 }
 
 extern "C" int gqa_attn_decode_tree(
@@ -281,19 +1387,51 @@ extern "C" int gqa_attn_decode_tree(
         workspace_bytes < gqa_attn_decode_tree_workspace_size(H_q, H_kv, d, max_tokens)))
         return GQA_ERR_WORKSPACE;
     if (empty) return GQA_OK;
+    const int sms = num_sms();
+    const TreePlan plan = tree_plan(H_q / H_kv, max_tokens);
     Params p{};
-    p.q = q; p.k = k_new; p.v = v_new; p.kc = k_cache; p.vc = v_cache; p.o = o; p.lse = lse;
+    p.v = v_new; p.o = o; p.lse = lse;
     p.cu_q = cu_seqlens; p.ctx = context_lens;
     p.mask = reinterpret_cast<const uint32_t*>(tree_mask);
     p.status = status_word();
-    if (!p.status) return GQA_ERR_CUDA;
-    p.q_st = q_stride_t; p.q_sh = q_stride_h; p.k_st = k_stride_t; p.k_sh = k_stride_h;
+    if (!p.status || sms <= 0) return GQA_ERR_CUDA;
     p.v_st = v_stride_t; p.v_sh = v_stride_h;
     p.B = B; p.H_q = H_q; p.H_kv = H_kv; p.G = H_q / H_kv; p.total_q = total; p.total_k = total;
     p.S_max = S_max; p.max_tokens = max_tokens; p.mask_words = mask_words;
-    p.causal = 1; p.tree = 1;
+    p.causal = 1;
+    p.tok = plan.tok; p.team = plan.team; p.part_rows = plan.part_rows;
+    p.min_tiles = 1;
     p.scale_log2 = scale * kLog2e;
-    return launch_rows(p, d, stream);
+    p.inject_timeout = take_injected_timeout() ? 1 : 0;
+    // no more teams than tiles there can be
+    const int64_t tiles = int64_t(B) * H_kv * ((int64_t(S_max) + BN - 1) / BN + 1);
+    const int most = (sms < kTreeCtas ? sms : kTreeCtas) / plan.team;
+    p.n_teams = int(tiles < most ? tiles : most < 1 ? 1 : most);
+    const int ctas = p.n_teams * plan.team;
+    p.part_o = static_cast<float*>(workspace);
+    p.part_lse = p.part_o + size_t(2) * ctas * p.part_rows * d;
+    Maps m;
+    if (!packed_maps(m, p, q, k_new, v_new, d, q_stride_t, q_stride_h, k_stride_t, k_stride_h,
+                     v_stride_t, v_stride_h) ||
+        encode_tmap_3d_bf16(&m.kc, k_cache, d, S_max, uint64_t(B) * H_kv, 64, BN,
+                            CU_TENSOR_MAP_SWIZZLE_128B) != cudaSuccess ||
+        encode_tmap_3d_bf16(&m.vc, v_cache, d, S_max, uint64_t(B) * H_kv, 64, BN,
+                            CU_TENSOR_MAP_SWIZZLE_128B) != cudaSuccess)
+        return GQA_ERR_CUDA;
+    int rl;
+    if (d == 128)
+        rl = plan.alt ? launch_ragged<128, kTreeAlt>(m, p, ctas, stream)
+                      : launch_ragged<128, kTreePair>(m, p, ctas, stream);
+    else
+        rl = plan.alt ? launch_ragged<64, kTreeAlt>(m, p, ctas, stream)
+                      : launch_ragged<64, kTreePair>(m, p, ctas, stream);
+    if (rl != GQA_OK || p.n_teams == 1) return rl;
+    const unsigned grid =
+        unsigned(B) * H_kv * plan.team * ((p.part_rows + kMergeWarps - 1) / kMergeWarps);
+    return launch(d == 128 ? merge_kernel<128> : merge_kernel<64>, grid, kMergeWarps * 32, 0,
+                  stream, p) == cudaSuccess
+               ? GQA_OK
+               : GQA_ERR_CUDA;
 }
 
 extern "C" int gqa_attn_cache_append(uint16_t* k_cache, uint16_t* v_cache, const uint16_t* k_new,
