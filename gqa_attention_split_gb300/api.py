@@ -648,57 +648,79 @@ def gqa_attn_cache_append(k_cache, v_cache, k_new, v_new, cu_seqlens, starts, in
                                        v_stride_t, v_stride_h, stream)
 
 
-def _packed(name, t, heads=None, d=None):
-    """Checks a packed [tokens, heads, d] bf16 tensor; returns its token and head strides."""
-    import torch
+# The checks below run on every call of a serving step whose kernels take a few microseconds, so
+# they ask each tensor as little as they can (get_device is -1 for a CPU tensor).
 
+
+def _packed(torch, name, t, heads, d, device):
+    """Checks a packed [tokens, heads, d] bf16 tensor (heads, d or device None: any); returns its
+    token and head strides."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dtype != torch.bfloat16:
+    if t.dtype is not torch.bfloat16:
         raise TypeError(f"{name} must be bfloat16, got {t.dtype}")
-    if t.dim() != 3 or (heads is not None and t.shape[1] != heads) or (
-            d is not None and t.shape[2] != d):
+    shape = t.shape
+    if len(shape) != 3 or (heads is not None and shape[1] != heads) or (
+            d is not None and shape[2] != d):
         want = f"[tokens, {'heads' if heads is None else heads}, {'d' if d is None else d}]"
-        raise ValueError(f"{name} must be {want}, got {tuple(t.shape)}")
-    if t.stride(2) != 1:
+        raise ValueError(f"{name} must be {want}, got {tuple(shape)}")
+    if device is not None and t.get_device() != device:
+        raise ValueError(f"{name} must be on cuda:{device}, got {t.device}")
+    st, sh, sd = t.stride()
+    if sd != 1:
         raise ValueError(f"the last dimension of {name} must be contiguous")
     # the stride of a dimension of size 1 says nothing: any valid one will do
-    st = t.stride(0) if t.shape[0] > 1 else 8
-    sh = t.stride(1) if t.shape[1] > 1 else 8
-    return st, sh
+    return (st if shape[0] > 1 else 8), (sh if shape[1] > 1 else 8)
 
 
-def _ints(name, t, n, device):
-    import torch
-
-    if not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or not t.is_contiguous():
+def _ints(torch, name, t, n, device):
+    if not isinstance(t, torch.Tensor) or t.dtype is not torch.int32 or not t.is_contiguous():
         raise TypeError(f"{name} must be a contiguous int32 CUDA tensor")
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}")
+    if t.get_device() != device:
+        raise ValueError(f"{name} must be on cuda:{device}, got {t.device}")
     if t.numel() != n:
         raise ValueError(f"{name} must have {n} elements, got {t.numel()}")
+    return t.data_ptr()
 
 
-def _outputs(q, out, lse):
-    import torch
+def _cache(torch, k_cache, v_cache, H_kv, d, device):
+    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+        if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype is not torch.bfloat16:
+            raise TypeError(f"{name} must be a bfloat16 CUDA tensor")
+        if not t.is_contiguous() or t.get_device() != device:
+            raise ValueError(f"{name} must be contiguous and on cuda:{device}")
+    shape = k_cache.shape
+    if len(shape) != 4 or v_cache.shape != shape or shape[1] != H_kv or shape[3] != d:
+        raise ValueError(f"k_cache, v_cache must be [B, {H_kv}, S_max, {d}]")
+    return shape[0], shape[2]
 
+
+def _outputs(torch, q, out, lse):
     if out is None:
-        out = torch.empty(tuple(q.shape), dtype=torch.bfloat16, device=q.device)
-    elif (out.dtype != torch.bfloat16 or out.shape != q.shape or not out.is_contiguous()
-          or out.device != q.device):
+        out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+    elif (out.dtype is not torch.bfloat16 or out.shape != q.shape or not out.is_contiguous()
+          or out.get_device() != q.get_device()):
         raise ValueError("out must be a contiguous bfloat16 tensor shaped like q on its device")
     if lse is None:
-        lse = torch.empty(tuple(q.shape[:2]), dtype=torch.float32, device=q.device)
-    elif (lse.dtype != torch.float32 or lse.shape != q.shape[:2] or not lse.is_contiguous()
-          or lse.device != q.device):
+        lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
+    elif (lse.dtype is not torch.float32 or lse.shape != q.shape[:2] or not lse.is_contiguous()
+          or lse.get_device() != q.get_device()):
         raise ValueError("lse must be a contiguous float32 [tokens, H_q] tensor on q's device")
     return out, lse
 
 
-def _same_device(q, **others):
-    for name, t in others.items():
-        if t is not None and t.device != q.device:
-            raise ValueError(f"{name} must be on {q.device}, got {t.device}")
+def _on_device(torch, device, call):
+    """Runs call() with ``device`` current."""
+    if torch._C._cuda_getDevice() == device:
+        return call()
+    with torch.cuda.device(device):
+        return call()
+
+
+def _raw_stream(torch, device, stream):
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(device)
 
 
 def prefill_packed(q, k, v, cu_seqlens, cu_seqlens_k=None, *, causal: bool = True,
@@ -714,38 +736,32 @@ def prefill_packed(q, k, v, cu_seqlens, cu_seqlens_k=None, *, causal: bool = Tru
     """
     import torch
 
-    qs = _packed("q", q)
+    qs, qh = _packed(torch, "q", q, None, None, None)
     total_q, H_q, d = q.shape
-    ks = _packed("k", k, None, d)
-    vs = _packed("v", v, k.shape[1], d)
-    if v.shape != k.shape:
+    dev = q.get_device()
+    ks, kh = _packed(torch, "k", k, None, d, dev)
+    total_k, H_kv, _ = k.shape
+    vs, vh = _packed(torch, "v", v, H_kv, d, dev)
+    if v.shape[0] != total_k:
         raise ValueError("k and v must have the same shape")
-    _same_device(q, k=k, v=v)
     B = cu_seqlens.numel() - 1 if isinstance(cu_seqlens, torch.Tensor) else 0
     if B < 0:
         raise ValueError("cu_seqlens must have B + 1 elements")
-    _ints("cu_seqlens", cu_seqlens, B + 1, q.device)
+    cu_q = _ints(torch, "cu_seqlens", cu_seqlens, B + 1, dev)
+    cu_k = None
     if cu_seqlens_k is not None:
-        _ints("cu_seqlens_k", cu_seqlens_k, B + 1, q.device)
-    elif k.shape[0] != total_q:
+        cu_k = _ints(torch, "cu_seqlens_k", cu_seqlens_k, B + 1, dev)
+    elif total_k != total_q:
         raise ValueError("k and v must have q's tokens when cu_seqlens_k is not given")
+    out, lse = _outputs(torch, q, out, lse)
     sc = 1.0 / math.sqrt(d) if scale is None else float(scale)
-    with torch.cuda.device(q.device):
-        out, lse = _outputs(q, out, lse)
-        rc = gqa_attn_prefill_packed(_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse),
-                                     _ptr(cu_seqlens), _ptr(cu_seqlens_k), B, H_q, k.shape[1], d,
-                                     total_q, k.shape[0], *qs, *ks, *vs, 1 if causal else 0, sc,
-                                     _stream_ptr(stream))
+    rc = _on_device(torch, dev, lambda: lib().gqa_attn_prefill_packed(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(), cu_q, cu_k, B,
+        H_q, H_kv, d, total_q, total_k, qs, qh, ks, kh, vs, vh, 1 if causal else 0, sc,
+        _raw_stream(torch, dev, stream)))
     if rc != GQA_OK:
         raise GqaError(rc, "gqa_attn_prefill_packed")
     return out, lse
-
-
-def _check_cache(k_cache, v_cache, H_kv, d):
-    _check_cuda_bf16("k_cache", k_cache, 4)
-    _check_cuda_bf16("v_cache", v_cache, 4)
-    if v_cache.shape != k_cache.shape or k_cache.shape[1] != H_kv or k_cache.shape[3] != d:
-        raise ValueError("k_cache, v_cache must be [B, H_kv, S_max, d] matching k_new, v_new")
 
 
 def decode_tree(q, k_new, v_new, k_cache, v_cache, context_lens, *, cu_seqlens=None,
@@ -765,46 +781,48 @@ def decode_tree(q, k_new, v_new, k_cache, v_cache, context_lens, *, cu_seqlens=N
     """
     import torch
 
-    qs = _packed("q", q)
+    qs, qh = _packed(torch, "q", q, None, None, None)
     total, H_q, d = q.shape
-    ks = _packed("k_new", k_new, None, d)
-    vs = _packed("v_new", v_new, k_new.shape[1], d)
+    dev = q.get_device()
+    ks, kh = _packed(torch, "k_new", k_new, None, d, dev)
     H_kv = k_new.shape[1]
-    if v_new.shape != k_new.shape or k_new.shape[0] != total:
+    vs, vh = _packed(torch, "v_new", v_new, H_kv, d, dev)
+    if v_new.shape[0] != total or k_new.shape[0] != total:
         raise ValueError("k_new, v_new must be [total, H_kv, d] with q's tokens")
-    _check_cache(k_cache, v_cache, H_kv, d)
-    _same_device(q, k_new=k_new, v_new=v_new, k_cache=k_cache, v_cache=v_cache,
-                 tree_mask=tree_mask, workspace=workspace)
-    B, S_max = k_cache.shape[0], k_cache.shape[2]
-    _ints("context_lens", context_lens, B, q.device)
+    B, S_max = _cache(torch, k_cache, v_cache, H_kv, d, dev)
+    ctx = _ints(torch, "context_lens", context_lens, B, dev)
+    cu = None
     if cu_seqlens is not None:
-        _ints("cu_seqlens", cu_seqlens, B + 1, q.device)
+        cu = _ints(torch, "cu_seqlens", cu_seqlens, B + 1, dev)
         if max_tokens is None:
             raise ValueError("max_tokens is needed with cu_seqlens")
     else:
         if B == 0 or total % B:
             raise ValueError("without cu_seqlens every row has total / B drafted tokens")
         max_tokens = max(1, total // B) if max_tokens is None else max_tokens
-    words = 0
+    words, mask = 0, None
     if tree_mask is not None:
-        if (tree_mask.dtype != torch.int32 or tree_mask.dim() != 2 or tree_mask.shape[0] != total
-                or not tree_mask.is_contiguous()):
+        if tree_mask.dim() != 2 or tree_mask.shape[0] != total:
             raise ValueError("tree_mask must be a contiguous int32 [total, words] tensor")
         words = tree_mask.shape[1]
+        mask = _ints(torch, "tree_mask", tree_mask, total * words, dev)
+    out, lse = _outputs(torch, q, out, lse)
     sc = 1.0 / math.sqrt(d) if scale is None else float(scale)
-    with torch.cuda.device(q.device):
-        st = stream if stream is not None else torch.cuda.current_stream()
-        out, lse = _outputs(q, out, lse)
-        if workspace is None:
-            # from the launch stream's pool: its memory is reused only behind this call
-            n = gqa_attn_decode_tree_workspace_size(H_q, H_kv, d, max_tokens)
-            with torch.cuda.stream(st):
-                workspace = torch.empty(max(n, 256), dtype=torch.uint8, device=q.device)
-        rc = gqa_attn_decode_tree(_ptr(q), _ptr(k_new), _ptr(v_new), _ptr(k_cache), _ptr(v_cache),
-                                  _ptr(out), _ptr(lse), _ptr(cu_seqlens), _ptr(context_lens),
-                                  _ptr(tree_mask), words, B, H_q, H_kv, d, total, max_tokens,
-                                  S_max, *qs, *ks, *vs, sc, _ptr(workspace),
-                                  workspace.numel() * workspace.element_size(), st.cuda_stream)
+    if workspace is None:
+        # from the launch stream's pool: its memory is reused only behind this call
+        n = lib().gqa_attn_decode_tree_workspace_size(H_q, H_kv, d, max_tokens)
+        if stream is None:
+            workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
+        else:
+            with torch.cuda.stream(stream):
+                workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be contiguous and on cuda:{dev}")
+    rc = _on_device(torch, dev, lambda: lib().gqa_attn_decode_tree(
+        q.data_ptr(), k_new.data_ptr(), v_new.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+        out.data_ptr(), lse.data_ptr(), cu, ctx, mask, words, B, H_q, H_kv, d, total, max_tokens,
+        S_max, qs, qh, ks, kh, vs, vh, sc, workspace.data_ptr(),
+        workspace.numel() * workspace.element_size(), _raw_stream(torch, dev, stream)))
     if rc != GQA_OK:
         raise GqaError(rc, "gqa_attn_decode_tree")
     return out, lse
@@ -818,27 +836,25 @@ def cache_append(k_cache, v_cache, k_new, v_new, starts, *, cu_seqlens=None, ind
     index[e] (int32) when index is given, such as the accepted path of a drafted tree."""
     import torch
 
-    ks = _packed("k_new", k_new)
+    ks, kh = _packed(torch, "k_new", k_new, None, None, None)
     total_new, H_kv, d = k_new.shape
-    vs = _packed("v_new", v_new, H_kv, d)
-    if v_new.shape != k_new.shape:
+    dev = k_new.get_device()
+    vs, vh = _packed(torch, "v_new", v_new, H_kv, d, dev)
+    if v_new.shape[0] != total_new:
         raise ValueError("k_new and v_new must have the same shape")
-    _check_cache(k_cache, v_cache, H_kv, d)
-    _same_device(k_cache, v_cache=v_cache, k_new=k_new, v_new=v_new)
-    B, S_max = k_cache.shape[0], k_cache.shape[2]
-    _ints("starts", starts, B, k_cache.device)
-    total = total_new
+    B, S_max = _cache(torch, k_cache, v_cache, H_kv, d, dev)
+    first = _ints(torch, "starts", starts, B, dev)
+    total, idx, cu = total_new, None, None
     if index is not None:
         total = index.numel() if isinstance(index, torch.Tensor) else 0
-        _ints("index", index, total, k_cache.device)
+        idx = _ints(torch, "index", index, total, dev)
     if cu_seqlens is not None:
-        _ints("cu_seqlens", cu_seqlens, B + 1, k_cache.device)
+        cu = _ints(torch, "cu_seqlens", cu_seqlens, B + 1, dev)
     elif B == 0 or total % B:
         raise ValueError("without cu_seqlens every row has the same number of entries")
-    with torch.cuda.device(k_cache.device):
-        rc = gqa_attn_cache_append(_ptr(k_cache), _ptr(v_cache), _ptr(k_new), _ptr(v_new),
-                                   _ptr(cu_seqlens), _ptr(starts), _ptr(index), B, H_kv, d, S_max,
-                                   total, total_new, *ks, *vs, _stream_ptr(stream))
+    rc = _on_device(torch, dev, lambda: lib().gqa_attn_cache_append(
+        k_cache.data_ptr(), v_cache.data_ptr(), k_new.data_ptr(), v_new.data_ptr(), cu, first, idx,
+        B, H_kv, d, S_max, total, total_new, ks, kh, vs, vh, _raw_stream(torch, dev, stream)))
     if rc != GQA_OK:
         raise GqaError(rc, "gqa_attn_cache_append")
 
