@@ -27,6 +27,8 @@
 #include <cuda_runtime.h>
 #include <math.h>
 
+#include <type_traits>
+
 #include "gqa_attn.h"
 #include "plan.cuh"
 #include "ptx.cuh"
@@ -155,6 +157,18 @@ __device__ __forceinline__ int tile_keys(const Params& p, const Item& w, int jj,
     if (kMode != kPrompts && jj < w.c_t) return min(BN, w.ctx - jj * BN);
     return clampi(group_last<kMode>(p, w, g) - (jj - w.c_t) * BN, 0, BN);
 }
+// The same value in every lane, in a form that the compiler knows to be so:
+// loop bounds and ring positions derived from it stay in uniform registers,
+// where the descriptors of the matrix instructions have to be.
+__device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
+
+// Leading tiles of an item that every row of group g (and of the groups before
+// it) sees whole: no mask, no repair, all 128 keys.
+template <int kMode>
+__device__ __forceinline__ int plain_tiles(const Params& p, const Item& w, int g) {
+    const int whole = (kMode == kPrompts ? group_first<kMode>(p, w, g) : w.ctx) / BN;
+    return clampi(whole - w.j0, 0, w.n);
+}
 // The keys of V tile jj that the P V products read are [0, end). Those from
 // `seen` on are not visible to every row, those from `keys` on to none.
 struct Repair {
@@ -190,6 +204,19 @@ struct Geo {
     static constexpr int kSmemBytes = 1024 + kBarOff + 512;
     static_assert(kSmemBytes <= 232448, "more dynamic shared memory than one CTA may have");
 };
+// An item, read from its slot in shared memory each time it is written here:
+// the softmax warps keep few of its fields in registers over a tile loop.
+__device__ __forceinline__ Item read_item(uint32_t addr) {
+    Item w;
+    int4* q = reinterpret_cast<int4*>(&w);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        asm volatile("ld.shared.v4.s32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(q[i].x), "=r"(q[i].y), "=r"(q[i].z), "=r"(q[i].w)
+                     : "r"(addr + i * 16));
+    return w;
+}
+
 __device__ __forceinline__ uint32_t col_s_of(int g) { return uint32_t(g) * 128u; }
 __device__ __forceinline__ uint32_t col_o_of(int g) { return 256u + uint32_t(g) * 128u; }
 
@@ -255,6 +282,7 @@ __device__ __forceinline__ void schedule_prompts(const Params& p, int2* seqs, Pu
         return make_int2((p.causal ? max(n - T, 0) : n) / block, cdiv(T, block));
     };
     int top = 0, blocks = 0;
+#pragma unroll 1
     for (int b = lane; b < p.B; b += 32) {
         const int2 s = levels(b);
         if (b < kSchedSeqs) seqs[b] = s;
@@ -268,6 +296,7 @@ __device__ __forceinline__ void schedule_prompts(const Params& p, int2* seqs, Pu
     auto get = [&](int b) { return b < kSchedSeqs ? seqs[b] : levels(b); };
     auto above = [&](int l) {  // blocks on levels > l
         int c = 0;
+#pragma unroll 1
         for (int b = lane; b < p.B; b += 32) {
             const int2 s = get(b);
             c += p.causal ? clampi(s.x + s.y - 1 - l, 0, s.y) : (s.x > l ? s.y : 0);
@@ -297,6 +326,7 @@ __device__ __forceinline__ void schedule_prompts(const Params& p, int2* seqs, Pu
         hint = lo;
         int k = rank - above(lo);  // the k-th block of this level
         int b = 0, i = 0;
+#pragma unroll 1
         for (int b0 = 0; b0 < p.B; b0 += 32) {
             int c = 0;
             int2 s = make_int2(0, 0);
@@ -348,6 +378,7 @@ struct TreeSplit {
 };
 __device__ __forceinline__ TreeSplit tree_split(const Params& p, int lane, bool& bad) {
     int t = 0;
+#pragma unroll 1
     for (int b = lane; b < p.B; b += 32) {
         int q0, T, ctx;
         tree_row(p, b, q0, T, ctx, bad);
@@ -517,7 +548,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     // set once a repaired V tile held a value that is not finite; never cleared
     volatile uint32_t* odd_values = tmem_slot + 1;
     auto bar = [&](int i) { return smem_u32(&bars[i]); };
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // (through uniform(): with the roles chosen by a value that the compiler
+    // knows to be the same in a warp, addresses and descriptors are computed on
+    // the uniform path; causal 8K 861 -> 820 us)
+    const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
         mbar_init(bar(bQFull), 1);
@@ -553,82 +587,94 @@ __global__ void __launch_bounds__(kThreads, 1)
     // Nothing above touches global memory: it overlaps the previous kernel.
     grid_launch_dependents();
     grid_wait_primary();
-    const uint32_t tmem = *tmem_slot;
+    const uint32_t tmem = uniform(*tmem_slot);
     const int wg = warp >> 2;
 
-    // Item number `it`, read by one lane or by a whole warp.
-    auto take = [&](int it, Item& w) {
-        const int s = it % kItemSlots;
-        if (!mbar_wait_bounded(bar(bItemFull + s), (it / kItemSlots) & 1, p.status)) return false;
-        w = *reinterpret_cast<const Item*>(smem + Gm::kItemOff + s * sizeof(Item));
-        return true;
-    };
-    auto release = [&](int it) { mbar_arrive(bar(bItemEmpty + it % kItemSlots)); };
     auto ring_wait = [&](int r) {
         return mbar_wait_bounded(bar(bSlotFull + r % kRingSlots), (r / kRingSlots) & 1, p.status);
     };
 
     if (wg == 0) {
       asm volatile("setmaxnreg.dec.sync.aligned.u32 104;" ::: "memory");
+      // The item loops run on whole warps (see uniform()); lane 0 issues.
+      auto wait_item = [&](int it) {
+          return bool(__all_sync(0xffffffffu,
+                                 mbar_wait_bounded(bar(bItemFull + it % kItemSlots),
+                                                   (it / kItemSlots) & 1, p.status)));
+      };
+      auto item_at = [&](int it) {
+          const Item w = read_item(smem_u32(smem + Gm::kItemOff + (it % kItemSlots) * sizeof(Item)));
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(bItemEmpty + it % kItemSlots));
+          return w;
+      };
       if (warp == 0) {
-        if (lane == 0) {
         // ------------------------------------------------------ TMA producer
-        tma_prefetch_desc(&tmap_q);
-        tma_prefetch_desc(&tmap_k);
-        tma_prefetch_desc(&tmap_v);
-        if (kTree) {
-            tma_prefetch_desc(&tmap_kc);
-            tma_prefetch_desc(&tmap_vc);
+        if (lane == 0) {
+            tma_prefetch_desc(&tmap_q);
+            tma_prefetch_desc(&tmap_k);
+            tma_prefetch_desc(&tmap_v);
+            if (kTree) {
+                tma_prefetch_desc(&tmap_kc);
+                tma_prefetch_desc(&tmap_vc);
+            }
         }
-        Item w{};
-        bool alive = true, withheld = false;
-        int r = 0, q_loads = 0;
-        for (int it = 0; alive; ++it) {
-            alive = take(it, w);
-            if (!alive || w.n < 0) break;
-            release(it);
-            if (w.n == 0) continue;  // no key: nothing to load
-            if (q_loads > 0) alive = mbar_wait_bounded(bar(bQEmpty), (q_loads - 1) & 1, p.status);
-            if (!alive) break;
+        int r = 0, q_loads = 0;  // ring items and Q loads before this item
+        int issued = 0;          // ring items this lane issued
+        bool withheld = false;
+        for (int it = 0;; ++it) {
+            if (!wait_item(it)) break;
+            const Item w = item_at(it);
+            const int n = uniform(w.n);
+            if (n < 0) break;
+            if (n == 0) continue;  // no key: nothing to load
+            bool alive = true;
             // Test hook: block 0 withholds its first Q copy, so every wait on
             // it runs out and reports kStatusTimeout (nothing faults or hangs).
             withheld = p.inject_timeout && blockIdx.x == 0 && q_loads == 0;
-            if (!withheld) {
-                const int groups = !kAlt && w.tok0 + p.tok < w.T ? 2 : 1;
-                mbar_arrive_expect_tx(bar(bQFull), groups * Gm::kBoxes * p.G * p.tok * 128);
-                for (int g = 0; g < groups; ++g)
-                    for (int hh = 0; hh < Gm::kBoxes; ++hh)
-                        tma_load(smem_u32(smem + Gm::kQOff + g * kTileBytes) + hh * kBoxBytes,
-                                 &tmap_q, hh * 64, w.kvh * p.G, w.q_row + w.tok0 + g * p.tok,
-                                 bar(bQFull));
-                ++q_loads;
-            }
-            for (int i = 0; i < 2 * w.n; ++i, ++r) {  // K_0, V_0, K_1, V_1, ...
-                const int s = r % kRingSlots;
-                if (r >= kRingSlots)
-                    alive = mbar_wait_bounded(bar(bSlotEmpty + s), ((r / kRingSlots) - 1) & 1,
-                                              p.status);
-                if (!alive) break;
-                const int jj = w.j0 + (i >> 1);
-                const uint32_t dst = smem_u32(smem + Gm::kRingOff + s * kTileBytes);
-                mbar_arrive_expect_tx(bar(bSlotFull + s), kTileBytes);
-                for (int hh = 0; hh < Gm::kBoxes; ++hh) {
-                    if (kTree && jj < w.c_t)
-                        tma_load(dst + hh * kBoxBytes, (i & 1) ? &tmap_vc : &tmap_kc, hh * 64,
-                                 jj * BN, w.b * p.H_kv + w.kvh, bar(bSlotFull + s));
-                    else
-                        tma_load(dst + hh * kBoxBytes, (i & 1) ? &tmap_v : &tmap_k, hh * 64,
-                                 w.kvh, w.k_row + (jj - w.c_t) * BN, bar(bSlotFull + s));
+            if (lane == 0) {
+                if (q_loads > 0)
+                    alive = mbar_wait_bounded(bar(bQEmpty), (q_loads - 1) & 1, p.status);
+                if (alive && !withheld) {
+                    const int groups = !kAlt && w.tok0 + p.tok < w.T ? 2 : 1;
+                    mbar_arrive_expect_tx(bar(bQFull), groups * Gm::kBoxes * p.G * p.tok * 128);
+                    for (int g = 0; g < groups; ++g)
+                        for (int hh = 0; hh < Gm::kBoxes; ++hh)
+                            tma_load(smem_u32(smem + Gm::kQOff + g * kTileBytes) + hh * kBoxBytes,
+                                     &tmap_q, hh * 64, w.kvh * p.G, w.q_row + w.tok0 + g * p.tok,
+                                     bar(bQFull));
+                }
+#pragma unroll 1
+                for (int i = 0; i < 2 * n && alive; ++i) {  // K_0, V_0, K_1, V_1, ...
+                    const int ri = r + i, s = ri % kRingSlots;
+                    if (ri >= kRingSlots)
+                        alive = mbar_wait_bounded(bar(bSlotEmpty + s), ((ri / kRingSlots) - 1) & 1,
+                                                  p.status);
+                    if (!alive) break;
+                    const int jj = w.j0 + (i >> 1);
+                    const uint32_t dst = smem_u32(smem + Gm::kRingOff + s * kTileBytes);
+                    mbar_arrive_expect_tx(bar(bSlotFull + s), kTileBytes);
+                    for (int hh = 0; hh < Gm::kBoxes; ++hh) {
+                        if (kTree && jj < w.c_t)
+                            tma_load(dst + hh * kBoxBytes, (i & 1) ? &tmap_vc : &tmap_kc, hh * 64,
+                                     jj * BN, w.b * p.H_kv + w.kvh, bar(bSlotFull + s));
+                        else
+                            tma_load(dst + hh * kBoxBytes, (i & 1) ? &tmap_v : &tmap_k, hh * 64,
+                                     w.k_row + (jj - w.c_t) * BN, w.kvh, bar(bSlotFull + s));
+                    }
+                    issued = ri + 1;
                 }
             }
-            if (withheld) break;
+            if (!withheld) ++q_loads;
+            if (!__all_sync(0xffffffffu, alive) || withheld) break;
+            r += 2 * n;
         }
         // Every copy still in flight lands before the CTA exits.
-        if (q_loads > 0) mbar_wait_bounded(bar(bQFull), (q_loads - 1) & 1, p.status);
-        for (int i = max(0, r - kRingSlots); i < r; ++i) ring_wait(i);
+        if (lane == 0) {
+            if (q_loads > 0) mbar_wait_bounded(bar(bQFull), (q_loads - 1) & 1, p.status);
+            for (int i = max(0, issued - kRingSlots); i < issued; ++i) ring_wait(i);
         }
       } else if (warp == 1) {
-        if (lane == 0) {
         // -------------------------------------------------------- MMA issuer
         const uint32_t idesc_s = tc::idesc_bf16_f32(BM, BN, false);
         const uint32_t idesc_pv = tc::idesc_bf16_f32(BM, D, true);
@@ -653,73 +699,82 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc::commit(bar(bSFull + g));
         };
         // O_g (+)= P_g V over the first `keys` keys, V in ring item ri
-        auto issue_pv = [&](int g, int ri, bool first, int keys) {
+        auto issue_pv = [&](int g, int ri, bool first, auto keys) {
             const uint64_t vdesc = tc::sdesc_sw128(slot_addr(ri), kBoxBytes, 1024);
             const uint32_t vlo = uint32_t(vdesc), vhi = uint32_t(vdesc >> 32);
             const uint32_t dst = tmem + col_o_of(g), src = tmem + col_s_of(g);
             tc::mma_ts_lo(dst, src, vlo, vhi, idesc_pv, first ? 0u : 1u);
-            if (keys > BN - 16) {
 #pragma unroll
-                for (int ks = 1; ks < BN / 16; ++ks)
+            for (int ks = 1; ks < BN / 16; ++ks)
+                if (ks * 16 < keys)
                     tc::mma_ts_lo(dst, src + ks * 8, vlo + uint32_t((ks * 2048) >> 4), vhi,
                                   idesc_pv, 1u);
-            } else {
-                for (int ks = 1; ks * 16 < keys; ++ks)
-                    tc::mma_ts_lo(dst, src + ks * 8, vlo + uint32_t((ks * 2048) >> 4), vhi,
-                                  idesc_pv, 1u);
-            }
         };
-        Item w{};
-        bool alive = true;
-        int r = 0, qi = 0;   // ring items consumed, items with tiles
-        int t0 = 0, t1 = 0;  // tiles group 0 and 1 finished (their S and P phases)
+        constexpr std::integral_constant<int, BN> kAllKeys{};
+        int r = 0, qi = 0;   // ring items and items with tiles before this item
+        int t0 = 0, t1 = 0;  // tiles of group 0 and 1 before this item (their S and P phases)
         int asked = 0, fixed = 0;
-        // The repair of V tile j starts when the previous tile's products are
-        // issued: only then has its ring slot's earlier use been seen here.
-        auto ask = [&](int j) {
-            if (repair_of<kMode>(p, w, w.j0 + j).needed()) mbar_arrive(bar(bFixAsk + (asked++ & 1)));
-        };
-        auto repaired = [&](int j) {
-            if (!repair_of<kMode>(p, w, w.j0 + j).needed()) return true;
-            const int f = fixed++;
-            return mbar_wait_bounded(bar(bFixDone + (f & 1)), (f >> 1) & 1, p.status);
-        };
-        for (int it = 0; alive; ++it) {
-            alive = take(it, w);
-            if (!alive || w.n < 0) break;
-            release(it);
-            const int n = w.n;
+        for (int it = 0;; ++it) {
+            if (!wait_item(it)) break;
+            const Item w = item_at(it);
+            const int n = uniform(w.n);
+            if (n < 0) break;
             if (n == 0) continue;
-            ask(0);
-            alive = mbar_wait_bounded(bar(bQFull), qi & 1, p.status) && ring_wait(r);
-            if (!alive) break;
-            ++qi;
-            tc::fence_after_sync();
-            if constexpr (kAlt) {
+            const int n0 = kAlt ? (n + 1) >> 1 : uniform(w.n0), n1 = kAlt ? n >> 1 : uniform(w.n1);
+            // tiles before `plain` need no repair and count with all their keys;
+            // the last tile of a group (kPrompts), the context's last and the
+            // drafted tokens' tile (decode_tree) may count with fewer
+            const int plain = uniform(plain_tiles<kMode>(p, w, 0));
+            const int j_own = uniform(w.c_t - w.j0);
+            const int k0 = uniform(kMode == kPrompts ? tile_keys<kMode>(p, w, n0 - 1, 0) : w.n_own);
+            const int k1 = uniform(kMode == kPrompts ? tile_keys<kMode>(p, w, n1 - 1, 1)
+                                                     : w.ctx - (w.c_t - 1) * BN);
+            auto keys_of = [&](int j, int g) {
+                if (kMode == kPrompts) return j + 1 < (g ? n1 : n0) ? BN : (g ? k1 : k0);
+                return j < plain ? BN : (j < j_own ? k1 : k0);
+            };
+            // The repair of V tile j starts when the previous tile's products
+            // are issued: only then has its ring slot's earlier use been seen here.
+            auto ask = [&](int j) {
+                if (j >= plain && repair_of<kMode>(p, w, w.j0 + j).needed())
+                    mbar_arrive(bar(bFixAsk + (asked++ & 1)));
+            };
+            auto repaired = [&](int j) {
+                if (j < plain || !repair_of<kMode>(p, w, w.j0 + j).needed()) return true;
+                const int f = fixed++;
+                return mbar_wait_bounded(bar(bFixDone + (f & 1)), (f >> 1) & 1, p.status);
+            };
+            bool alive = true;
+            if (lane == 0) {
+                ask(0);
+                alive = mbar_wait_bounded(bar(bQFull), qi & 1, p.status) && ring_wait(r);
+            }
+            if (lane == 0 && alive) {
+              tc::fence_after_sync();
+              if constexpr (kAlt) {
                 issue_s(0, r);
                 tc::commit(bar(bSlotEmpty + r % kRingSlots));
                 if (n > 1) {
                     alive = ring_wait(r + 2);
-                    if (!alive) break;
-                    tc::fence_after_sync();
-                    issue_s(1, r + 2);
-                    tc::commit(bar(bSlotEmpty + (r + 2) % kRingSlots));
+                    if (alive) {
+                        tc::fence_after_sync();
+                        issue_s(1, r + 2);
+                        tc::commit(bar(bSlotEmpty + (r + 2) % kRingSlots));
+                    }
                 }
                 if (n <= 2) tc::commit(bar(bQEmpty));
+#pragma unroll 1
                 for (int j = 0; j < n && alive; ++j) {
                     const int g = j & 1, rv = r + 2 * j + 1;
                     if (j + 1 < n) ask(j + 1);
-                    alive = ring_wait(rv) && repaired(j) &&
-                            mbar_wait_bounded(bar(bPFull + g), (g ? t1 : t0) & 1, p.status);
+                    alive = ring_wait(rv) && (j + 2 >= n || ring_wait(rv + 3)) && repaired(j) &&
+                            mbar_wait_bounded(bar(bPFull + g), ((g ? t1 : t0) + (j >> 1)) & 1,
+                                              p.status);
                     if (!alive) break;
-                    (g ? t1 : t0) += 1;
                     tc::fence_after_sync();
-                    issue_pv(g, rv, j < 2, tile_keys<kMode>(p, w, w.j0 + j, 0));
+                    issue_pv(g, rv, j < 2, keys_of(j, 0));
                     tc::commit(bar(bSlotEmpty + rv % kRingSlots));
                     if (j + 2 < n) {
-                        alive = ring_wait(rv + 3);
-                        if (!alive) break;
-                        tc::fence_after_sync();
                         issue_s(g, rv + 3);  // K_{j+2}
                         tc::commit(bar(bSlotEmpty + (rv + 3) % kRingSlots));
                         if (j + 3 == n) tc::commit(bar(bQEmpty));
@@ -727,27 +782,51 @@ __global__ void __launch_bounds__(kThreads, 1)
                         tc::commit(bar(bODone + g));
                     }
                 }
-            } else {
+              } else {
                 // The last group that reads K_t / V_t is group 1 while it has tiles.
-                auto last_user = [&](int t) { return t < w.n1 ? 1 : 0; };
-                if (w.n0 > 0) issue_s(0, r);
-                if (w.n1 > 0) issue_s(1, r);
+                auto last_user = [&](int t) { return t < n1 ? 1 : 0; };
+                if (n0 > 0) issue_s(0, r);
+                if (n1 > 0) issue_s(1, r);
                 tc::commit(bar(bSlotEmpty + r % kRingSlots));
                 if (n == 1) tc::commit(bar(bQEmpty));
-                for (int j = 0; j < n && alive; ++j) {
+                // Tiles that both groups run whole and that are not a group's last:
+                // no conditions between the issues, which are on the critical path.
+                const int fast = min(plain, min(n0, n1) - 1);
+                int j = 0;
+#pragma unroll 1
+                for (; j < fast && alive; ++j) {
                     const int rv = r + 2 * j + 1;  // V_j; K_{j+1} follows it
+                    alive = ring_wait(rv) && ring_wait(rv + 1);
+                    if (alive) alive = mbar_wait_bounded(bar(bPFull), (t0 + j) & 1, p.status);
+                    if (!alive) break;
+                    tc::fence_after_sync();
+                    issue_pv(0, rv, j == 0, kAllKeys);
+                    issue_s(0, rv + 1);
+                    alive = mbar_wait_bounded(bar(bPFull + 1), (t1 + j) & 1, p.status);
+                    if (!alive) break;
+                    tc::fence_after_sync();
+                    issue_pv(1, rv, j == 0, kAllKeys);
+                    tc::commit(bar(bSlotEmpty + rv % kRingSlots));
+                    issue_s(1, rv + 1);
+                    tc::commit(bar(bSlotEmpty + (rv + 1) % kRingSlots));
+                    if (j + 2 == n) tc::commit(bar(bQEmpty));
+                }
+                if (j > 0 && j < n && alive) ask(j);
+#pragma unroll 1
+                for (; j < n && alive; ++j) {
+                    const int rv = r + 2 * j + 1;
                     if (j + 1 < n) ask(j + 1);
                     alive = ring_wait(rv) && (j + 1 == n || ring_wait(rv + 1)) && repaired(j);
 #pragma unroll
                     for (int g = 0; g < 2; ++g) {
                         if (!alive) break;
-                        const int n_g = g ? w.n1 : w.n0;
+                        const int n_g = g ? n1 : n0;
                         if (j >= n_g) continue;
                         alive = mbar_wait_bounded(bar(bPFull + g), ((g ? t1 : t0) + j) & 1,
                                                   p.status);
                         if (!alive) break;
                         tc::fence_after_sync();
-                        issue_pv(g, rv, j == 0, tile_keys<kMode>(p, w, w.j0 + j, g));
+                        issue_pv(g, rv, j == 0, keys_of(j, g));
                         if (g == last_user(j)) tc::commit(bar(bSlotEmpty + rv % kRingSlots));
                         if (j + 1 < n_g) {
                             issue_s(g, rv + 1);
@@ -760,14 +839,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     }
                 }
-                t0 += w.n0;
-                t1 += w.n1;
+              }
             }
+            if (!__all_sync(0xffffffffu, alive)) break;
+            ++qi;
+            t0 += n0;
+            t1 += n1;
             r += 2 * n;
         }
         // No product may still run when the tensor memory is freed.
-        tc::commit(bar(bDrain));
-        mbar_wait_bounded(bar(bDrain), 0, p.status);
+        if (lane == 0) {
+            tc::commit(bar(bDrain));
+            mbar_wait_bounded(bar(bDrain), 0, p.status);
         }
       } else if (warp == 2) {
         // --------------------------------------------------------- scheduler
@@ -782,15 +865,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         // tiles that reach past the first row's last key, V rows that nobody
         // sees are set to 0, and values that are not finite among the others
         // are too; the rows that do see those add them in the epilogue.
-        Item w{};
         bool alive = true;
         int r = 0, f = 0;
         for (int it = 0; alive; ++it) {
-            alive = __all_sync(0xffffffffu, take(it, w));
-            __syncwarp();
-            if (!alive || w.n < 0) break;
-            if (lane == 0) release(it);
-            for (int j = 0; j < w.n && alive; ++j) {
+            if (!wait_item(it)) break;
+            const Item w = item_at(it);
+            if (w.n < 0) break;
+            for (int j = plain_tiles<kMode>(p, w, 0); j < w.n && alive; ++j) {
                 const Repair fix = repair_of<kMode>(p, w, w.j0 + j);
                 if (!fix.needed()) continue;
                 const int ri = r + 2 * j + 1;
@@ -802,6 +883,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint32_t tile = smem_u32(smem + Gm::kRingOff + (ri % kRingSlots) * kTileBytes);
                 constexpr int kPieces = Gm::kBoxes * 8;  // 16-byte pieces of a row
                 bool odd = false;
+#pragma unroll 1
                 for (int i = fix.seen * kPieces + lane; i < fix.end * kPieces; i += 32) {
                     const int row = i / kPieces, piece = i % kPieces;
                     const uint32_t at = tile + (piece >> 3) * kBoxBytes + row * 128 + (piece & 7) * 16;
@@ -849,7 +931,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t stage = smem_u32(smem + Gm::kStageOff + (g * 4 + quad) * kStageBytes);
         float4* xch = reinterpret_cast<float4*>(smem + Gm::kXchOff);
         const uint64_t c2 = f2pack(p.scale_log2, p.scale_log2);
-        Item w{};
         bool alive = true;
         int tt = 0;              // tiles this group finished: its S phases
         int done0 = 0, done1 = 0;  // O_0, O_1 phases (kTreeAlt reads both, else its own)
@@ -857,32 +938,47 @@ __global__ void __launch_bounds__(kThreads, 1)
         auto wait_all = [&](int b, int phase) {
             return bool(__all_sync(0xffffffffu, mbar_wait_bounded(bar(b), phase & 1, p.status)));
         };
-        for (int it = 0; alive; ++it) {
-            alive = __all_sync(0xffffffffu, take(it, w));
-            __syncwarp();
-            if (!alive || w.n < 0) break;
-            if (lane == 0) release(it);
+        for (int it = 0;; ++it) {
+            // the warp gives the item's slot back when it is done with the item
+            auto done_with_item = [&] {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(bItemEmpty + it % kItemSlots));
+            };
+            alive = wait_all(bItemFull + it % kItemSlots, it / kItemSlots);
+            if (!alive) break;
+            const uint32_t item_addr =
+                smem_u32(smem + Gm::kItemOff + (it % kItemSlots) * sizeof(Item));
+            const Item w = read_item(item_addr);
+            if (uniform(w.n) < 0) break;
             const int tok0 = kAlt ? w.tok0 : w.tok0 + g * p.tok;
-            const int count = min(p.tok, w.T - tok0);  // tokens of this group
-            if (count <= 0) continue;
-            const int t = tok0 + row_tok;
-            const bool valid = row_tok < count;
-            const bool act = quad * 32 < count * p.G;  // some row of this warp is valid
-            const int ng = kAlt ? (w.n + 1 - g) >> 1 : (g ? w.n1 : w.n0);
-            const size_t orow = (size_t(w.q_row) + t) * p.H_q + w.kvh * p.G + row_head;
+            const int count = uniform(min(p.tok, w.T - tok0));  // tokens of this group
+            if (count <= 0) {
+                done_with_item();
+                continue;
+            }
+            const int ng = uniform(kAlt ? (w.n + 1 - g) >> 1 : (g ? w.n1 : w.n0));
+            // some row of this warp is valid
+            const bool act = __any_sync(0xffffffffu, row_tok < count);
             if (kMode == kPrompts && ng == 0) {  // queries that see no key
-                if (valid) {
+                if (row_tok < count) {
+                    const size_t orow = (size_t(w.q_row) + tok0 + row_tok) * p.H_q +
+                                        w.kvh * p.G + row_head;
                     uint4* dst = reinterpret_cast<uint4*>(p.o + orow * D);
+#pragma unroll 1
                     for (int i = 0; i < D / 8; ++i) dst[i] = make_uint4(0, 0, 0, 0);
                     if (p.lse) p.lse[orow] = -INFINITY;
                 }
+                done_with_item();
                 continue;
             }
-            const int lim = kTree ? 0 : token_limit(p, w, t);
-            const int lim_first = group_first<kMode>(p, w, g);
+            // Keys of tile i that this row sees, for the tiles from `plain` on:
+            // c < last - 128 i. The drafted tokens' tile goes by the bits.
+            const int plain = uniform(plain_tiles<kMode>(p, w, kTree ? 0 : g));
+            const int last = (kTree ? w.ctx : token_limit(p, w, tok0 + row_tok)) - w.j0 * BN;
+            const int own_tile = kTree ? uniform(w.c_t - w.j0) : 0;
             uint32_t bits[4] = {0, 0, 0, 0};  // drafted tokens this row sees
-            const bool own = w.j0 + w.n > w.c_t;  // the item has the row's own tokens
-            if (kTree && own && valid) {
+            if (kTree && own_tile < w.n && row_tok < count) {
+                const int t = tok0 + row_tok;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int rest = w.T - 32 * i;  // tokens from this word on
@@ -896,6 +992,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             RowState st{-INFINITY, 0.f, 0.f};
+#pragma unroll 1
             for (int i = 0; i < ng && alive; ++i) {
                 alive = wait_all(bSFull + g, tt + i);
                 if (!alive) break;
@@ -910,21 +1007,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int e = 0; e < 32; ++e) sv[c * 32 + e] = __uint_as_float(x[e]);
                     }
                     tc::tmem_wait_ld();
-                    const int jj = w.j0 + (kAlt ? 2 * i + g : i);
-                    if (kTree) {
-                        if (jj >= w.c_t) {
+                    const int j = kAlt ? 2 * i + g : i;
+                    if (j >= plain) {
+                        if (kTree && j >= own_tile) {
 #pragma unroll
                             for (int c = 0; c < BN; ++c)
                                 sv[c] = (bits[c >> 5] >> (c & 31)) & 1 ? sv[c] : -INFINITY;
-                        } else if (w.ctx - jj * BN < BN) {
-                            const int last = w.ctx - jj * BN;
+                        } else {
+                            const int lim = last - j * BN;
 #pragma unroll
-                            for (int c = 0; c < BN; ++c) sv[c] = c < last ? sv[c] : -INFINITY;
+                            for (int c = 0; c < BN; ++c) sv[c] = c < lim ? sv[c] : -INFINITY;
                         }
-                    } else if (lim_first - jj * BN < BN) {
-                        const int last = lim - jj * BN;
-#pragma unroll
-                        for (int c = 0; c < BN; ++c) sv[c] = c < last ? sv[c] : -INFINITY;
                     }
                     const float corr = softmax_tile(sv, st, p.scale_log2, c2, lane_base + col_s);
                     // O is complete here: this tile's S product was issued after
@@ -961,7 +1054,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             // ---- epilogue. Every read of O completes before this warp's next
             // P arrive, which is what lets the next item overwrite O.
             float f0 = 1.f, f1 = 0.f;  // weights of O_0 and O_1 (kTreeAlt)
-            const bool two = kAlt && w.n > 1;
+            const Item e = read_item(item_addr);
+            const bool two = kAlt && uniform(e.n) > 1;
             if constexpr (kAlt) {
                 xch[g * BM + row] = make_float4(st.m, st.l, st.lb, 0.f);
                 __syncwarp();
@@ -985,8 +1079,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (act) {
                 tc::fence_after_sync();
-                const bool direct = !kTree || w.dst < 0;
-                const size_t prow = kTree ? size_t(w.dst) * p.part_rows + (t - w.tok0) * p.G + row_head
+                const int t = (kAlt ? e.tok0 : e.tok0 + g * p.tok) + row_tok;
+                const bool valid = row_tok < p.tok && t < e.T;
+                const bool own = e.j0 + e.n > e.c_t;  // the item has the row's own tokens
+                const size_t orow = (size_t(e.q_row) + t) * p.H_q + e.kvh * p.G + row_head;
+                const bool direct = !kTree || uniform(e.dst) < 0;
+                const size_t prow = kTree ? size_t(e.dst) * p.part_rows + (t - e.tok0) * p.G + row_head
                                           : 0;
                 uint8_t* own_row =
                     !valid ? nullptr
@@ -998,6 +1096,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const bool odd = *odd_values != 0 && own;
                 const int c_begin = kAlt ? g * (D / 64) : 0;
                 const int c_end = kAlt ? (g + 1) * (D / 64) : D / 32;
+#pragma unroll 1
                 for (int c = c_begin; c < c_end; ++c) {
                     uint32_t x[32];
                     tc::tmem_ld32(lane_base + (kAlt ? col_o_of(0) : col_o) + c * 32, x);
@@ -1007,29 +1106,30 @@ __global__ void __launch_bounds__(kThreads, 1)
                             tc::tmem_ld32(lane_base + col_o_of(1) + c * 32, y);
                             tc::tmem_wait_ld();
 #pragma unroll
-                            for (int e = 0; e < 32; ++e)
-                                x[e] = __float_as_uint(f0 * __uint_as_float(x[e]) +
-                                                       f1 * __uint_as_float(y[e]));
+                            for (int i = 0; i < 32; ++i)
+                                x[i] = __float_as_uint(f0 * __uint_as_float(x[i]) +
+                                                       f1 * __uint_as_float(y[i]));
                         }
                     }
                     tc::tmem_wait_ld();
                     if (odd && valid) {
                         // values that are not finite among the keys that not every
                         // row sees: those that this row sees are added here
-                        const int k_end = kTree ? w.n_own : lim;
+                        const int k_end = kTree ? e.n_own : token_limit(p, e, t);
+#pragma unroll 1
                         for (int k = kTree ? 0 : group_first<kMode>(p, w, 0); k < k_end; ++k) {
                             if (kTree) {
                                 const uint32_t word = k < 32 ? bits[0] : k < 64 ? bits[1]
                                                     : k < 96 ? bits[2] : bits[3];
                                 if (!((word >> (k & 31)) & 1)) continue;
                             }
-                            const uint16_t* vr = p.v + (int64_t(w.k_row) + k) * p.v_st +
-                                                 w.kvh * p.v_sh + c * 32;
+                            const uint16_t* vr = p.v + (int64_t(e.k_row) + k) * p.v_st +
+                                                 e.kvh * p.v_sh + c * 32;
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) {
-                                const uint32_t bf = vr[e];
+                            for (int i = 0; i < 32; ++i) {
+                                const uint32_t bf = vr[i];
                                 if ((bf & 0x7f80u) == 0x7f80u)
-                                    x[e] = __float_as_uint(__uint_as_float(x[e]) +
+                                    x[i] = __float_as_uint(__uint_as_float(x[i]) +
                                                            __uint_as_float(bf << 16));
                             }
                         }
@@ -1038,9 +1138,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                         uint4 v[4];
                         uint32_t* u = reinterpret_cast<uint32_t*>(v);
 #pragma unroll
-                        for (int e = 0; e < 16; ++e)
-                            u[e] = pack_bf16x2(__uint_as_float(x[2 * e]) * inv,
-                                               __uint_as_float(x[2 * e + 1]) * inv);
+                        for (int i = 0; i < 16; ++i)
+                            u[i] = pack_bf16x2(__uint_as_float(x[2 * i]) * inv,
+                                               __uint_as_float(x[2 * i + 1]) * inv);
                         store_rows(stage, lane, v, rows, c * 64);
                     } else {
 #pragma unroll
@@ -1048,8 +1148,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                             uint4 v[4];
                             uint32_t* u = reinterpret_cast<uint32_t*>(v);
 #pragma unroll
-                            for (int e = 0; e < 16; ++e)
-                                u[e] = __float_as_uint(__uint_as_float(x[h * 16 + e]) * inv);
+                            for (int i = 0; i < 16; ++i)
+                                u[i] = __float_as_uint(__uint_as_float(x[h * 16 + i]) * inv);
                             store_rows(stage, lane, v, rows, c * 128 + h * 64);
                         }
                     }
@@ -1068,8 +1168,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(bXchDone));
                 alive = wait_all(bXchDone, xk);
+                if (!alive) break;
                 ++xk;
             }
+            done_with_item();
         }
     }
 
@@ -1205,10 +1307,10 @@ bool packed_maps(Maps& m, const Params& p, const uint16_t* q, const uint16_t* k,
         return false;
     m.k = m.v = m.kc = m.vc = m.q;  // never read unless set
     if (p.total_k == 0) return true;
-    return encode_tmap_3d_bf16_strided(&m.k, k, d, p.H_kv, p.total_k, fix(k_sh, p.H_kv),
-                                       fix(k_st, p.total_k), 1, BN) == cudaSuccess &&
-           encode_tmap_3d_bf16_strided(&m.v, v, d, p.H_kv, p.total_k, fix(v_sh, p.H_kv),
-                                       fix(v_st, p.total_k), 1, BN) == cudaSuccess;
+    return encode_tmap_3d_bf16_strided(&m.k, k, d, p.total_k, p.H_kv, fix(k_st, p.total_k),
+                                       fix(k_sh, p.H_kv), BN, 1) == cudaSuccess &&
+           encode_tmap_3d_bf16_strided(&m.v, v, d, p.total_k, p.H_kv, fix(v_st, p.total_k),
+                                       fix(v_sh, p.H_kv), BN, 1) == cudaSuccess;
 }
 
 // CTAs of a decode_tree launch work in teams of one per block of 2 * tok
