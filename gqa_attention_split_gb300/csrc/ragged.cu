@@ -48,6 +48,7 @@ constexpr int kRingSlots = 4;        // K/V tiles in flight
 constexpr int kItemSlots = 4;        // work items known ahead
 constexpr int kSchedSeqs = 1024;     // sequences whose schedule is kept in shared memory
 constexpr int kTreeCtas = 152;       // most CTAs of a decode_tree launch (workspace size)
+constexpr int kWholeTiles = 9;       // decode_tree: rows of at most this many tiles are not cut
 constexpr uint32_t kBoxBytes = BM * 128;       // 128 rows x 64 bf16
 constexpr uint32_t kStageBytes = 32 * 64;      // a warp's output stage: 32 rows x 64 B
 constexpr uint32_t kTmemCols = 512;            // S_0, S_1, O_0, O_1
@@ -64,7 +65,11 @@ struct Params {
     const uint16_t* v;            // packed V, read again only for values that are not finite
     uint16_t* o;                  // [total_q, H_q, d]
     float* lse;                   // [total_q, H_q] or null
-    float *part_o, *part_lse;     // decode_tree: [slot][part_rows][d], [slot][part_rows]
+    // decode_tree: partial results, two slots per CTA. O is laid out
+    // [slot][d / 4][part_rows][4] so that a warp, one row per lane, reads and
+    // writes 512 contiguous bytes at a time.
+    float *part_o, *part_lse;     // lse: [slot][part_rows]
+    int4* part_info;              // [CTA]: the unit that begins there (see schedule_tree)
     const int32_t *cu_q, *cu_k, *ctx;
     const uint32_t* mask;         // [total_q, mask_words] or null
     unsigned* status;
@@ -73,7 +78,8 @@ struct Params {
     int tok;          // tokens of a group
     int head_group;   // kPrompts: KV heads whose items are scheduled together
     int team;         // decode_tree: CTAs that share a range of keys, one per token block
-    int n_teams, min_tiles, part_rows;
+    int n_teams, part_rows;
+    int whole;        // decode_tree: no (row, KV head) is cut
     float scale_log2;
     int inject_timeout;  // test hook: block 0 withholds its first Q copy
 };
@@ -368,60 +374,109 @@ __device__ __forceinline__ void schedule_prompts(const Params& p, int2* seqs, Pu
     pub.put(end, lane);
 }
 
-// decode_tree. The tiles of all rows and KV heads in one line, cut into equal
-// ranges, one per team of CTAs: however ragged the contexts are, every CTA
-// streams the same number of keys. The members of a team take the token blocks
-// of the same keys at the same time (K and V come from L2 for all but one). A
-// (row, head) that is cut leaves partial results for the merge.
-struct TreeSplit {
-    int total, per;  // tiles, tiles of a team
-};
-__device__ __forceinline__ TreeSplit tree_split(const Params& p, int lane, bool& bad) {
-    int t = 0;
-#pragma unroll 1
-    for (int b = lane; b < p.B; b += 32) {
-        int q0, T, ctx;
-        tree_row(p, b, q0, T, ctx, bad);
-        t += tree_tiles(T, ctx) * p.H_kv;
-    }
-    TreeSplit s;
-    s.total = __reduce_add_sync(0xffffffffu, t);
-    s.per = max(p.min_tiles, cdiv(s.total, p.n_teams));
-    return s;
-}
+// decode_tree. A unit is one KV head of one row: tiles of keys that one block
+// of drafted tokens runs. CTAs work in teams; the members of a team take the
+// token blocks of the same keys at the same time (K and V come from L2 for all
+// but one). How the units are cut into the teams' shares:
+//  - whole: not at all, unit u goes to team u mod n_teams (short caches);
+//  - even: every unit into equal parts of at most `even` tiles, one part per
+//    team, when that many parts exist;
+//  - else all units in one line, cut every `per` tiles: however ragged the
+//    contexts are, every team streams the same number of keys, at the price of
+//    a second and third item where a share crosses into the next unit.
+// "even" may take up to kEvenSlack more tiles than the line would: about what
+// an item's first loads and epilogue cost. A unit that is cut leaves partial
+// results for the merge.
+constexpr int kEvenSlack = 4;
 
+// The CTA that holds the first part of a unit describes it for the merge in
+// part_info: x the packed index of its token block's first token, y the rows of
+// the block (tokens x G), z the KV head, w the number of parts (0: nothing to
+// merge); the other parts are those of the next teams.
 template <int kMode>
 __device__ __forceinline__ void schedule_tree(const Params& p, Publisher& pub, int lane) {
     bool bad = false;
-    const TreeSplit sp = tree_split(p, lane, bad);
-    if (bad && blockIdx.x == 0) atomicOr(p.status, kStatusBadSeqlen);
     const int team = blockIdx.x / p.team, member = blockIdx.x % p.team;
-    const int64_t begin = int64_t(team) * sp.per;
-    const int end = int(min(int64_t(sp.total), begin + sp.per));
-    int before = 0;  // tiles of the rows before b0
-    int x = int(min(begin, int64_t(end)));
-    for (int b0 = 0; b0 < p.B && x < end; b0 += 32) {
-        int q0 = 0, T = 0, ctx = 0, tiles = 0;
-        if (b0 + lane < p.B) {
-            tree_row(p, b0 + lane, q0, T, ctx, bad);
-            tiles = tree_tiles(T, ctx);
+    // the first 32 rows' numbers stay in registers
+    int q0_0 = 0, T_0 = 0, ctx_0 = 0;
+    if (lane < p.B) tree_row(p, lane, q0_0, T_0, ctx_0, bad);
+    auto row_of = [&](int b0, int& q0, int& T, int& ctx) {
+        if (b0 == 0) {
+            q0 = q0_0;
+            T = T_0;
+            ctx = ctx_0;
+        } else {
+            q0 = T = ctx = 0;
+            if (b0 + lane < p.B) tree_row(p, b0 + lane, q0, T, ctx, bad);
         }
-        int sum = tiles * p.H_kv;  // inclusive prefix sum over the lanes
+    };
+    // sums over the rows of the parts of at most L tiles (L = 1: of the tiles)
+    auto parts_of = [&](int L) {
+        int t = 0;
+#pragma unroll 1
+        for (int b0 = 0; b0 < p.B; b0 += 32) {
+            int q0, T, ctx;
+            row_of(b0, q0, T, ctx);
+            t += cdiv(tree_tiles(T, ctx), L);
+        }
+        return __reduce_add_sync(0xffffffffu, t) * p.H_kv;
+    };
+    int even = 0, per = 1, end = 0, x = 0;  // this team's share [x, end) of the line
+    if (p.whole) {
+        x = team;
+        end = 0x7fffffff;
+    } else {
+        const int total = parts_of(1);
+        per = max(1, cdiv(total, p.n_teams));
+#pragma unroll 1
+        for (int L = per; L <= per + kEvenSlack && !even; ++L)
+            if (parts_of(L) <= p.n_teams) even = L;
+        const int64_t begin = int64_t(team) * per;
+        x = even ? team : int(min(begin, int64_t(total)));
+        end = even ? team + 1 : int(min(int64_t(total), begin + per));
+    }
+    if (bad && blockIdx.x == 0) atomicOr(p.status, kStatusBadSeqlen);
+    if (!p.whole && lane == 0) p.part_info[blockIdx.x] = make_int4(0, 0, 0, 0);
+    // In the line a unit is `size` steps long: its tiles, its parts, or 1.
+    int before = 0;  // steps of the rows before b0
+#pragma unroll 1
+    for (int b0 = 0; b0 < p.B && x < end; b0 += 32) {
+        int q0, T, ctx;
+        row_of(b0, q0, T, ctx);
+        const int tiles = tree_tiles(T, ctx);
+        const int size = p.whole ? min(tiles, 1) : even ? cdiv(tiles, even) : tiles;
+        int sum = size * p.H_kv;  // inclusive prefix sum over the lanes
         for (int o = 1; o < 32; o <<= 1) {
             const int y = __shfl_up_sync(0xffffffffu, sum, o);
             if (lane >= o) sum += y;
         }
         const int all = __shfl_sync(0xffffffffu, sum, 31);
+#pragma unroll 1
         while (x < end && x < before + all) {
             const int src = __ffs(__ballot_sync(0xffffffffu, before + sum > x)) - 1;
             const int row_tiles = __shfl_sync(0xffffffffu, tiles, src);
-            const int row_begin =
-                before + __shfl_sync(0xffffffffu, sum, src) - row_tiles * p.H_kv;
+            const int row_size = __shfl_sync(0xffffffffu, size, src);
+            const int at = x - (before + __shfl_sync(0xffffffffu, sum, src) - row_size * p.H_kv);
+            const int i = at % row_size;  // step of the unit
             Item w{};
             w.b = b0 + src;
-            w.kvh = (x - row_begin) / row_tiles;
-            w.j0 = (x - row_begin) % row_tiles;
-            w.n = min(row_tiles - w.j0, end - x);
+            w.kvh = at / row_size;
+            int parts;
+            if (p.whole) {
+                w.n = row_tiles;
+                parts = 1;
+                x += p.n_teams;
+            } else if (even) {
+                w.j0 = int(int64_t(row_tiles) * i / row_size);
+                w.n = int(int64_t(row_tiles) * (i + 1) / row_size) - w.j0;
+                parts = row_size;
+                ++x;
+            } else {
+                w.j0 = i;
+                w.n = min(row_tiles - i, end - x);
+                parts = (x - i + row_tiles - 1) / per - (x - i) / per + 1;
+                x += w.n;
+            }
             w.q_row = w.k_row = __shfl_sync(0xffffffffu, q0, src);
             w.T = w.n_own = __shfl_sync(0xffffffffu, T, src);
             w.ctx = __shfl_sync(0xffffffffu, ctx, src);
@@ -429,10 +484,13 @@ __device__ __forceinline__ void schedule_tree(const Params& p, Publisher& pub, i
             w.tok0 = member * 2 * p.tok;
             w.n0 = w.n;
             w.n1 = w.tok0 + p.tok < w.T ? w.n : 0;
-            // slot 2c: the range begins inside the (row, head); 2c + 1: it ends inside
-            w.dst = w.n == row_tiles ? -1 : 2 * int(blockIdx.x) + (w.j0 == 0);
-            x += w.n;
-            if (w.tok0 < w.T && !pub.put(w, lane)) return;
+            if (w.tok0 >= w.T) continue;
+            // slot 2c + 1 holds the first part of a unit, 2c another one
+            w.dst = parts == 1 ? -1 : 2 * int(blockIdx.x) + (w.j0 == 0);
+            if (parts > 1 && w.j0 == 0 && lane == 0)
+                p.part_info[blockIdx.x] = make_int4(
+                    w.q_row + w.tok0, min(w.T - w.tok0, 2 * p.tok) * p.G, w.kvh, parts);
+            if (!pub.put(w, lane)) return;
         }
         before += all;
     }
@@ -584,6 +642,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
+    if (threadIdx.x == 0) {
+        tma_prefetch_desc(&tmap_q);
+        tma_prefetch_desc(&tmap_k);
+        tma_prefetch_desc(&tmap_v);
+        if (kTree) {
+            tma_prefetch_desc(&tmap_kc);
+            tma_prefetch_desc(&tmap_vc);
+        }
+    }
     // Nothing above touches global memory: it overlaps the previous kernel.
     grid_launch_dependents();
     grid_wait_primary();
@@ -610,15 +677,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       if (warp == 0) {
         // ------------------------------------------------------ TMA producer
-        if (lane == 0) {
-            tma_prefetch_desc(&tmap_q);
-            tma_prefetch_desc(&tmap_k);
-            tma_prefetch_desc(&tmap_v);
-            if (kTree) {
-                tma_prefetch_desc(&tmap_kc);
-                tma_prefetch_desc(&tmap_vc);
-            }
-        }
         int r = 0, q_loads = 0;  // ring items and Q loads before this item
         int issued = 0;          // ring items this lane issued
         bool withheld = false;
@@ -1084,12 +1142,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const bool own = e.j0 + e.n > e.c_t;  // the item has the row's own tokens
                 const size_t orow = (size_t(e.q_row) + t) * p.H_q + e.kvh * p.G + row_head;
                 const bool direct = !kTree || uniform(e.dst) < 0;
-                const size_t prow = kTree ? size_t(e.dst) * p.part_rows + (t - e.tok0) * p.G + row_head
-                                          : 0;
+                // row of the item's token block
+                const int prow = (t - e.tok0) * p.G + row_head;
                 uint8_t* own_row =
-                    !valid ? nullptr
-                    : direct ? reinterpret_cast<uint8_t*>(p.o + orow * D)
-                             : reinterpret_cast<uint8_t*>(p.part_o + prow * D);
+                    valid && direct ? reinterpret_cast<uint8_t*>(p.o + orow * D) : nullptr;
                 const RowPtrs rows(own_row, lane);
                 // l is 0 only for a row that saw no key (and NaN stays NaN)
                 const float inv = st.lb == 0.f ? 0.f : 1.f / st.lb;
@@ -1142,22 +1198,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                             u[i] = pack_bf16x2(__uint_as_float(x[2 * i]) * inv,
                                                __uint_as_float(x[2 * i + 1]) * inv);
                         store_rows(stage, lane, v, rows, c * 64);
-                    } else {
+                    } else if (valid) {
+                        float4* dst = reinterpret_cast<float4*>(p.part_o) +
+                                      (size_t(e.dst) * (D / 4) + c * 8) * p.part_rows + prow;
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            uint4 v[4];
-                            uint32_t* u = reinterpret_cast<uint32_t*>(v);
-#pragma unroll
-                            for (int i = 0; i < 16; ++i)
-                                u[i] = __float_as_uint(__uint_as_float(x[h * 16 + i]) * inv);
-                            store_rows(stage, lane, v, rows, c * 128 + h * 64);
-                        }
+                        for (int h = 0; h < 8; ++h)
+                            dst[size_t(h) * p.part_rows] =
+                                make_float4(__uint_as_float(x[4 * h]) * inv,
+                                            __uint_as_float(x[4 * h + 1]) * inv,
+                                            __uint_as_float(x[4 * h + 2]) * inv,
+                                            __uint_as_float(x[4 * h + 3]) * inv);
                     }
                 }
                 if (valid && (!kAlt || g == 0)) {
                     const float lse = st.l == 0.f ? -INFINITY : (st.m + log2f(st.l)) * kLn2;
                     if (!direct)
-                        p.part_lse[prow] = lse;
+                        p.part_lse[size_t(e.dst) * p.part_rows + prow] = lse;
                     else if (p.lse)
                         p.lse[orow] = lse;
                 }
@@ -1183,75 +1239,109 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-// Folds the partial results of every (row, KV head, token block) that more
-// than one range of keys covers, in key order:
+// Folds the partial results of every unit that was cut, in key order:
 //   lse = ln sum_i exp(lse_i),  O = sum_i exp(lse_i - lse) O_i.
-// One warp per query row; nothing to do for a block that one item covered.
-constexpr int kMergeWarps = 8;
+// A task is 32 rows (one per lane) x 32 columns of one unit's token block; of
+// the 8 warps, two take 16 columns each and four a quarter of the parts each,
+// so that a unit cut into many parts is read with every load in flight. The
+// work is bound by those loads' latency and bytes (L2).
+constexpr int kMergeThreads = 256;
 
 template <int D>
-__global__ void __launch_bounds__(kMergeWarps * 32) merge_kernel(const Params p) {
-    constexpr int kPer = D / 32;
+__global__ void __launch_bounds__(kMergeThreads) merge_kernel(const Params p) {
+    __shared__ int list[kTreeCtas];       // CTAs that begin a unit that was cut
+    __shared__ int counts[kMergeThreads / 32];
+    __shared__ float4 acc_s[6][5][32];    // per warp: 4 x 4 columns, the weights' sum
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     grid_launch_dependents();
     grid_wait_primary();
-    const int lane = threadIdx.x & 31;
-    const int chunks = cdiv(p.part_rows, kMergeWarps);
-    const int unit = blockIdx.x / chunks;  // (row, KV head, block), block innermost
-    const int r = (blockIdx.x % chunks) * kMergeWarps + (threadIdx.x >> 5);
-    const int member = unit % p.team, kvh = (unit / p.team) % p.H_kv, b = unit / p.team / p.H_kv;
-    bool bad = false;
-    int q0, T, ctx;
-    tree_row(p, b, q0, T, ctx, bad);
-    const int tok = member * 2 * p.tok + r / p.G;
-    if (r >= p.part_rows || tok >= T) return;
-    const TreeSplit sp = tree_split(p, lane, bad);
-    int before = 0;  // tiles of the rows before b
-    for (int i = lane; i < b; i += 32) {
-        int a, t, c;
-        tree_row(p, i, a, t, c, bad);
-        before += tree_tiles(t, c) * p.H_kv;
+    const int ctas = p.n_teams * p.team;
+    static_assert(kTreeCtas <= kMergeThreads, "one thread per CTA of the launch");
+    const bool cut = int(threadIdx.x) < ctas && p.part_info[threadIdx.x].w > 0;
+    const unsigned votes = __ballot_sync(0xffffffffu, cut);
+    if (lane == 0) counts[warp] = __popc(votes);
+    __syncthreads();
+    int n = 0, mine = __popc(votes & ((1u << lane) - 1));
+    for (int i = 0; i < kMergeThreads / 32; ++i) {
+        if (i < warp) mine += counts[i];
+        n += counts[i];
     }
-    const int tiles = tree_tiles(T, ctx);
-    const int x0 = __reduce_add_sync(0xffffffffu, before) + kvh * tiles;
-    const int first = x0 / sp.per, last = (x0 + tiles - 1) / sp.per;  // teams
-    if (first == last) return;
-    // part i comes from team first + i: slot 2c + 1 of its first CTA, 2c of the others
-    auto slot = [&](int i) {
-        const int c = (first + i) * p.team + member;
-        return size_t(2 * c + (i == 0)) * p.part_rows + r;
-    };
-    const int parts = last - first + 1;
-    float mx = -INFINITY;
-    for (int i = lane; i < parts; i += 32) mx = fmaxf(mx, p.part_lse[slot(i)]);
-    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-    const float ms = mx == -INFINITY ? 0.f : mx;
-    float acc[kPer], sum = 0.f;
+    if (cut) list[mine] = threadIdx.x;
+    __syncthreads();
+    const int chunks = cdiv(p.part_rows, 32);
+    const int col_warp = warp & 1, part_warp = warp >> 1;
+    for (int task = blockIdx.x; task < n * chunks * (D / 32); task += gridDim.x) {
+        const int c = list[task / (chunks * (D / 32))];
+        const int chunk = task / (D / 32) % chunks;
+        const int col4 = (task % (D / 32)) * 8 + col_warp * 4;  // first group of 4 columns
+        const int4 info = p.part_info[c];
+        const int r = chunk * 32 + lane, parts = info.w;
+        if (chunk * 32 >= info.y) continue;  // (the same for the whole block)
+        const bool valid = r < info.y;
+        // part i is that of CTA c + i * team: slot 2c + 1 for the first, 2c for the others
+        auto slot = [&](int i) { return size_t(2 * (c + i * p.team) + (i == 0)); };
+        float mx = -INFINITY;
+        if (valid)
+            for (int i = 0; i < parts; ++i)
+                mx = fmaxf(mx, p.part_lse[slot(i) * p.part_rows + r]);
+        const float ms = mx == -INFINITY ? 0.f : mx;
+        float sum = 0.f;
+        float4 acc[4];
 #pragma unroll
-    for (int e = 0; e < kPer; ++e) acc[e] = 0.f;
-    for (int base = 0; base < parts; base += 32) {
-        const int cnt = min(32, parts - base);
-        const float wt = lane < cnt ? exp2f((p.part_lse[slot(base + lane)] - ms) * kLog2e) : 0.f;
-        sum += wt;
-#pragma unroll 4
-        for (int i = 0; i < cnt; ++i) {
-            const float wi = __shfl_sync(0xffffffffu, wt, i);
-            const float* src = p.part_o + slot(base + i) * D + lane * kPer;
-            float f[kPer];
-            if constexpr (kPer == 4)
-                *reinterpret_cast<float4*>(f) = *reinterpret_cast<const float4*>(src);
-            else
-                *reinterpret_cast<float2*>(f) = *reinterpret_cast<const float2*>(src);
+        for (int h = 0; h < 4; ++h) acc[h] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (valid) {
+#pragma unroll 2
+            for (int i = part_warp; i < parts; i += 4) {
+                const float w = exp2f((p.part_lse[slot(i) * p.part_rows + r] - ms) * kLog2e);
+                const float4* src = reinterpret_cast<const float4*>(p.part_o) +
+                                    (slot(i) * (D / 4) + col4) * p.part_rows + r;
+                sum += w;
 #pragma unroll
-            for (int e = 0; e < kPer; ++e) acc[e] += wi * f[e];
+                for (int h = 0; h < 4; ++h) {
+                    const float4 v = src[size_t(h) * p.part_rows];
+                    acc[h].x += w * v.x;
+                    acc[h].y += w * v.y;
+                    acc[h].z += w * v.z;
+                    acc[h].w += w * v.w;
+                }
+            }
         }
-    }
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    const size_t orow = (size_t(q0) + tok) * p.H_q + kvh * p.G + r % p.G;
-    uint32_t* out = reinterpret_cast<uint32_t*>(p.o + orow * D) + lane * (kPer / 2);
+        if (part_warp > 0) {
+            float4(*mine_s)[32] = acc_s[warp - 2];
 #pragma unroll
-    for (int e = 0; e < kPer / 2; ++e) out[e] = pack_bf16x2(acc[2 * e] * inv, acc[2 * e + 1] * inv);
-    if (lane == 0 && p.lse) p.lse[orow] = sum == 0.f ? -INFINITY : ms + logf(sum);
+            for (int h = 0; h < 4; ++h) mine_s[h][lane] = acc[h];
+            mine_s[4][lane].x = sum;
+        }
+        __syncthreads();
+        if (part_warp == 0 && valid) {
+#pragma unroll
+            for (int k = 1; k < 4; ++k) {
+                float4(*other)[32] = acc_s[2 * k + col_warp - 2];
+#pragma unroll
+                for (int h = 0; h < 4; ++h) {
+                    const float4 v = other[h][lane];
+                    acc[h].x += v.x;
+                    acc[h].y += v.y;
+                    acc[h].z += v.z;
+                    acc[h].w += v.w;
+                }
+                sum += other[4][lane].x;
+            }
+            const float inv = sum == 0.f ? 0.f : 1.f / sum;
+            const size_t orow = (size_t(info.x) + r / p.G) * p.H_q + info.z * p.G + r % p.G;
+            uint4* out = reinterpret_cast<uint4*>(p.o + orow * D + col4 * 4);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const float4 a = acc[2 * h], b = acc[2 * h + 1];
+                out[h] = make_uint4(pack_bf16x2(a.x * inv, a.y * inv),
+                                    pack_bf16x2(a.z * inv, a.w * inv),
+                                    pack_bf16x2(b.x * inv, b.y * inv),
+                                    pack_bf16x2(b.z * inv, b.w * inv));
+            }
+            if (col4 == 0 && p.lse) p.lse[orow] = sum == 0.f ? -INFINITY : ms + logf(sum);
+        }
+        __syncthreads();  // acc_s is free again
+    }
 }
 
 // ------------------------------------------------------------------ host side
@@ -1451,8 +1541,8 @@ extern "C" size_t gqa_attn_decode_tree_workspace_size(int H_q, int H_kv, int d, 
         max_tokens > ragged::kMaxTreeTokens || H_q / H_kv > 16)
         return 0;
     const ragged::TreePlan t = ragged::tree_plan(H_q / H_kv, max_tokens);
-    // two slots per CTA: fp32 O and lse of part_rows rows
-    return size_t(2) * ragged::kTreeCtas * t.part_rows * (d + 1) * 4;
+    // a description and two slots per CTA: fp32 O and lse of part_rows rows
+    return size_t(ragged::kTreeCtas) * (16 + size_t(2) * t.part_rows * (d + 1) * 4);
 }
 
 extern "C" int gqa_attn_decode_tree(
@@ -1502,15 +1592,17 @@ extern "C" int gqa_attn_decode_tree(
     p.S_max = S_max; p.max_tokens = max_tokens; p.mask_words = mask_words;
     p.causal = 1;
     p.tok = plan.tok; p.team = plan.team; p.part_rows = plan.part_rows;
-    p.min_tiles = 1;
     p.scale_log2 = scale * kLog2e;
     p.inject_timeout = take_injected_timeout() ? 1 : 0;
-    // no more teams than tiles there can be
-    const int64_t tiles = int64_t(B) * H_kv * ((int64_t(S_max) + BN - 1) / BN + 1);
+    // no more teams than there can be tiles, or units that are not cut
+    const int64_t row_tiles = (int64_t(S_max) + BN - 1) / BN + 1;
+    p.whole = row_tiles <= kWholeTiles;
+    const int64_t shares = int64_t(B) * H_kv * (p.whole ? 1 : row_tiles);
     const int most = (sms < kTreeCtas ? sms : kTreeCtas) / plan.team;
-    p.n_teams = int(tiles < most ? tiles : most < 1 ? 1 : most);
+    p.n_teams = int(shares < most ? shares : most < 1 ? 1 : most);
     const int ctas = p.n_teams * plan.team;
-    p.part_o = static_cast<float*>(workspace);
+    p.part_info = static_cast<int4*>(workspace);
+    p.part_o = reinterpret_cast<float*>(p.part_info + kTreeCtas);
     p.part_lse = p.part_o + size_t(2) * ctas * p.part_rows * d;
     Maps m;
     if (!packed_maps(m, p, q, k_new, v_new, d, q_stride_t, q_stride_h, k_stride_t, k_stride_h,
@@ -1527,11 +1619,11 @@ extern "C" int gqa_attn_decode_tree(
     else
         rl = plan.alt ? launch_ragged<64, kTreeAlt>(m, p, ctas, stream)
                       : launch_ragged<64, kTreePair>(m, p, ctas, stream);
-    if (rl != GQA_OK || p.n_teams == 1) return rl;
-    const unsigned grid =
-        unsigned(B) * H_kv * plan.team * ((p.part_rows + kMergeWarps - 1) / kMergeWarps);
-    return launch(d == 128 ? merge_kernel<128> : merge_kernel<64>, grid, kMergeWarps * 32, 0,
-                  stream, p) == cudaSuccess
+    if (rl != GQA_OK || p.whole || p.n_teams == 1) return rl;
+    const int64_t tasks = int64_t(ctas) * ((p.part_rows + 31) / 32) * (d / 32);
+    const unsigned grid = unsigned(tasks < 4 * kTreeCtas ? tasks : 4 * kTreeCtas);
+    return launch(d == 128 ? merge_kernel<128> : merge_kernel<64>, grid, kMergeThreads, 0, stream,
+                  p) == cudaSuccess
                ? GQA_OK
                : GQA_ERR_CUDA;
 }
