@@ -410,27 +410,30 @@ __device__ __forceinline__ void schedule_tree(const Params& p, Publisher& pub, i
             if (b0 + lane < p.B) tree_row(p, b0 + lane, q0, T, ctx, bad);
         }
     };
-    // sums over the rows of the parts of at most L tiles (L = 1: of the tiles)
-    auto parts_of = [&](int L) {
-        int t = 0;
-#pragma unroll 1
-        for (int b0 = 0; b0 < p.B; b0 += 32) {
-            int q0, T, ctx;
-            row_of(b0, q0, T, ctx);
-            t += cdiv(tree_tiles(T, ctx), L);
-        }
-        return __reduce_add_sync(0xffffffffu, t) * p.H_kv;
-    };
     int even = 0, per = 1, end = 0, x = 0;  // this team's share [x, end) of the line
     if (p.whole) {
         x = team;
         end = 0x7fffffff;
     } else {
-        const int total = parts_of(1);
-        per = max(1, cdiv(total, p.n_teams));
+        int total = 0, parts[kEvenSlack + 1] = {};  // parts of at most per + i tiles
+        auto for_rows = [&](auto f) {
 #pragma unroll 1
-        for (int L = per; L <= per + kEvenSlack && !even; ++L)
-            if (parts_of(L) <= p.n_teams) even = L;
+            for (int b0 = 0; b0 < p.B; b0 += 32) {
+                int q0, T, ctx;
+                row_of(b0, q0, T, ctx);
+                f(tree_tiles(T, ctx));
+            }
+        };
+        for_rows([&](int tiles) { total += tiles; });
+        total = __reduce_add_sync(0xffffffffu, total) * p.H_kv;
+        per = max(1, cdiv(total, p.n_teams));
+        for_rows([&](int tiles) {
+#pragma unroll
+            for (int i = 0; i <= kEvenSlack; ++i) parts[i] += cdiv(tiles, per + i);
+        });
+#pragma unroll
+        for (int i = kEvenSlack; i >= 0; --i)
+            if (__reduce_add_sync(0xffffffffu, parts[i]) * p.H_kv <= p.n_teams) even = per + i;
         const int64_t begin = int64_t(team) * per;
         x = even ? team : int(min(begin, int64_t(total)));
         end = even ? team + 1 : int(min(int64_t(total), begin + per));
@@ -467,8 +470,9 @@ __device__ __forceinline__ void schedule_tree(const Params& p, Publisher& pub, i
                 parts = 1;
                 x += p.n_teams;
             } else if (even) {
-                w.j0 = int(int64_t(row_tiles) * i / row_size);
-                w.n = int(int64_t(row_tiles) * (i + 1) / row_size) - w.j0;
+                // (below 2^32: a row has less than 2^24 tiles and kTreeCtas parts)
+                w.j0 = int(unsigned(row_tiles) * unsigned(i) / unsigned(row_size));
+                w.n = int(unsigned(row_tiles) * unsigned(i + 1) / unsigned(row_size)) - w.j0;
                 parts = row_size;
                 ++x;
             } else {
@@ -791,10 +795,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (kMode == kPrompts) return j + 1 < (g ? n1 : n0) ? BN : (g ? k1 : k0);
                 return j < plain ? BN : (j < j_own ? k1 : k0);
             };
-            // The repair of V tile j starts when the previous tile's products
-            // are issued: only then has its ring slot's earlier use been seen here.
+            // The repair of V tile j may start once V tile j - 2, which had its
+            // ring slot, has been seen here; at most two are asked for at a time.
             auto ask = [&](int j) {
-                if (j >= plain && repair_of<kMode>(p, w, w.j0 + j).needed())
+                if (j >= plain && j < n && repair_of<kMode>(p, w, w.j0 + j).needed())
                     mbar_arrive(bar(bFixAsk + (asked++ & 1)));
             };
             auto repaired = [&](int j) {
@@ -803,8 +807,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 return mbar_wait_bounded(bar(bFixDone + (f & 1)), (f >> 1) & 1, p.status);
             };
             bool alive = true;
+            // Tiles that both groups run whole and that are not a group's last:
+            // no conditions between the issues, which are on the critical path.
+            const int fast = kAlt ? 0 : min(plain, min(n0, n1) - 1);
             if (lane == 0) {
-                ask(0);
+                if (fast <= 0) {
+                    ask(0);
+                    ask(1);
+                }
                 alive = mbar_wait_bounded(bar(bQFull), qi & 1, p.status) && ring_wait(r);
             }
             if (lane == 0 && alive) {
@@ -824,9 +834,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
                 for (int j = 0; j < n && alive; ++j) {
                     const int g = j & 1, rv = r + 2 * j + 1;
-                    if (j + 1 < n) ask(j + 1);
-                    alive = ring_wait(rv) && (j + 2 >= n || ring_wait(rv + 3)) && repaired(j) &&
-                            mbar_wait_bounded(bar(bPFull + g), ((g ? t1 : t0) + (j >> 1)) & 1,
+                    alive = ring_wait(rv) && (j + 2 >= n || ring_wait(rv + 3)) && repaired(j);
+                    if (!alive) break;
+                    ask(j + 2);
+                    alive = mbar_wait_bounded(bar(bPFull + g), ((g ? t1 : t0) + (j >> 1)) & 1,
                                               p.status);
                     if (!alive) break;
                     tc::fence_after_sync();
@@ -847,9 +858,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (n1 > 0) issue_s(1, r);
                 tc::commit(bar(bSlotEmpty + r % kRingSlots));
                 if (n == 1) tc::commit(bar(bQEmpty));
-                // Tiles that both groups run whole and that are not a group's last:
-                // no conditions between the issues, which are on the critical path.
-                const int fast = min(plain, min(n0, n1) - 1);
                 int j = 0;
 #pragma unroll 1
                 for (; j < fast && alive; ++j) {
@@ -869,12 +877,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tc::commit(bar(bSlotEmpty + (rv + 1) % kRingSlots));
                     if (j + 2 == n) tc::commit(bar(bQEmpty));
                 }
-                if (j > 0 && j < n && alive) ask(j);
+                if (j > 0 && alive) {
+                    ask(j);
+                    ask(j + 1);
+                }
 #pragma unroll 1
                 for (; j < n && alive; ++j) {
                     const int rv = r + 2 * j + 1;
-                    if (j + 1 < n) ask(j + 1);
                     alive = ring_wait(rv) && (j + 1 == n || ring_wait(rv + 1)) && repaired(j);
+                    if (alive) ask(j + 2);
 #pragma unroll
                     for (int g = 0; g < 2; ++g) {
                         if (!alive) break;
@@ -1243,15 +1254,16 @@ __global__ void __launch_bounds__(kThreads, 1)
 //   lse = ln sum_i exp(lse_i),  O = sum_i exp(lse_i - lse) O_i.
 // A task is 32 rows (one per lane) x 32 columns of one unit's token block; of
 // the 8 warps, two take 16 columns each and four a quarter of the parts each,
-// so that a unit cut into many parts is read with every load in flight. The
-// work is bound by those loads' latency and bytes (L2).
+// kMergeBatch at a time: bound by the loads' latency, so a unit cut into up to
+// 20 parts is read with every load in flight at once.
 constexpr int kMergeThreads = 256;
+constexpr int kMergeBatch = 5;
 
 template <int D>
 __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const Params p) {
     __shared__ int list[kTreeCtas];       // CTAs that begin a unit that was cut
     __shared__ int counts[kMergeThreads / 32];
-    __shared__ float4 acc_s[6][5][32];    // per warp: 4 x 4 columns, the weights' sum
+    __shared__ float4 acc_s[kMergeThreads / 32][5][32];  // per warp: 4 x 4 columns; maximum, sum
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     grid_launch_dependents();
     grid_wait_primary();
@@ -1269,6 +1281,7 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const Params p) {
     if (cut) list[mine] = threadIdx.x;
     __syncthreads();
     const int chunks = cdiv(p.part_rows, 32);
+    constexpr int kPartWarps = kMergeThreads / 64;
     const int col_warp = warp & 1, part_warp = warp >> 1;
     for (int task = blockIdx.x; task < n * chunks * (D / 32); task += gridDim.x) {
         const int c = list[task / (chunks * (D / 32))];
@@ -1280,52 +1293,81 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const Params p) {
         const bool valid = r < info.y;
         // part i is that of CTA c + i * team: slot 2c + 1 for the first, 2c for the others
         auto slot = [&](int i) { return size_t(2 * (c + i * p.team) + (i == 0)); };
-        float mx = -INFINITY;
-        if (valid)
-            for (int i = 0; i < parts; ++i)
-                mx = fmaxf(mx, p.part_lse[slot(i) * p.part_rows + r]);
-        const float ms = mx == -INFINITY ? 0.f : mx;
-        float sum = 0.f;
+        float mx = -INFINITY, sum = 0.f;
         float4 acc[4];
+        auto add = [&](float w, const float4* v) {
+#pragma unroll
+            for (int h = 0; h < 4; ++h) {
+                acc[h].x += w * v[h].x;
+                acc[h].y += w * v[h].y;
+                acc[h].z += w * v[h].z;
+                acc[h].w += w * v[h].w;
+            }
+        };
+        auto scale = [&](float f) {
+            sum *= f;
+#pragma unroll
+            for (int h = 0; h < 4; ++h) {
+                acc[h].x *= f;
+                acc[h].y *= f;
+                acc[h].z *= f;
+                acc[h].w *= f;
+            }
+        };
+        // exp(lse - mx), 0 for a part that saw no key (-inf), whatever mx is
+        auto weight = [&](float lse) {
+            return lse == -INFINITY ? 0.f : exp2f((lse - mx) * kLog2e);
+        };
 #pragma unroll
         for (int h = 0; h < 4; ++h) acc[h] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (valid) {
-#pragma unroll 2
-            for (int i = part_warp; i < parts; i += 4) {
-                const float w = exp2f((p.part_lse[slot(i) * p.part_rows + r] - ms) * kLog2e);
-                const float4* src = reinterpret_cast<const float4*>(p.part_o) +
-                                    (slot(i) * (D / 4) + col4) * p.part_rows + r;
-                sum += w;
+        for (int i0 = part_warp; i0 < parts; i0 += kPartWarps * kMergeBatch) {
+            float lse[kMergeBatch];
+            float4 v[kMergeBatch][4];
 #pragma unroll
-                for (int h = 0; h < 4; ++h) {
-                    const float4 v = src[size_t(h) * p.part_rows];
-                    acc[h].x += w * v.x;
-                    acc[h].y += w * v.y;
-                    acc[h].z += w * v.z;
-                    acc[h].w += w * v.w;
+            for (int u = 0; u < kMergeBatch; ++u) {
+                const int i = i0 + u * kPartWarps;
+                lse[u] = -INFINITY;
+                if (i < parts && valid) {
+                    lse[u] = p.part_lse[slot(i) * p.part_rows + r];
+                    const float4* src = reinterpret_cast<const float4*>(p.part_o) +
+                                        (slot(i) * (D / 4) + col4) * p.part_rows + r;
+#pragma unroll
+                    for (int h = 0; h < 4; ++h) v[u][h] = src[size_t(h) * p.part_rows];
+                } else {
+#pragma unroll
+                    for (int h = 0; h < 4; ++h) v[u][h] = make_float4(0.f, 0.f, 0.f, 0.f);
                 }
             }
-        }
-        if (part_warp > 0) {
-            float4(*mine_s)[32] = acc_s[warp - 2];
+            float m = mx;
 #pragma unroll
-            for (int h = 0; h < 4; ++h) mine_s[h][lane] = acc[h];
-            mine_s[4][lane].x = sum;
+            for (int u = 0; u < kMergeBatch; ++u) m = fmaxf(m, lse[u]);
+            const float f = mx == -INFINITY ? 0.f : exp2f((mx - m) * kLog2e);
+            mx = m;
+            scale(f);
+#pragma unroll
+            for (int u = 0; u < kMergeBatch; ++u) {
+                const float w = weight(lse[u]);
+                sum += w;
+                add(w, v[u]);
+            }
         }
+#pragma unroll
+        for (int h = 0; h < 4; ++h) acc_s[warp][h][lane] = acc[h];
+        acc_s[warp][4][lane] = make_float4(mx, sum, 0.f, 0.f);
         __syncthreads();
         if (part_warp == 0 && valid) {
+            for (int k = 1; k < kPartWarps; ++k) mx = fmaxf(mx, acc_s[2 * k + col_warp][4][lane].x);
+            const float own = acc_s[warp][4][lane].x;
+            scale(own == -INFINITY ? 0.f : exp2f((own - mx) * kLog2e));
 #pragma unroll
-            for (int k = 1; k < 4; ++k) {
-                float4(*other)[32] = acc_s[2 * k + col_warp - 2];
+            for (int k = 1; k < kPartWarps; ++k) {
+                const float4 ms = acc_s[2 * k + col_warp][4][lane];
+                const float w = weight(ms.x);
+                float4 v[4];
 #pragma unroll
-                for (int h = 0; h < 4; ++h) {
-                    const float4 v = other[h][lane];
-                    acc[h].x += v.x;
-                    acc[h].y += v.y;
-                    acc[h].z += v.z;
-                    acc[h].w += v.w;
-                }
-                sum += other[4][lane].x;
+                for (int h = 0; h < 4; ++h) v[h] = acc_s[2 * k + col_warp][h][lane];
+                sum += w * ms.y;
+                add(w, v);
             }
             const float inv = sum == 0.f ? 0.f : 1.f / sum;
             const size_t orow = (size_t(info.x) + r / p.G) * p.H_q + info.z * p.G + r % p.G;
@@ -1338,7 +1380,7 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const Params p) {
                                     pack_bf16x2(b.x * inv, b.y * inv),
                                     pack_bf16x2(b.z * inv, b.w * inv));
             }
-            if (col4 == 0 && p.lse) p.lse[orow] = sum == 0.f ? -INFINITY : ms + logf(sum);
+            if (col4 == 0 && p.lse) p.lse[orow] = sum == 0.f ? -INFINITY : mx + logf(sum);
         }
         __syncthreads();  // acc_s is free again
     }
@@ -1621,7 +1663,7 @@ extern "C" int gqa_attn_decode_tree(
                       : launch_ragged<64, kTreePair>(m, p, ctas, stream);
     if (rl != GQA_OK || p.whole || p.n_teams == 1) return rl;
     const int64_t tasks = int64_t(ctas) * ((p.part_rows + 31) / 32) * (d / 32);
-    const unsigned grid = unsigned(tasks < 4 * kTreeCtas ? tasks : 4 * kTreeCtas);
+    const unsigned grid = unsigned(tasks < 2 * kTreeCtas ? tasks : 2 * kTreeCtas);
     return launch(d == 128 ? merge_kernel<128> : merge_kernel<64>, grid, kMergeThreads, 0, stream,
                   p) == cudaSuccess
                ? GQA_OK
