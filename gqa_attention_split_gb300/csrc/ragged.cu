@@ -950,35 +950,55 @@ __global__ void __launch_bounds__(kThreads, 1)
                         __all_sync(0xffffffffu, ring_wait(ri));
                 if (!alive) break;
                 const uint32_t tile = smem_u32(smem + Gm::kRingOff + (ri % kRingSlots) * kTileBytes);
-                constexpr int kPieces = Gm::kBoxes * 8;  // 16-byte pieces of a row
-                bool odd = false;
-#pragma unroll 1
-                for (int i = fix.seen * kPieces + lane; i < fix.end * kPieces; i += 32) {
+                // Four 16-byte pieces a lane at a time; a piece without a halfword
+                // whose exponent is all ones (x has none if no lane of
+                // ~x & (0x7f80, 0x7f80) is 0) is left as it is.
+                constexpr int kPieces = Gm::kBoxes * 8;  // pieces of a row
+                auto at = [&](int i) {
                     const int row = i / kPieces, piece = i % kPieces;
-                    const uint32_t at = tile + (piece >> 3) * kBoxBytes + row * 128 + (piece & 7) * 16;
-                    if (row >= fix.keys) {
-                        st_shared_v4(at, make_uint4(0, 0, 0, 0));
-                        continue;
-                    }
-                    uint4 x = ld_shared_v4(at);
-                    uint32_t* u = reinterpret_cast<uint32_t*>(&x);
-                    bool here = false;
+                    return tile + (piece >> 3) * kBoxBytes + row * 128 + (piece & 7) * 16;
+                };
+                bool odd = false;
+                const int scan_end = fix.keys * kPieces;
+#pragma unroll 1
+                for (int i0 = fix.seen * kPieces + lane; i0 < scan_end; i0 += 128) {
+                    uint4 x[4];
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        if ((u[c] & 0x7f80u) == 0x7f80u) {
-                            u[c] &= 0xffff0000u;
-                            here = true;
-                        }
-                        if ((u[c] & 0x7f800000u) == 0x7f800000u) {
-                            u[c] &= 0xffffu;
-                            here = true;
-                        }
+                    for (int u = 0; u < 4; ++u)
+                        x[u] = i0 + 32 * u < scan_end ? ld_shared_v4(at(i0 + 32 * u))
+                                                      : make_uint4(0, 0, 0, 0);
+                    uint32_t hit = 0;
+                    auto test = [&](uint32_t v) {
+                        const uint32_t z = ~v & 0x7f807f80u;
+                        hit |= (z - 0x00010001u) & ~z & 0x80008000u;
+                    };
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) {
+                        test(x[u].x);
+                        test(x[u].y);
+                        test(x[u].z);
+                        test(x[u].w);
                     }
-                    if (here) {
-                        st_shared_v4(at, x);
-                        odd = true;
+                    if (!hit) continue;
+#pragma unroll 1
+                    for (int u = 0; u < 4; ++u) {
+                        if (i0 + 32 * u >= scan_end) break;
+                        uint4 y = ld_shared_v4(at(i0 + 32 * u));
+                        auto clean = [&](uint32_t v) {
+                            if ((v & 0x7f80u) == 0x7f80u) v &= 0xffff0000u;
+                            if ((v & 0x7f800000u) == 0x7f800000u) v &= 0xffffu;
+                            return v;
+                        };
+                        const uint4 z = make_uint4(clean(y.x), clean(y.y), clean(y.z), clean(y.w));
+                        if (z.x != y.x || z.y != y.y || z.z != y.z || z.w != y.w) {
+                            st_shared_v4(at(i0 + 32 * u), z);
+                            odd = true;
+                        }
                     }
                 }
+#pragma unroll 1
+                for (int i = scan_end + lane; i < fix.end * kPieces; i += 32)
+                    st_shared_v4(at(i), make_uint4(0, 0, 0, 0));
                 if (odd) *odd_values = 1;
                 fence_proxy_async_smem();
                 __syncwarp();
@@ -1129,11 +1149,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 xch[g * BM + row] = make_float4(st.m, st.l, st.lb, 0.f);
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(bXch));
-                alive = wait_all(bODone, done0) && (!two || wait_all(bODone + 1, done1)) &&
-                        wait_all(bXch, xk);
+                alive = wait_all(bXch, xk);
                 if (!alive) break;
-                done0 += 1;
-                done1 += two;
                 const float4 a = xch[row], b = xch[BM + row];  // group 1 without tiles: -inf, 0, 0
                 const float m = fmaxf(a.x, b.x), ms = m == -INFINITY ? 0.f : m;
                 f0 = fast_exp2(a.x - ms);
@@ -1141,25 +1158,36 @@ __global__ void __launch_bounds__(kThreads, 1)
                 st.m = m;
                 st.l = f0 * a.y + f1 * b.y;
                 st.lb = f0 * a.z + f1 * b.z;
+            }
+            // (what does not need O comes before the wait for it)
+            const int t = (kAlt ? e.tok0 : e.tok0 + g * p.tok) + row_tok;
+            const bool valid = row_tok < p.tok && t < e.T;
+            const bool own = e.j0 + e.n > e.c_t;  // the item has the row's own tokens
+            const size_t orow = (size_t(e.q_row) + t) * p.H_q + e.kvh * p.G + row_head;
+            const bool direct = !kTree || uniform(e.dst) < 0;
+            // row of the item's token block
+            const int prow = (t - e.tok0) * p.G + row_head;
+            const RowPtrs rows(
+                valid && direct ? reinterpret_cast<uint8_t*>(p.o + orow * D) : nullptr, lane);
+            // l is 0 only for a row that saw no key (and NaN stays NaN)
+            const float inv = st.lb == 0.f ? 0.f : 1.f / st.lb;
+            if (valid && (!kAlt || g == 0)) {
+                const float lse = st.l == 0.f ? -INFINITY : (st.m + log2f(st.l)) * kLn2;
+                if (!direct)
+                    p.part_lse[size_t(e.dst) * p.part_rows + prow] = lse;
+                else if (p.lse)
+                    p.lse[orow] = lse;
+            }
+            if constexpr (kAlt) {
+                alive = wait_all(bODone, done0) && (!two || wait_all(bODone + 1, done1));
+                done1 += two;
             } else {
                 alive = wait_all(bODone + g, done0);
-                if (!alive) break;
-                done0 += 1;
             }
+            if (!alive) break;
+            ++done0;
             if (act) {
                 tc::fence_after_sync();
-                const int t = (kAlt ? e.tok0 : e.tok0 + g * p.tok) + row_tok;
-                const bool valid = row_tok < p.tok && t < e.T;
-                const bool own = e.j0 + e.n > e.c_t;  // the item has the row's own tokens
-                const size_t orow = (size_t(e.q_row) + t) * p.H_q + e.kvh * p.G + row_head;
-                const bool direct = !kTree || uniform(e.dst) < 0;
-                // row of the item's token block
-                const int prow = (t - e.tok0) * p.G + row_head;
-                uint8_t* own_row =
-                    valid && direct ? reinterpret_cast<uint8_t*>(p.o + orow * D) : nullptr;
-                const RowPtrs rows(own_row, lane);
-                // l is 0 only for a row that saw no key (and NaN stays NaN)
-                const float inv = st.lb == 0.f ? 0.f : 1.f / st.lb;
                 const bool odd = *odd_values != 0 && own;
                 const int c_begin = kAlt ? g * (D / 64) : 0;
                 const int c_end = kAlt ? (g + 1) * (D / 64) : D / 32;
@@ -1184,7 +1212,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         // row sees: those that this row sees are added here
                         const int k_end = kTree ? e.n_own : token_limit(p, e, t);
 #pragma unroll 1
-                        for (int k = kTree ? 0 : group_first<kMode>(p, w, 0); k < k_end; ++k) {
+                        for (int k = kTree ? 0 : group_first<kMode>(p, e, 0); k < k_end; ++k) {
                             if (kTree) {
                                 const uint32_t word = k < 32 ? bits[0] : k < 64 ? bits[1]
                                                     : k < 96 ? bits[2] : bits[3];
@@ -1220,13 +1248,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                                             __uint_as_float(x[4 * h + 2]) * inv,
                                             __uint_as_float(x[4 * h + 3]) * inv);
                     }
-                }
-                if (valid && (!kAlt || g == 0)) {
-                    const float lse = st.l == 0.f ? -INFINITY : (st.m + log2f(st.l)) * kLn2;
-                    if (!direct)
-                        p.part_lse[size_t(e.dst) * p.part_rows + prow] = lse;
-                    else if (p.lse)
-                        p.lse[orow] = lse;
                 }
             }
             if constexpr (kAlt) {
