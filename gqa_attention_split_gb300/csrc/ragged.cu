@@ -374,81 +374,95 @@ __device__ __forceinline__ void schedule_prompts(const Params& p, int2* seqs, Pu
     pub.put(end, lane);
 }
 
-// decode_tree. A unit is one KV head of one row: tiles of keys that one block
-// of drafted tokens runs. CTAs work in teams; the members of a team take the
-// token blocks of the same keys at the same time (K and V come from L2 for all
-// but one). How the units are cut into the teams' shares:
+// decode_tree. CTAs work in teams of as many as the longest row can have
+// blocks of drafted tokens. The members of a team run the same tiles of a row
+// at the same time: its blocks against one KV head (K and V then come from L2
+// for all but one), and where a row has fewer blocks, several KV heads. Such a
+// set of KV heads is a unit. How the units are cut into the teams' shares:
 //  - whole: not at all, unit u goes to team u mod n_teams (short caches);
 //  - even: every unit into equal parts of at most `even` tiles, one part per
 //    team, when that many parts exist;
-//  - else all units in one line, cut every `per` tiles: however ragged the
+//  - else all units in one line, cut every `per` steps: however ragged the
 //    contexts are, every team streams the same number of keys, at the price of
-//    a second and third item where a share crosses into the next unit.
-// "even" may take up to kEvenSlack more tiles than the line would: about what
-// an item's first loads and epilogue cost. A unit that is cut leaves partial
-// results for the merge.
+//    a second and third item where a share crosses into the next unit. A unit
+//    is its tiles long and kItemCost steps before them, about what an item's
+//    first loads and its end cost.
+// "even" may take up to kEvenSlack more tiles than the line would, for the same
+// reason. A unit that is cut leaves partial results for the merge. (A batch of
+// 8 rows with contexts of 17 to 31007 and 1 to 64 drafts: 189 us without the
+// item cost and with one KV head in every unit, 153 us with them.)
 constexpr int kEvenSlack = 4;
+constexpr int kItemCost = 2;
 
-// The CTA that holds the first part of a unit describes it for the merge in
-// part_info: x the packed index of its token block's first token, y the rows of
-// the block (tokens x G), z the KV head, w the number of parts (0: nothing to
-// merge); the other parts are those of the next teams.
+// The CTA that holds the first part of a block of a unit describes it for the
+// merge in part_info: x the packed index of the block's first token, y the rows
+// of the block (tokens x G), z the KV head, w the number of parts (0: nothing to
+// merge); the other parts are those of the same member of the next teams.
 template <int kMode>
 __device__ __forceinline__ void schedule_tree(const Params& p, Publisher& pub, int lane) {
     bool bad = false;
     const int team = blockIdx.x / p.team, member = blockIdx.x % p.team;
-    // the first 32 rows' numbers stay in registers
-    int q0_0 = 0, T_0 = 0, ctx_0 = 0;
-    if (lane < p.B) tree_row(p, lane, q0_0, T_0, ctx_0, bad);
-    auto row_of = [&](int b0, int& q0, int& T, int& ctx) {
-        if (b0 == 0) {
-            q0 = q0_0;
-            T = T_0;
-            ctx = ctx_0;
-        } else {
-            q0 = T = ctx = 0;
-            if (b0 + lane < p.B) tree_row(p, b0 + lane, q0, T, ctx, bad);
-        }
+    struct Row {
+        int q0, T, ctx, tiles;
+        int blocks, heads, units;  // blocks of tokens; KV heads of a unit; units
     };
+    auto load_row = [&](int b) {
+        Row r{0, 0, 0, 0, 1, 1, 0};
+        if (b >= p.B) return r;
+        tree_row(p, b, r.q0, r.T, r.ctx, bad);
+        r.tiles = tree_tiles(r.T, r.ctx);
+        if (r.tiles == 0) return r;
+        r.units = p.H_kv;
+        if (p.team > 1) {
+            r.blocks = cdiv(r.T, 2 * p.tok);
+            r.heads = p.team / r.blocks;
+            r.units = cdiv(p.H_kv, r.heads);
+        }
+        return r;
+    };
+    const Row row_0 = load_row(lane);  // the first 32 rows stay in registers
+    auto row_of = [&](int b0) { return b0 == 0 ? row_0 : load_row(b0 + lane); };
     int even = 0, per = 1, end = 0, x = 0;  // this team's share [x, end) of the line
     if (p.whole) {
         x = team;
         end = 0x7fffffff;
     } else {
-        int total = 0, parts[kEvenSlack + 1] = {};  // parts of at most per + i tiles
-        auto for_rows = [&](auto f) {
+        int tiles = 0, units = 0, parts[kEvenSlack + 1] = {};  // parts of at most most + i tiles
 #pragma unroll 1
-            for (int b0 = 0; b0 < p.B; b0 += 32) {
-                int q0, T, ctx;
-                row_of(b0, q0, T, ctx);
-                f(tree_tiles(T, ctx));
-            }
-        };
-        for_rows([&](int tiles) { total += tiles; });
-        total = __reduce_add_sync(0xffffffffu, total) * p.H_kv;
-        per = max(1, cdiv(total, p.n_teams));
-        for_rows([&](int tiles) {
+        for (int b0 = 0; b0 < p.B; b0 += 32) {
+            const Row r = row_of(b0);
+            tiles += r.tiles * r.units;
+            units += r.units;
+        }
+        tiles = __reduce_add_sync(0xffffffffu, tiles);
+        const int steps = tiles + __reduce_add_sync(0xffffffffu, units) * kItemCost;
+        const int most = max(1, cdiv(tiles, p.n_teams));
+        per = max(1, cdiv(steps, p.n_teams));
+#pragma unroll 1
+        for (int b0 = 0; b0 < p.B; b0 += 32) {
+            const Row r = row_of(b0);
 #pragma unroll
-            for (int i = 0; i <= kEvenSlack; ++i) parts[i] += cdiv(tiles, per + i);
-        });
+            for (int i = 0; i <= kEvenSlack; ++i) parts[i] += cdiv(r.tiles, most + i) * r.units;
+        }
 #pragma unroll
         for (int i = kEvenSlack; i >= 0; --i)
-            if (__reduce_add_sync(0xffffffffu, parts[i]) * p.H_kv <= p.n_teams) even = per + i;
+            if (__reduce_add_sync(0xffffffffu, parts[i]) <= p.n_teams) even = most + i;
         const int64_t begin = int64_t(team) * per;
-        x = even ? team : int(min(begin, int64_t(total)));
-        end = even ? team + 1 : int(min(int64_t(total), begin + per));
+        x = even ? team : int(min(begin, int64_t(steps)));
+        end = even ? team + 1 : int(min(int64_t(steps), begin + per));
     }
     if (bad && blockIdx.x == 0) atomicOr(p.status, kStatusBadSeqlen);
     if (!p.whole && lane == 0) p.part_info[blockIdx.x] = make_int4(0, 0, 0, 0);
-    // In the line a unit is `size` steps long: its tiles, its parts, or 1.
     int before = 0;  // steps of the rows before b0
 #pragma unroll 1
     for (int b0 = 0; b0 < p.B && x < end; b0 += 32) {
-        int q0, T, ctx;
-        row_of(b0, q0, T, ctx);
-        const int tiles = tree_tiles(T, ctx);
-        const int size = p.whole ? min(tiles, 1) : even ? cdiv(tiles, even) : tiles;
-        int sum = size * p.H_kv;  // inclusive prefix sum over the lanes
+        const Row mine = row_of(b0);
+        // steps of a unit in the line: 1, its parts, or the item cost and its tiles
+        const int len = mine.tiles == 0 ? 0
+                        : p.whole       ? 1
+                        : even          ? cdiv(mine.tiles, even)
+                                        : mine.tiles + kItemCost;
+        int sum = len * mine.units;  // inclusive prefix sum over the lanes
         for (int o = 1; o < 32; o <<= 1) {
             const int y = __shfl_up_sync(0xffffffffu, sum, o);
             if (lane >= o) sum += y;
@@ -457,38 +471,39 @@ __device__ __forceinline__ void schedule_tree(const Params& p, Publisher& pub, i
 #pragma unroll 1
         while (x < end && x < before + all) {
             const int src = __ffs(__ballot_sync(0xffffffffu, before + sum > x)) - 1;
-            const int row_tiles = __shfl_sync(0xffffffffu, tiles, src);
-            const int row_size = __shfl_sync(0xffffffffu, size, src);
-            const int at = x - (before + __shfl_sync(0xffffffffu, sum, src) - row_size * p.H_kv);
-            const int i = at % row_size;  // step of the unit
+            auto of = [&](int v) { return __shfl_sync(0xffffffffu, v, src); };
+            const int tiles = of(mine.tiles), blocks = of(mine.blocks), heads = of(mine.heads);
+            const int unit = of(len);
+            const int at = x - (before + of(sum) - unit * of(mine.units));
+            const int i = at % unit;  // step of the unit
             Item w{};
             w.b = b0 + src;
-            w.kvh = at / row_size;
-            int parts;
+            w.kvh = at / unit * heads + member / blocks;
+            w.n = tiles;
+            int parts = 1;
             if (p.whole) {
-                w.n = row_tiles;
-                parts = 1;
                 x += p.n_teams;
             } else if (even) {
                 // (below 2^32: a row has less than 2^24 tiles and kTreeCtas parts)
-                w.j0 = int(unsigned(row_tiles) * unsigned(i) / unsigned(row_size));
-                w.n = int(unsigned(row_tiles) * unsigned(i + 1) / unsigned(row_size)) - w.j0;
-                parts = row_size;
+                w.j0 = int(unsigned(tiles) * unsigned(i) / unsigned(unit));
+                w.n = int(unsigned(tiles) * unsigned(i + 1) / unsigned(unit)) - w.j0;
+                parts = unit;
                 ++x;
             } else {
-                w.j0 = i;
-                w.n = min(row_tiles - i, end - x);
-                parts = (x - i + row_tiles - 1) / per - (x - i) / per + 1;
-                x += w.n;
+                const int start = x - i + kItemCost;  // of the unit's tiles in the line
+                w.j0 = max(0, i - kItemCost);
+                w.n = min(tiles, end - start) - w.j0;  // (0: the share ends in the item cost)
+                parts = (start + tiles - 1) / per - start / per + 1;
+                x += min(unit - i, end - x);
             }
-            w.q_row = w.k_row = __shfl_sync(0xffffffffu, q0, src);
-            w.T = w.n_own = __shfl_sync(0xffffffffu, T, src);
-            w.ctx = __shfl_sync(0xffffffffu, ctx, src);
-            w.c_t = row_tiles - 1;
-            w.tok0 = member * 2 * p.tok;
+            w.q_row = w.k_row = of(mine.q0);
+            w.T = w.n_own = of(mine.T);
+            w.ctx = of(mine.ctx);
+            w.c_t = tiles - 1;
+            w.tok0 = member % blocks * 2 * p.tok;
             w.n0 = w.n;
             w.n1 = w.tok0 + p.tok < w.T ? w.n : 0;
-            if (w.tok0 >= w.T) continue;
+            if (w.n <= 0 || member >= blocks * heads || w.kvh >= p.H_kv) continue;
             // slot 2c + 1 holds the first part of a unit, 2c another one
             w.dst = parts == 1 ? -1 : 2 * int(blockIdx.x) + (w.j0 == 0);
             if (parts > 1 && w.j0 == 0 && lane == 0)
