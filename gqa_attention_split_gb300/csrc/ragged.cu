@@ -203,8 +203,8 @@ struct Geo {
     static constexpr uint32_t kQOff = 0;  // two groups
     static constexpr uint32_t kRingOff = 2 * kTileBytes;
     static constexpr uint32_t kStageOff = kRingOff + kRingSlots * kTileBytes;  // 8 warps
-    static constexpr uint32_t kXchOff = kStageOff + 8 * kStageBytes;  // float4 [2][128]
-    static constexpr uint32_t kSeqOff = kXchOff + 2 * BM * 16;        // int2 [kSchedSeqs]
+    static constexpr uint32_t kXchOff = kStageOff + 8 * kStageBytes;  // float2 [2][128]
+    static constexpr uint32_t kSeqOff = kXchOff + 2 * BM * 8;         // int2 [kSchedSeqs]
     static constexpr uint32_t kItemOff = kSeqOff + kSchedSeqs * 8;
     static constexpr uint32_t kBarOff = kItemOff + kItemSlots * 64;
     static constexpr int kSmemBytes = 1024 + kBarOff + 512;
@@ -390,7 +390,7 @@ __device__ __forceinline__ void schedule_prompts(const Params& p, int2* seqs, Pu
 // "even" may take up to kEvenSlack more tiles than the line would, for the same
 // reason. A unit that is cut leaves partial results for the merge. (A batch of
 // 8 rows with contexts of 17 to 31007 and 1 to 64 drafts: 189 us without the
-// item cost and with one KV head in every unit, 153 us with them.)
+// item cost and with one KV head in every unit, 153 with them.)
 constexpr int kEvenSlack = 4;
 constexpr int kItemCost = 2;
 
@@ -521,11 +521,18 @@ __device__ __forceinline__ void schedule_tree(const Params& p, Publisher& pub, i
 // ---- softmax of one tile of scores
 
 struct RowState {
-    float m, l, lb;  // running maximum (base 2), sums of p and of bf16(p)
+    float m, l;  // running maximum (base 2), sum of p
 };
 
-// P = 2^(s - m) over the tile, written as bf16 pairs over S; returns the factor
-// that O has to be scaled by (1: left as it is).
+// P = 2^(s - m) over the tile, written as bf16 pairs over S (the operand type of
+// the P V product); returns the factor that O has to be scaled by (1: left as it
+// is). O is divided by l, the fp32 sum of the unrounded p: each p is off by half
+// a bf16 step at most, and so is O relative to sum p |v|. Dividing by the sum of
+// the rounded values, which the uniform prefill does, costs two additions for
+// every pair of keys and a tenth of the time (packed 32K 4.40 against 4.00 ms,
+// packed 8K batch 174 against 156 us) and changes O's distance from 64 bits by
+// 0 to 6% (relative 0.0017 against 0.0018 on short prompts, 0.0020 both on long
+// ones; bf16 output alone has 0.0016).
 __device__ __forceinline__ float softmax_tile(const float (&sv)[BN], RowState& st,
                                               float scale_log2, uint64_t c2, uint32_t s_addr) {
     float mm[8];
@@ -544,13 +551,7 @@ __device__ __forceinline__ float softmax_tile(const float (&sv)[BN], RowState& s
     // a row that has seen no key yet keeps m = -inf and p = 0
     const float m_sub = st.m == -INFINITY ? 0.f : st.m;
     const uint64_t n2 = f2pack(-m_sub, -m_sub);
-    uint64_t s2[4];
-    float bl[4], bh[4];
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-        s2[u] = 0ull;
-        bl[u] = bh[u] = 0.f;
-    }
+    uint64_t s2[4] = {0ull, 0ull, 0ull, 0ull};
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
         uint32_t pk[32];
@@ -561,22 +562,14 @@ __device__ __forceinline__ float softmax_tile(const float (&sv)[BN], RowState& s
             f2unpack(ffma2(f2pack(sv[c], sv[c + 1]), c2, n2), x0, x1);
             const float e0 = fast_exp2(x0), e1 = fast_exp2(x1);
             s2[i & 3] = fadd2(s2[i & 3], f2pack(e0, e1));
-            pk[i] = pack_bf16x2(e0, e1);  // P in bf16: the operand type of the P V product
-            bl[i & 3] = add_f32_bf16_lo(bl[i & 3], pk[i]);
-            bh[i & 3] = add_f32_bf16_hi(bh[i & 3], pk[i]);
+            pk[i] = pack_bf16x2(e0, e1);
         }
         tc::tmem_st32(s_addr + half * 32, pk);
     }
-    float t[8], tb[8];
+    float t[8];
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-        f2unpack(s2[u], t[2 * u], t[2 * u + 1]);
-        tb[2 * u] = bl[u];
-        tb[2 * u + 1] = bh[u];
-    }
+    for (int u = 0; u < 4; ++u) f2unpack(s2[u], t[2 * u], t[2 * u + 1]);
     st.l = st.l * corr + (((t[0] + t[1]) + (t[2] + t[3])) + ((t[4] + t[5]) + (t[6] + t[7])));
-    st.lb = st.lb * corr +
-            (((tb[0] + tb[1]) + (tb[2] + tb[3])) + ((tb[4] + tb[5]) + (tb[6] + tb[7])));
     return corr;
 }
 
@@ -1033,7 +1026,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t lane_base = tmem + (uint32_t(quad * 32) << 16);
         const uint32_t col_s = col_s_of(g), col_o = col_o_of(g);
         const uint32_t stage = smem_u32(smem + Gm::kStageOff + (g * 4 + quad) * kStageBytes);
-        float4* xch = reinterpret_cast<float4*>(smem + Gm::kXchOff);
+        float2* xch = reinterpret_cast<float2*>(smem + Gm::kXchOff);
         const uint64_t c2 = f2pack(p.scale_log2, p.scale_log2);
         bool alive = true;
         int tt = 0;              // tiles this group finished: its S phases
@@ -1095,7 +1088,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                                    : (1u << upto) - 1u);
                 }
             }
-            RowState st{-INFINITY, 0.f, 0.f};
+            RowState st{-INFINITY, 0.f};
 #pragma unroll 1
             for (int i = 0; i < ng && alive; ++i) {
                 alive = wait_all(bSFull + g, tt + i);
@@ -1161,18 +1154,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             const Item e = read_item(item_addr);
             const bool two = kAlt && uniform(e.n) > 1;
             if constexpr (kAlt) {
-                xch[g * BM + row] = make_float4(st.m, st.l, st.lb, 0.f);
+                xch[g * BM + row] = make_float2(st.m, st.l);
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(bXch));
                 alive = wait_all(bXch, xk);
                 if (!alive) break;
-                const float4 a = xch[row], b = xch[BM + row];  // group 1 without tiles: -inf, 0, 0
+                const float2 a = xch[row], b = xch[BM + row];  // group 1 without tiles: -inf, 0
                 const float m = fmaxf(a.x, b.x), ms = m == -INFINITY ? 0.f : m;
                 f0 = fast_exp2(a.x - ms);
                 f1 = fast_exp2(b.x - ms);
                 st.m = m;
                 st.l = f0 * a.y + f1 * b.y;
-                st.lb = f0 * a.z + f1 * b.z;
             }
             // (what does not need O comes before the wait for it)
             const int t = (kAlt ? e.tok0 : e.tok0 + g * p.tok) + row_tok;
@@ -1185,7 +1177,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const RowPtrs rows(
                 valid && direct ? reinterpret_cast<uint8_t*>(p.o + orow * D) : nullptr, lane);
             // l is 0 only for a row that saw no key (and NaN stays NaN)
-            const float inv = st.lb == 0.f ? 0.f : 1.f / st.lb;
+            const float inv = st.l == 0.f ? 0.f : 1.f / st.l;
             if (valid && (!kAlt || g == 0)) {
                 const float lse = st.l == 0.f ? -INFINITY : (st.m + log2f(st.l)) * kLn2;
                 if (!direct)

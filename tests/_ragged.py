@@ -1,10 +1,11 @@
 """Plain 64-bit attention over explicit visibility, with the error bound of a bf16 kernel.
 
 For each query: O = sum_j p_j v_j over the visible keys, lse = ln sum exp(scale q.k_j). A kernel
-that rounds the weights to bf16 before the product with V, normalises by the sum of the rounded
+that rounds the weights to bf16 before the product with V, normalises by the sum of the unrounded
 weights and rounds O to bf16 is off by at most (u = 2^-8, half a bf16 step)
-    |dO_c| <= (u / (1 - u) + 2 e) * sum_j p_j |v_jc - O_c| + u (|O_c| + that) + 2^-18 max|v|
-since O' - O = sum p_j d_j (v_j - O) / sum p_j (1 + d_j) with |d_j| <= u, where e bounds the fp32
+    |dO_c| <= u sum_j p_j |v_jc| + 2 e sum_j p_j |v_jc - O_c| + u (|O_c| + those) + 2^-18 max|v|
+since its O' = sum p_j (1 + d_j) v_j / sum p_j with |d_j| <= u, and relative errors e_j of the
+weights themselves move O by sum p_j e_j (v_j - O) / sum p_j (1 + e_j), where e bounds the fp32
 error of a scaled score: d products summed in fp32, each step off by at most 2^-23 of the sum of
 magnitudes (the tensor core may truncate), plus the exponential's and the exponent's own
 roundings, 2^-20 of the largest score and of 1. lse is off by at most e plus fp32 roundings.
@@ -49,7 +50,7 @@ def attend(q, k, v, visible, scale):
                 kb = slice(s0, s0 + 256)
                 spread[blk] += np.einsum("ts,tsc->tc", p[blk, kb],
                                          np.abs(V[None, kb] - O[blk, None, h]))
-        bO[:, h] = ((U / (1 - U) + 2 * e[:, None]) * spread * (1 + U) + U * np.abs(O[:, h])
+        bO[:, h] = ((U * (p @ np.abs(V)) + 2 * e[:, None] * spread) * (1 + U) + U * np.abs(O[:, h])
                     + 2.0 ** -18 * np.abs(V).max())
         bL[:, h] = e + 2.0 ** -20 * (np.abs(np.where(some, L[:, h], 0.0)) + 1.0)
     return O, L, bO, bL
