@@ -291,20 +291,45 @@ __device__ __forceinline__ void schedule_prompts(const Params& p, int2* seqs, Pu
 #pragma unroll 1
     for (int b = lane; b < p.B; b += 32) {
         const int2 s = levels(b);
-        if (b < kSchedSeqs) seqs[b] = s;
+        if (p.B <= kSchedSeqs) seqs[b] = s;
         blocks += s.y;
         if (s.y > 0) top = max(top, p.causal ? s.x + s.y - 1 : s.x);
     }
     if (bad && blockIdx.x == 0) atomicOr(p.status, kStatusBadSeqlen);
     top = __reduce_max_sync(0xffffffffu, top);
     blocks = __reduce_add_sync(0xffffffffu, blocks);
+    // More sequences than the table holds: the blocks run in the sequences'
+    // order instead, found through the block counts of `chunk` sequences each
+    // (counting through all levels for every item takes B / 32 rounds a step;
+    // 20000 sequences of 1 to 4 tokens: NEWMANY). There are many items then, so
+    // their order matters little for the balance.
+    const bool in_order = p.B > kSchedSeqs;
+    const int chunk = cdiv(p.B, kSchedSeqs);
+    int* before_chunk = reinterpret_cast<int*>(seqs);  // blocks before chunk c
+    if (in_order) {
+        __syncwarp();
+        int sum = 0;
+#pragma unroll 1
+        for (int c0 = 0; c0 < kSchedSeqs; c0 += 32) {
+            int n = 0;
+#pragma unroll 1
+            for (int b = (c0 + lane) * chunk; b < min(p.B, (c0 + lane + 1) * chunk); ++b)
+                n += levels(b).y;
+            int incl = n;
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, incl, o);
+                if (lane >= o) incl += y;
+            }
+            before_chunk[c0 + lane] = sum + incl - n;
+            sum += __shfl_sync(0xffffffffu, incl, 31);
+        }
+    }
     __syncwarp();
-    auto get = [&](int b) { return b < kSchedSeqs ? seqs[b] : levels(b); };
     auto above = [&](int l) {  // blocks on levels > l
         int c = 0;
 #pragma unroll 1
         for (int b = lane; b < p.B; b += 32) {
-            const int2 s = get(b);
+            const int2 s = seqs[b];
             c += p.causal ? clampi(s.x + s.y - 1 - l, 0, s.y) : (s.x > l ? s.y : 0);
         }
         return __reduce_add_sync(0xffffffffu, c);
@@ -323,36 +348,60 @@ __device__ __forceinline__ void schedule_prompts(const Params& p, int2* seqs, Pu
             hint = top;
             hint_group = hg;
         }
-        int lo = 0, hi = hint;  // the lowest level with at most `rank` blocks above it
-        while (lo < hi) {
-            const int mid = (lo + hi) >> 1;
-            if (above(mid) <= rank) hi = mid;
-            else lo = mid + 1;
-        }
-        hint = lo;
-        int k = rank - above(lo);  // the k-th block of this level
         int b = 0, i = 0;
+        if (in_order) {
+            int c = 0;  // the last chunk with at most `rank` blocks before it
+            for (int step = kSchedSeqs / 2; step > 0; step >>= 1)
+                if (before_chunk[c + step] <= rank) c += step;
+            int k = rank - before_chunk[c];
+            b = c * chunk;
+            for (int b0 = b;; b0 += 32) {
+                const int y = b0 + lane < min(p.B, (c + 1) * chunk) ? levels(b0 + lane).y : 0;
+                int incl = y;
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int z = __shfl_up_sync(0xffffffffu, incl, o);
+                    if (lane >= o) incl += z;
+                }
+                const unsigned hit = __ballot_sync(0xffffffffu, incl > k);
+                if (hit || b0 + 32 >= (c + 1) * chunk) {
+                    const int src = hit ? __ffs(hit) - 1 : 0;
+                    b = b0 + src;
+                    i = __shfl_sync(0xffffffffu, y - 1 - (k - (incl - y)), src);
+                    break;
+                }
+                k -= __shfl_sync(0xffffffffu, incl, 31);
+            }
+        } else {
+            int lo = 0, hi = hint;  // the lowest level with at most `rank` blocks above it
+            while (lo < hi) {
+                const int mid = (lo + hi) >> 1;
+                if (above(mid) <= rank) hi = mid;
+                else lo = mid + 1;
+            }
+            hint = lo;
+            int k = rank - above(lo);  // the k-th block of this level
 #pragma unroll 1
-        for (int b0 = 0; b0 < p.B; b0 += 32) {
-            int c = 0;
-            int2 s = make_int2(0, 0);
-            if (b0 + lane < p.B) {
-                s = get(b0 + lane);
-                c = p.causal ? (lo >= s.x && lo < s.x + s.y) : (s.x == lo ? s.y : 0);
+            for (int b0 = 0; b0 < p.B; b0 += 32) {
+                int c = 0;
+                int2 s = make_int2(0, 0);
+                if (b0 + lane < p.B) {
+                    s = seqs[b0 + lane];
+                    c = p.causal ? (lo >= s.x && lo < s.x + s.y) : (s.x == lo ? s.y : 0);
+                }
+                int sum = c;
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int x = __shfl_up_sync(0xffffffffu, sum, o);
+                    if (lane >= o) sum += x;
+                }
+                const unsigned hit = __ballot_sync(0xffffffffu, sum > k);
+                if (hit) {
+                    const int src = __ffs(hit) - 1;
+                    b = b0 + src;
+                    i = __shfl_sync(0xffffffffu, p.causal ? lo - s.x : k - (sum - c), src);
+                    break;
+                }
+                k -= __shfl_sync(0xffffffffu, sum, 31);
             }
-            int sum = c;
-            for (int o = 1; o < 32; o <<= 1) {
-                const int x = __shfl_up_sync(0xffffffffu, sum, o);
-                if (lane >= o) sum += x;
-            }
-            const unsigned hit = __ballot_sync(0xffffffffu, sum > k);
-            if (hit) {
-                const int src = __ffs(hit) - 1;
-                b = b0 + src;
-                i = __shfl_sync(0xffffffffu, p.causal ? lo - s.x : k - (sum - c), src);
-                break;
-            }
-            k -= __shfl_sync(0xffffffffu, sum, 31);
         }
         Item w{};
         w.kvh = hg * p.head_group + int(in_group % heads);
@@ -1519,34 +1568,87 @@ struct AppendParams {
     int B, H_kv, d, S_max, total, total_new;
 };
 
-// One warp per entry: K and V of one token, every head.
-__global__ void __launch_bounds__(128) append_kernel(const AppendParams p) {
+// One warp per entry: K and V of one token, every head, four 16-byte pieces of
+// each a lane at a time with all their loads in flight. A copy, bound by HBM (a
+// packed step of 7205 tokens, 59 MB: NEWAPP us against 8.7 at the copy rate) or,
+// for a few tokens, by the chain launch - prefix sums - start - copy (4.4 us).
+constexpr int kAppendWarps = 8;
+
+template <int D>
+__global__ void __launch_bounds__(kAppendWarps * 32) append_kernel(const AppendParams p) {
+    grid_launch_dependents();
+    grid_wait_primary();
     const int lane = threadIdx.x & 31;
-    const int e = blockIdx.x * 4 + (threadIdx.x >> 5);
-    if (e >= p.total) return;
+    const int e = blockIdx.x * kAppendWarps + (threadIdx.x >> 5);
     bool bad = false;
-    int b = 0, first = 0, n = 0;
-    for (; b < p.B; ++b) {
-        row_range(p.cu, p.B, p.total, b, first, n, bad);
-        if (e >= first && e < first + n) break;
+    if (blockIdx.x == 0 && p.cu) {  // bad prefix sums are reported by the first block
+#pragma unroll 1
+        for (int b = threadIdx.x; b < p.B; b += blockDim.x) {
+            int first, n;
+            row_range(p.cu, p.B, p.total, b, first, n, bad);
+        }
     }
-    if (bad && lane == 0) atomicOr(p.status, kStatusBadSeqlen);
-    if (b == p.B) return;
-    const int64_t slot = int64_t(p.starts[b]) + (e - first);
-    const int src = p.index ? p.index[e] : e;
-    if (slot < 0 || slot >= p.S_max || src < 0 || src >= p.total_new) {
-        if (lane == 0) atomicOr(p.status, kStatusBadSeqlen);
-        return;
+    // the entry's row: the last b with cu[b] <= e, by 32 probes at a time
+    int b = 0, i = 0;
+    bool mine = e < p.total;
+    if (!p.cu) {
+        const int per = p.total / p.B;
+        if (mine) {
+            b = e / per;
+            i = e - b * per;
+        }
+    } else if (mine) {
+        int lo = 0, hi = p.B;  // cu[lo] <= e (or lo = 0), the answer below hi
+        while (hi - lo > 1) {
+            const int step = cdiv(hi - lo, 32);
+            const int at = lo + lane * step;
+            const unsigned le = __ballot_sync(0xffffffffu, at < hi && p.cu[at] <= e);
+            const int k = le ? 31 - __clz(le) : 0;
+            lo += k * step;
+            hi = min(hi, lo + step);
+        }
+        b = lo;
+        int first, n;
+        bool dummy = false;
+        row_range(p.cu, p.B, p.total, b, first, n, dummy);
+        i = e - first;
+        mine = i >= 0 && i < n;  // (else it lies before the first or behind the last row)
     }
-    const int per = p.d / 8;
-    for (int i = lane; i < p.H_kv * per; i += 32) {
-        const int h = i / per, c = i % per;
-        const size_t dst = ((size_t(b) * p.H_kv + h) * p.S_max + slot) * p.d + c * 8;
-        *reinterpret_cast<uint4*>(p.kc + dst) =
-            *reinterpret_cast<const uint4*>(p.k + src * p.k_st + h * p.k_sh + c * 8);
-        *reinterpret_cast<uint4*>(p.vc + dst) =
-            *reinterpret_cast<const uint4*>(p.v + src * p.v_st + h * p.v_sh + c * 8);
+    if (mine) {
+        const int64_t slot = int64_t(p.starts[b]) + i;
+        const int src = p.index ? p.index[e] : e;
+        if (slot < 0 || slot >= p.S_max || src < 0 || src >= p.total_new) {
+            bad = true;
+        } else {
+            constexpr int kPieces = D / 8, kBatch = 4;
+            const uint16_t* k_src = p.k + src * p.k_st;
+            const uint16_t* v_src = p.v + src * p.v_st;
+            const size_t base = (size_t(b) * p.H_kv * p.S_max + slot) * D;
+            const size_t head = size_t(p.S_max) * D;
+            const int n = p.H_kv * kPieces;
+#pragma unroll 1
+            for (int v0 = lane; v0 < n; v0 += 32 * kBatch) {
+                uint4 kx[kBatch], vx[kBatch];
+#pragma unroll
+                for (int u = 0; u < kBatch; ++u) {
+                    const int v = v0 + 32 * u;
+                    if (v >= n) break;
+                    const int h = v / kPieces, c = v % kPieces * 8;
+                    kx[u] = *reinterpret_cast<const uint4*>(k_src + h * p.k_sh + c);
+                    vx[u] = *reinterpret_cast<const uint4*>(v_src + h * p.v_sh + c);
+                }
+#pragma unroll
+                for (int u = 0; u < kBatch; ++u) {
+                    const int v = v0 + 32 * u;
+                    if (v >= n) break;
+                    const size_t dst = base + v / kPieces * head + v % kPieces * 8;
+                    *reinterpret_cast<uint4*>(p.kc + dst) = kx[u];
+                    *reinterpret_cast<uint4*>(p.vc + dst) = vx[u];
+                }
+            }
+        }
     }
+    if (bad) atomicOr(p.status, kStatusBadSeqlen);
 }
 
 }  // namespace ragged
@@ -1726,6 +1828,9 @@ extern "C" int gqa_attn_cache_append(uint16_t* k_cache, uint16_t* v_cache, const
     const AppendParams p{k_cache, v_cache, k_new, v_new, cu_seqlens, starts, index, status,
                          k_stride_t, k_stride_h, v_stride_t, v_stride_h, B, H_kv, d, S_max,
                          total, total_new};
-    append_kernel<<<unsigned((total + 3) / 4), 128, 0, stream>>>(p);
-    return cudaGetLastError() == cudaSuccess ? GQA_OK : GQA_ERR_CUDA;
+    return launch(d == 128 ? append_kernel<128> : append_kernel<64>,
+                  unsigned((total + kAppendWarps - 1) / kAppendWarps), kAppendWarps * 32, 0,
+                  stream, p) == cudaSuccess
+               ? GQA_OK
+               : GQA_ERR_CUDA;
 }

@@ -97,6 +97,26 @@ def test_packed_many_sequences():
     _check_packed(o, lse, q, k, v, lens, lens, True, 1 / 8)
 
 
+def test_packed_more_sequences_than_the_schedule_table_holds_twice():
+    rng = np.random.RandomState(4)
+    lens = list(rng.randint(0, 5, 2100)) + [300, 129] + [0] * 50
+    q, k, v = _packed_inputs(lens, lens, 3, 1, 64, 10)
+    for causal in (True, False):
+        o, lse = api.prefill_packed(q, k, v, _cu(lens), causal=causal)
+        api.check()
+        _check_packed(o, lse, q, k, v, lens, lens, causal, 1 / 8)
+
+
+@pytest.mark.parametrize("H_q,H_kv", [(32, 1), (100, 1), (128, 1), (18, 2)])
+def test_packed_large_groups_of_heads(H_q, H_kv):
+    # 100 heads: one token to a block; 9 heads: 14 tokens, two rows of a block unused
+    lens = [7, 1, 150]
+    q, k, v = _packed_inputs(lens, lens, H_q, H_kv, 128, 12)
+    o, lse = api.prefill_packed(q, k, v, _cu(lens))
+    api.check()
+    _check_packed(o, lse, q, k, v, lens, lens, True, 1 / math.sqrt(128))
+
+
 def test_packed_persistent_items():
     # several work items per CTA, of very different lengths
     lens = [1500, 3, 260, 900, 31, 1100]
@@ -458,6 +478,68 @@ def test_append_bad_slots_and_tokens_are_left_out_and_reported(starts, index):
             if 0 <= s < 10 and 0 <= t < 4:
                 want[b, :, s] = kn[t]
     assert torch.equal(kc, want)
+
+
+def test_append_many_rows():
+    # more rows than the search looks at in one step, empty ones among them
+    rng = np.random.RandomState(6)
+    counts = rng.randint(0, 3, 1200)
+    n = int(counts.sum())
+    kc = torch.zeros(1200, 1, 4, 64, dtype=torch.bfloat16, device="cuda")
+    vc = torch.zeros_like(kc)
+    kn, vn = _randn(1, n + 4, 1, 64), _randn(2, n + 4, 1, 64)
+    starts = rng.randint(0, 3, 1200).astype(np.int32)
+    cu = _cu(counts) + 2  # two entries in front and two behind belong to nobody
+    wk, e = torch.zeros_like(kc), 2
+    for b in range(1200):
+        for i in range(counts[b]):
+            wk[b, :, starts[b] + i] = kn[e]
+            e += 1
+    api.cache_append(kc, vc, kn, vn, torch.from_numpy(starts).cuda(), cu_seqlens=cu)
+    api.check()
+    assert torch.equal(kc, wk)
+
+
+@pytest.mark.parametrize("cu", [[0, 3, 2, 4], [-1, 1, 2, 4], [0, 1, 2, 9]])
+def test_append_bad_prefix_sums_are_reported(cu):
+    kc = torch.zeros(3, 1, 10, 64, dtype=torch.bfloat16, device="cuda")
+    vc = torch.zeros_like(kc)
+    kn, vn = _randn(1, 4, 1, 64), _randn(2, 4, 1, 64)
+    zero = torch.zeros(3, dtype=torch.int32, device="cuda")
+    api.cache_append(kc, vc, kn, vn, zero, cu_seqlens=torch.tensor(cu, dtype=torch.int32,
+                                                                    device="cuda"))
+    with pytest.raises(api.GqaError) as e:
+        api.check()
+    assert e.value.code == api.GQA_ERR_DEVICE_BAD_INPUT
+
+
+# ------------------------------------------------------------------ failure reporting
+
+
+@pytest.mark.parametrize("call", ["packed", "tree", "tree_wide"])
+def test_timeout_is_reported_and_the_next_call_is_correct(call):
+    # the first block withholds a copy: its waits run out, nothing faults
+    ctx, drafts, H_q = [700, 90], ([9, 3] if call != "tree_wide" else [60, 40]), 8
+    T = max(drafts)
+    q, kn, vn, kc, vc, cl = _tree_inputs(ctx, drafts, 1024, H_q, 1, 128, 97)
+
+    def run():
+        if call == "packed":
+            return api.prefill_packed(q, kn, vn, _cu(drafts))
+        return api.decode_tree(q, kn, vn, kc, vc, cl, cu_seqlens=_cu(drafts), max_tokens=T)
+
+    api.check()
+    assert api.gqa_attn_debug_inject_timeout(1) == api.GQA_OK
+    run()
+    with pytest.raises(api.GqaError) as e:
+        api.check()
+    assert e.value.code == api.GQA_ERR_DEVICE_TIMEOUT
+    o, lse = run()
+    api.check()
+    if call == "packed":
+        _check_packed(o, lse, q, kn, vn, drafts, drafts, True, 1 / math.sqrt(128))
+    else:
+        _check_tree(o, lse, q, kn, vn, kc, vc, ctx, drafts, None, 1 / math.sqrt(128))
 
 
 # ----------------------------------------------------------------------- together
