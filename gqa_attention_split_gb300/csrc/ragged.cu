@@ -19,10 +19,28 @@
 //
 // Roles of a CTA (one per SM, persistent): warp 0 TMA, warp 1 issues every
 // tcgen05.mma, warp 2 finds the work items from the prefix sums on the device
-// and passes them on through a ring in shared memory, warp 3 repairs V tiles
-// whose keys not every row may see, two warpgroups run the online softmax,
-// one query row per thread. S and O live in tensor memory, P is written over
-// its S columns and read from there by the P V product.
+// (the host never waits for them) and passes them on through a ring in shared
+// memory, warp 3 repairs V tiles whose keys not every row may see, two
+// warpgroups run the online softmax, one query row per thread. S and O live in
+// tensor memory, P is written over its S columns and read from there by the P V
+// product.
+//
+// What bounds it. A group's tile is a chain: S ready, softmax (about 1700
+// cycles), P V and the next S (1024 cycles of tensor work at d = 128), hand-over
+// (about 200). Two groups take turns at the tensor cores, so a pair of tiles
+// takes about 2870 cycles where the products alone would take 2048: packed 32K
+// tokens 1.50-1.53 PFLOP/s, 0.80-0.82 of the measured bf16 rate. A long context
+// under few queries is bound by HBM, a short one by latencies: launch 1 us,
+// prefix sums to first tile 4, per tile 1.5, end of an item 2, merge 4.
+// Measured and slower on the same box (packed 8K batch / packed 32K, against
+// 174 / 4300 us at that point): steps of 64 keys with two S buffers per group
+// (208 / 5930: S products of N = 64 run at 0.6 of the rate); one S buffer for
+// both groups with P in columns of its own (194 / 4750: the next S is not ready
+// in time); P handed over in halves (191 / 4600); a worker per group with its own
+// items and K/V ring, as two CTAs per SM (230 / 5110: their products interleave
+// and both wait) or in one CTA with a lock around the issue (203 / 4600); the end
+// of an item behind the next item's first tile (188 / 4350); O through TMA boxes
+// (172 / 4300).
 
 #include <cuda_runtime.h>
 #include <math.h>
@@ -48,7 +66,10 @@ constexpr int kRingSlots = 4;        // K/V tiles in flight
 constexpr int kItemSlots = 4;        // work items known ahead
 constexpr int kSchedSeqs = 1024;     // sequences whose schedule is kept in shared memory
 constexpr int kTreeCtas = 152;       // most CTAs of a decode_tree launch (workspace size)
-constexpr int kWholeTiles = 9;       // decode_tree: rows of at most this many tiles are not cut
+// decode_tree: rows of at most this many tiles (a cache of 512 slots) are not cut, which saves
+// the merge (8 units of 2 tiles 8.8 us against 11.2 cut, 4 tiles 9.9 against 10.2, 9 tiles 15.6
+// against 10.6)
+constexpr int kWholeTiles = 5;
 constexpr uint32_t kBoxBytes = BM * 128;       // 128 rows x 64 bf16
 constexpr uint32_t kStageBytes = 32 * 64;      // a warp's output stage: 32 rows x 64 B
 constexpr uint32_t kTmemCols = 512;            // S_0, S_1, O_0, O_1
@@ -58,7 +79,9 @@ constexpr float kRescaleThreshold = 8.f;
 // kPrompts: items are blocks of 2 * tok tokens of a sequence, all of its keys.
 // kTreePair: items are blocks of 2 * tok drafted tokens, a range of the keys.
 // kTreeAlt: all drafted tokens of a row fit in one group; the two softmax
-// groups take alternate K/V tiles and are merged in the epilogue.
+// groups take alternate K/V tiles and are merged in the epilogue (28/4 heads,
+// 5 drafts, contexts of 64 to 9100: 18.5 us against 19.7 as kTreePair, whose
+// second group would be empty).
 enum Mode { kPrompts, kTreePair, kTreeAlt };
 
 struct Params {
@@ -76,7 +99,6 @@ struct Params {
     int64_t v_st, v_sh;
     int B, H_q, H_kv, G, total_q, total_k, S_max, max_tokens, mask_words, causal;
     int tok;          // tokens of a group
-    int head_group;   // kPrompts: KV heads whose items are scheduled together
     int team;         // decode_tree: CTAs that share a range of keys, one per token block
     int n_teams, part_rows;
     int whole;        // decode_tree: no (row, KV head) is cut
@@ -274,8 +296,10 @@ struct Publisher {
 // blocks are numbered by levels (key position of the block / block length) and
 // the launch runs the levels from the highest down over all sequences, in
 // snake order over the CTAs: heaviest first, found from the prefix sums by
-// counting, without sorting, so that every CTA finds its own items alone.
-// KV heads are taken in groups whose K and V fit in L2 together.
+// counting, without sorting, so that every CTA finds its own items alone. All KV
+// heads run together even where their K and V are larger than L2: one group of
+// heads after another, each within L2, ends on heavy items several times (one
+// sequence of 64K tokens, 16/8 heads: 11.9 ms in groups, 10.8 this way).
 __device__ __forceinline__ void schedule_prompts(const Params& p, int2* seqs, Publisher& pub,
                                                  int lane) {
     const int block = 2 * p.tok;
@@ -287,43 +311,42 @@ __device__ __forceinline__ void schedule_prompts(const Params& p, int2* seqs, Pu
         else n = T;
         return make_int2((p.causal ? max(n - T, 0) : n) / block, cdiv(T, block));
     };
-    int top = 0, blocks = 0;
-#pragma unroll 1
-    for (int b = lane; b < p.B; b += 32) {
-        const int2 s = levels(b);
-        if (p.B <= kSchedSeqs) seqs[b] = s;
-        blocks += s.y;
-        if (s.y > 0) top = max(top, p.causal ? s.x + s.y - 1 : s.x);
-    }
-    if (bad && blockIdx.x == 0) atomicOr(p.status, kStatusBadSeqlen);
-    top = __reduce_max_sync(0xffffffffu, top);
-    blocks = __reduce_add_sync(0xffffffffu, blocks);
     // More sequences than the table holds: the blocks run in the sequences'
     // order instead, found through the block counts of `chunk` sequences each
     // (counting through all levels for every item takes B / 32 rounds a step;
-    // 20000 sequences of 1 to 4 tokens: NEWMANY). There are many items then, so
-    // their order matters little for the balance.
+    // 20000 sequences of 1 to 4 tokens: 171 ms that way, 2.8 this way). There are
+    // many items then, so their order matters little for the balance.
     const bool in_order = p.B > kSchedSeqs;
     const int chunk = cdiv(p.B, kSchedSeqs);
     int* before_chunk = reinterpret_cast<int*>(seqs);  // blocks before chunk c
+    int top = 0, blocks = 0;
     if (in_order) {
-        __syncwarp();
-        int sum = 0;
 #pragma unroll 1
         for (int c0 = 0; c0 < kSchedSeqs; c0 += 32) {
             int n = 0;
-#pragma unroll 1
-            for (int b = (c0 + lane) * chunk; b < min(p.B, (c0 + lane + 1) * chunk); ++b)
-                n += levels(b).y;
+            const int first = min(p.B, (c0 + lane) * chunk);
+#pragma unroll 4
+            for (int b = first; b < min(p.B, first + chunk); ++b) n += levels(b).y;
             int incl = n;
             for (int o = 1; o < 32; o <<= 1) {
                 const int y = __shfl_up_sync(0xffffffffu, incl, o);
                 if (lane >= o) incl += y;
             }
-            before_chunk[c0 + lane] = sum + incl - n;
-            sum += __shfl_sync(0xffffffffu, incl, 31);
+            before_chunk[c0 + lane] = blocks + incl - n;
+            blocks += __shfl_sync(0xffffffffu, incl, 31);
         }
+    } else {
+#pragma unroll 1
+        for (int b = lane; b < p.B; b += 32) {
+            const int2 s = levels(b);
+            seqs[b] = s;
+            blocks += s.y;
+            if (s.y > 0) top = max(top, p.causal ? s.x + s.y - 1 : s.x);
+        }
+        top = __reduce_max_sync(0xffffffffu, top);
+        blocks = __reduce_add_sync(0xffffffffu, blocks);
     }
+    if (bad && blockIdx.x == 0) atomicOr(p.status, kStatusBadSeqlen);
     __syncwarp();
     auto above = [&](int l) {  // blocks on levels > l
         int c = 0;
@@ -336,18 +359,11 @@ __device__ __forceinline__ void schedule_prompts(const Params& p, int2* seqs, Pu
     };
     const int64_t total = int64_t(blocks) * p.H_kv;
     const int ctas = gridDim.x;
-    int hint = top, hint_group = 0;
+    int hint = top;
     for (int it = 0;; ++it) {
         const int64_t R = int64_t(it) * ctas + ((it & 1) ? ctas - 1 - int(blockIdx.x) : blockIdx.x);
         if (R >= total) break;
-        const int64_t per_group = int64_t(blocks) * p.head_group;
-        const int hg = int(R / per_group), heads = min(p.head_group, p.H_kv - hg * p.head_group);
-        const int64_t in_group = R - hg * per_group;
-        const int rank = int(in_group / heads);
-        if (hg != hint_group) {
-            hint = top;
-            hint_group = hg;
-        }
+        const int rank = int(R / p.H_kv);  // of the block, whose KV heads follow one another
         int b = 0, i = 0;
         if (in_order) {
             int c = 0;  // the last chunk with at most `rank` blocks before it
@@ -404,7 +420,7 @@ __device__ __forceinline__ void schedule_prompts(const Params& p, int2* seqs, Pu
             }
         }
         Item w{};
-        w.kvh = hg * p.head_group + int(in_group % heads);
+        w.kvh = int(R % p.H_kv);
         w.b = b;
         w.dst = -1;
         row_range(p.cu_q, p.B, p.total_q, b, w.q_row, w.T, bad);
@@ -429,18 +445,16 @@ __device__ __forceinline__ void schedule_prompts(const Params& p, int2* seqs, Pu
 // for all but one), and where a row has fewer blocks, several KV heads. Such a
 // set of KV heads is a unit. How the units are cut into the teams' shares:
 //  - whole: not at all, unit u goes to team u mod n_teams (short caches);
-//  - even: every unit into equal parts of at most `even` tiles, one part per
-//    team, when that many parts exist;
+//  - even: every unit into equal parts of at most `even` tiles, the tiles of all
+//    units over the teams, when there are no more parts than teams: one part each;
 //  - else all units in one line, cut every `per` steps: however ragged the
 //    contexts are, every team streams the same number of keys, at the price of
 //    a second and third item where a share crosses into the next unit. A unit
 //    is its tiles long and kItemCost steps before them, about what an item's
 //    first loads and its end cost.
-// "even" may take up to kEvenSlack more tiles than the line would, for the same
-// reason. A unit that is cut leaves partial results for the merge. (A batch of
+// A unit that is cut leaves partial results for the merge. (A batch of
 // 8 rows with contexts of 17 to 31007 and 1 to 64 drafts: 189 us without the
 // item cost and with one KV head in every unit, 153 with them.)
-constexpr int kEvenSlack = 4;
 constexpr int kItemCost = 2;
 
 // The CTA that holds the first part of a block of a unit describes it for the
@@ -476,7 +490,7 @@ __device__ __forceinline__ void schedule_tree(const Params& p, Publisher& pub, i
         x = team;
         end = 0x7fffffff;
     } else {
-        int tiles = 0, units = 0, parts[kEvenSlack + 1] = {};  // parts of at most most + i tiles
+        int tiles = 0, units = 0, parts = 0;
 #pragma unroll 1
         for (int b0 = 0; b0 < p.B; b0 += 32) {
             const Row r = row_of(b0);
@@ -490,12 +504,9 @@ __device__ __forceinline__ void schedule_tree(const Params& p, Publisher& pub, i
 #pragma unroll 1
         for (int b0 = 0; b0 < p.B; b0 += 32) {
             const Row r = row_of(b0);
-#pragma unroll
-            for (int i = 0; i <= kEvenSlack; ++i) parts[i] += cdiv(r.tiles, most + i) * r.units;
+            parts += cdiv(r.tiles, most) * r.units;
         }
-#pragma unroll
-        for (int i = kEvenSlack; i >= 0; --i)
-            if (__reduce_add_sync(0xffffffffu, parts[i]) <= p.n_teams) even = most + i;
+        if (__reduce_add_sync(0xffffffffu, parts) <= p.n_teams) even = most;
         const int64_t begin = int64_t(team) * per;
         x = even ? team : int(min(begin, int64_t(steps)));
         end = even ? team + 1 : int(min(int64_t(steps), begin + per));
@@ -1570,8 +1581,8 @@ struct AppendParams {
 
 // One warp per entry: K and V of one token, every head, four 16-byte pieces of
 // each a lane at a time with all their loads in flight. A copy, bound by HBM (a
-// packed step of 7205 tokens, 59 MB: NEWAPP us against 8.7 at the copy rate) or,
-// for a few tokens, by the chain launch - prefix sums - start - copy (4.4 us).
+// packed step of 7205 tokens, 59 MB: 11.5 us against 8.7 at the copy rate) or,
+// for a few tokens, by the chain launch, prefix sums, start, copy (2.7 us in a graph).
 constexpr int kAppendWarps = 8;
 
 template <int D>
@@ -1692,11 +1703,6 @@ extern "C" int gqa_attn_prefill_packed(const uint16_t* q, const uint16_t* k, con
     p.tok = BM / p.G;
     p.scale_log2 = scale * kLog2e;
     p.inject_timeout = take_injected_timeout() ? 1 : 0;
-    // KV heads whose K and V together fit in the L2 budget run at the same time
-    const int64_t head_bytes = int64_t(total_k) * d * 4;
-    p.head_group = int(head_bytes * H_kv <= kPrefillL2Budget
-                           ? H_kv
-                           : kPrefillL2Budget / head_bytes > 1 ? kPrefillL2Budget / head_bytes : 1);
     // at most this many blocks, however the tokens are spread over the rows
     const int64_t blocks = int64_t(total_q) / (2 * p.tok) + (B < total_q ? B : total_q);
     const int ctas = int(blocks * H_kv < sms ? blocks * H_kv : sms);
@@ -1729,8 +1735,7 @@ extern "C" int gqa_attn_decode_tree(
     const int rc = check_common(q, k_new, v_new, o, lse, B, H_q, H_kv, d, scale);
     if (rc != GQA_OK) return rc;
     const bool empty = B == 0 || total == 0;  // nothing to do: the tensors may be null
-    if ((!empty && (!q || !k_new || !v_new || !k_cache || !v_cache || !o || !context_lens ||
-                    !workspace)) ||
+    if ((!empty && (!q || !k_new || !v_new || !k_cache || !v_cache || !o || !context_lens)) ||
         total < 0 || S_max < 1 || max_tokens < 1 || (B > 0 && !cu_seqlens && total % B != 0) ||
         (B > 0 && !cu_seqlens && total / B > max_tokens) ||
         (tree_mask && int64_t(mask_words) * 32 < max_tokens))
@@ -1747,7 +1752,7 @@ extern "C" int gqa_attn_decode_tree(
         ((reinterpret_cast<uintptr_t>(cu_seqlens) | reinterpret_cast<uintptr_t>(context_lens) |
           reinterpret_cast<uintptr_t>(tree_mask)) & 3u))
         return GQA_ERR_MISALIGNED;
-    if (!empty && ((reinterpret_cast<uintptr_t>(workspace) & 255u) ||
+    if (!empty && (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) ||
         workspace_bytes < gqa_attn_decode_tree_workspace_size(H_q, H_kv, d, max_tokens)))
         return GQA_ERR_WORKSPACE;
     if (empty) return GQA_OK;

@@ -390,7 +390,8 @@ GQA_API int gqa_attn_prefill_packed(const uint16_t* q, const uint16_t* k, const 
  *                  gqa_attn_decode_tree_workspace_size() bytes. It holds no
  *                  state between calls; calls that overlap on the GPU must not
  *                  share one.
- * H_q / H_kv <= 16. The result does not depend on the other rows. */
+ * H_q / H_kv <= 16. The same inputs give the same bits; where a row's keys are
+ * cut for the CTAs, and so its last bits, depends on the other rows' lengths. */
 GQA_API int gqa_attn_decode_tree(const uint16_t* q, const uint16_t* k_new,
                                  const uint16_t* v_new, const uint16_t* k_cache,
                                  const uint16_t* v_cache, uint16_t* o, float* lse,

@@ -392,7 +392,7 @@ def test_tree_bad_context_is_clamped_and_reported(ctx):
     _check_tree(o, lse, q, kn, vn, kc, vc, [min(64, max(0, c)) for c in ctx], drafts, None, 1 / 8)
 
 
-def test_tree_does_not_depend_on_the_other_rows():
+def test_tree_gives_the_same_bits_every_time():
     ctx, drafts = [1500, 90, 4000], [17, 40, 3]
     q, kn, vn, kc, vc, cl = _tree_inputs(ctx, drafts, 4096, 16, 2, 128, 37)
     o, lse = api.decode_tree(q, kn, vn, kc, vc, cl, cu_seqlens=_cu(drafts), max_tokens=40)

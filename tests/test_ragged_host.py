@@ -68,7 +68,7 @@ def test_prefill_packed_refuses(kw, code):
 
 @pytest.mark.parametrize("kw,code", [
     (dict(q=None), INVALID), (dict(k_new=None), INVALID), (dict(v_cache=None), INVALID),
-    (dict(context_lens=None), INVALID), (dict(workspace=None), INVALID), (dict(S_max=0), INVALID),
+    (dict(context_lens=None), INVALID), (dict(workspace=None), api.GQA_ERR_WORKSPACE), (dict(S_max=0), INVALID),
     (dict(max_tokens=0), INVALID), (dict(max_tokens=129, mask_words=5), UNSUPPORTED),
     (dict(max_tokens=33), INVALID), (dict(mask_words=0), INVALID), (dict(mask_words=-1), INVALID),
     (dict(cu_seqlens=None, total=11), INVALID), (dict(cu_seqlens=None, total=18), INVALID),
