@@ -749,6 +749,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       if (warp == 0) {
         // ------------------------------------------------------ TMA producer
+        // A context streams through L2 once (for all members of a team at the same
+        // time): it leaves room for what is read again, code and partial results
+        // among it.
+        const uint64_t once = l2_policy_evict_first();
         int r = 0, q_loads = 0;  // ring items and Q loads before this item
         int issued = 0;          // ring items this lane issued
         bool withheld = false;
@@ -786,8 +790,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     mbar_arrive_expect_tx(bar(bSlotFull + s), kTileBytes);
                     for (int hh = 0; hh < Gm::kBoxes; ++hh) {
                         if (kTree && jj < w.c_t)
-                            tma_load(dst + hh * kBoxBytes, (i & 1) ? &tmap_vc : &tmap_kc, hh * 64,
-                                     jj * BN, w.b * p.H_kv + w.kvh, bar(bSlotFull + s));
+                            tma_load_3d(dst + hh * kBoxBytes, (i & 1) ? &tmap_vc : &tmap_kc,
+                                        hh * 64, jj * BN, w.b * p.H_kv + w.kvh,
+                                        bar(bSlotFull + s), once);
                         else
                             tma_load(dst + hh * kBoxBytes, (i & 1) ? &tmap_v : &tmap_k, hh * 64,
                                      w.k_row + (jj - w.c_t) * BN, w.kvh, bar(bSlotFull + s));
@@ -1340,16 +1345,20 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // Folds the partial results of every unit that was cut, in key order:
 //   lse = ln sum_i exp(lse_i),  O = sum_i exp(lse_i - lse) O_i.
-// A task is 32 rows (one per lane) x 32 columns of one unit's token block; of
-// the 8 warps, two take 16 columns each and four a quarter of the parts each,
-// kMergeBatch at a time: bound by the loads' latency, so a unit cut into up to
-// 20 parts is read with every load in flight at once.
+// A warp takes 32 rows (one per lane) x 16 columns and kMergeBatch parts at a
+// time with all their loads in flight. A unit cut into no more parts than that is
+// merged by the 8 warps of a block for all columns at once; of more parts, two
+// warps take 16 columns each and four a quarter of the parts each. Bound by the
+// loads' latency (26 drafts on 8K tokens, 8 units in 17 parts, 14 MB: 3 us; a
+// batch of 8 trees in 2 to 4 parts, 23 MB: 140 us in all with every unit merged the
+// second way, 136 like this).
 constexpr int kMergeThreads = 256;
-constexpr int kMergeBatch = 5;
+constexpr int kMergeBatch = 4;
 
 template <int D>
-__global__ void __launch_bounds__(kMergeThreads) merge_kernel(const Params p) {
+__global__ void __launch_bounds__(kMergeThreads, 2) merge_kernel(const Params p) {
     __shared__ int list[kTreeCtas];       // CTAs that begin a unit that was cut
+    __shared__ int4 infos[kTreeCtas];     // their part_info
     __shared__ int counts[kMergeThreads / 32];
     __shared__ float4 acc_s[kMergeThreads / 32][5][32];  // per warp: 4 x 4 columns; maximum, sum
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -1357,7 +1366,9 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const Params p) {
     grid_wait_primary();
     const int ctas = p.n_teams * p.team;
     static_assert(kTreeCtas <= kMergeThreads, "one thread per CTA of the launch");
-    const bool cut = int(threadIdx.x) < ctas && p.part_info[threadIdx.x].w > 0;
+    const int4 mine_info =
+        int(threadIdx.x) < ctas ? p.part_info[threadIdx.x] : make_int4(0, 0, 0, 0);
+    const bool cut = mine_info.w > 0;
     const unsigned votes = __ballot_sync(0xffffffffu, cut);
     if (lane == 0) counts[warp] = __popc(votes);
     __syncthreads();
@@ -1366,19 +1377,25 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const Params p) {
         if (i < warp) mine += counts[i];
         n += counts[i];
     }
-    if (cut) list[mine] = threadIdx.x;
+    if (cut) {
+        list[mine] = threadIdx.x;
+        infos[mine] = mine_info;
+    }
     __syncthreads();
     const int chunks = cdiv(p.part_rows, 32);
     constexpr int kPartWarps = kMergeThreads / 64;
     const int col_warp = warp & 1, part_warp = warp >> 1;
     for (int task = blockIdx.x; task < n * chunks * (D / 32); task += gridDim.x) {
-        const int c = list[task / (chunks * (D / 32))];
-        const int chunk = task / (D / 32) % chunks;
-        const int col4 = (task % (D / 32)) * 8 + col_warp * 4;  // first group of 4 columns
-        const int4 info = p.part_info[c];
+        const int nth = task / (chunks * (D / 32)), c = list[nth];
+        const int chunk = task / (D / 32) % chunks, quarter = task % (D / 32);
+        const int4 info = infos[nth];
         const int r = chunk * 32 + lane, parts = info.w;
-        if (chunk * 32 >= info.y) continue;  // (the same for the whole block)
-        const bool valid = r < info.y;
+        // (these are the same for the whole block)
+        const bool few = parts <= kMergeBatch;
+        if (chunk * 32 >= info.y || (few && quarter > 0)) continue;
+        // first group of 4 columns
+        const int col4 = few ? warp * 4 : quarter * 8 + col_warp * 4;
+        const bool valid = r < info.y && col4 < D / 4;
         // part i is that of CTA c + i * team: slot 2c + 1 for the first, 2c for the others
         auto slot = [&](int i) { return size_t(2 * (c + i * p.team) + (i == 0)); };
         float mx = -INFINITY, sum = 0.f;
@@ -1408,12 +1425,13 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const Params p) {
         };
 #pragma unroll
         for (int h = 0; h < 4; ++h) acc[h] = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int i0 = part_warp; i0 < parts; i0 += kPartWarps * kMergeBatch) {
+        const int step = few ? 1 : kPartWarps;
+        for (int i0 = few ? 0 : part_warp; i0 < parts; i0 += step * kMergeBatch) {
             float lse[kMergeBatch];
             float4 v[kMergeBatch][4];
 #pragma unroll
             for (int u = 0; u < kMergeBatch; ++u) {
-                const int i = i0 + u * kPartWarps;
+                const int i = i0 + u * step;
                 lse[u] = -INFINITY;
                 if (i < parts && valid) {
                     lse[u] = p.part_lse[slot(i) * p.part_rows + r];
@@ -1439,24 +1457,30 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const Params p) {
                 add(w, v[u]);
             }
         }
+        if (!few) {
 #pragma unroll
-        for (int h = 0; h < 4; ++h) acc_s[warp][h][lane] = acc[h];
-        acc_s[warp][4][lane] = make_float4(mx, sum, 0.f, 0.f);
-        __syncthreads();
-        if (part_warp == 0 && valid) {
-            for (int k = 1; k < kPartWarps; ++k) mx = fmaxf(mx, acc_s[2 * k + col_warp][4][lane].x);
-            const float own = acc_s[warp][4][lane].x;
-            scale(own == -INFINITY ? 0.f : exp2f((own - mx) * kLog2e));
+            for (int h = 0; h < 4; ++h) acc_s[warp][h][lane] = acc[h];
+            acc_s[warp][4][lane] = make_float4(mx, sum, 0.f, 0.f);
+            __syncthreads();
+            if (part_warp == 0 && valid) {
+                const float own = mx;
+                for (int k = 1; k < kPartWarps; ++k)
+                    mx = fmaxf(mx, acc_s[2 * k + col_warp][4][lane].x);
+                scale(own == -INFINITY ? 0.f : exp2f((own - mx) * kLog2e));
 #pragma unroll
-            for (int k = 1; k < kPartWarps; ++k) {
-                const float4 ms = acc_s[2 * k + col_warp][4][lane];
-                const float w = weight(ms.x);
-                float4 v[4];
+                for (int k = 1; k < kPartWarps; ++k) {
+                    const float4 ms = acc_s[2 * k + col_warp][4][lane];
+                    const float w = weight(ms.x);
+                    float4 v[4];
 #pragma unroll
-                for (int h = 0; h < 4; ++h) v[h] = acc_s[2 * k + col_warp][h][lane];
-                sum += w * ms.y;
-                add(w, v);
+                    for (int h = 0; h < 4; ++h) v[h] = acc_s[2 * k + col_warp][h][lane];
+                    sum += w * ms.y;
+                    add(w, v);
+                }
             }
+            __syncthreads();  // acc_s is free again
+        }
+        if (valid && (few || part_warp == 0)) {
             const float inv = sum == 0.f ? 0.f : 1.f / sum;
             const size_t orow = (size_t(info.x) + r / p.G) * p.H_q + info.z * p.G + r % p.G;
             uint4* out = reinterpret_cast<uint4*>(p.o + orow * D + col4 * 4);
@@ -1470,7 +1494,6 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const Params p) {
             }
             if (col4 == 0 && p.lse) p.lse[orow] = sum == 0.f ? -INFINITY : mx + logf(sum);
         }
-        __syncthreads();  // acc_s is free again
     }
 }
 
