@@ -201,7 +201,6 @@ __device__ __forceinline__ int plain_tiles(const Params& p, const Item& w, int g
 // `seen` on are not visible to every row, those from `keys` on to none.
 struct Repair {
     int seen, keys, end;
-    __device__ bool needed() const { return seen < end; }
 };
 template <int kMode>
 __device__ __forceinline__ Repair repair_of(const Params& p, const Item& w, int jj) {
@@ -871,11 +870,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             // The repair of V tile j may start once V tile j - 2, which had its
             // ring slot, has been seen here; at most two are asked for at a time.
             auto ask = [&](int j) {
-                if (j >= plain && j < n && repair_of<kMode>(p, w, w.j0 + j).needed())
-                    mbar_arrive(bar(bFixAsk + (asked++ & 1)));
+                if (j >= plain && j < n) mbar_arrive(bar(bFixAsk + (asked++ & 1)));
             };
             auto repaired = [&](int j) {
-                if (j < plain || !repair_of<kMode>(p, w, w.j0 + j).needed()) return true;
+                if (j < plain) return true;
                 const int f = fixed++;
                 return mbar_wait_bounded(bar(bFixDone + (f & 1)), (f >> 1) & 1, p.status);
             };
@@ -1015,7 +1013,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (w.n < 0) break;
             for (int j = plain_tiles<kMode>(p, w, 0); j < w.n && alive; ++j) {
                 const Repair fix = repair_of<kMode>(p, w, w.j0 + j);
-                if (!fix.needed()) continue;
                 const int ri = r + 2 * j + 1;
                 alive = __all_sync(0xffffffffu,
                                    mbar_wait_bounded(bar(bFixAsk + (f & 1)), (f >> 1) & 1,
