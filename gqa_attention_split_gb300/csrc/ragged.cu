@@ -1574,7 +1574,9 @@ bool bad_strides(int64_t st, int64_t sh, int64_t tokens, int heads) {
     if (heads > 1 && (sh <= 0 || sh >= lim)) return true;
     return tokens > 1 && (st <= 0 || st >= lim);
 }
-bool odd_strides(int64_t st, int64_t sh) { return (st | sh) & 7; }
+bool odd_strides(int64_t st, int64_t sh, int64_t tokens, int heads) {
+    return ((tokens > 1 ? st : 0) | (heads > 1 ? sh : 0)) & 7;
+}
 
 int check_common(const void* q, const void* k, const void* v, const void* o, const void* lse,
                  int B, int H_q, int H_kv, int d, float scale) {
@@ -1706,8 +1708,10 @@ extern "C" int gqa_attn_prefill_packed(const uint16_t* q, const uint16_t* k, con
         bad_strides(k_stride_t, k_stride_h, total_k, H_kv) ||
         bad_strides(v_stride_t, v_stride_h, total_k, H_kv))
         return GQA_ERR_INVALID_ARG;
-    if (odd_strides(q_stride_t, q_stride_h) || odd_strides(k_stride_t, k_stride_h) ||
-        odd_strides(v_stride_t, v_stride_h) || (reinterpret_cast<uintptr_t>(cu_q) & 3u) ||
+    if (odd_strides(q_stride_t, q_stride_h, total_q, H_q) ||
+        odd_strides(k_stride_t, k_stride_h, total_k, H_kv) ||
+        odd_strides(v_stride_t, v_stride_h, total_k, H_kv) ||
+        (reinterpret_cast<uintptr_t>(cu_q) & 3u) ||
         (reinterpret_cast<uintptr_t>(cu_k) & 3u))
         return GQA_ERR_MISALIGNED;
     if (B == 0 || total_q == 0) return GQA_OK;
@@ -1767,8 +1771,10 @@ extern "C" int gqa_attn_decode_tree(
         bad_strides(k_stride_t, k_stride_h, total, H_kv) ||
         bad_strides(v_stride_t, v_stride_h, total, H_kv))
         return GQA_ERR_INVALID_ARG;
-    if (odd_strides(q_stride_t, q_stride_h) || odd_strides(k_stride_t, k_stride_h) ||
-        odd_strides(v_stride_t, v_stride_h) || !aligned16(k_cache) || !aligned16(v_cache) ||
+    if (odd_strides(q_stride_t, q_stride_h, total, H_q) ||
+        odd_strides(k_stride_t, k_stride_h, total, H_kv) ||
+        odd_strides(v_stride_t, v_stride_h, total, H_kv) || !aligned16(k_cache) ||
+        !aligned16(v_cache) ||
         ((reinterpret_cast<uintptr_t>(cu_seqlens) | reinterpret_cast<uintptr_t>(context_lens) |
           reinterpret_cast<uintptr_t>(tree_mask)) & 3u))
         return GQA_ERR_MISALIGNED;
@@ -1843,7 +1849,8 @@ extern "C" int gqa_attn_cache_append(uint16_t* k_cache, uint16_t* v_cache, const
         bad_strides(v_stride_t, v_stride_h, total_new, H_kv))
         return GQA_ERR_INVALID_ARG;
     if (!aligned16(k_cache) || !aligned16(v_cache) || !aligned16(k_new) || !aligned16(v_new) ||
-        odd_strides(k_stride_t, k_stride_h) || odd_strides(v_stride_t, v_stride_h) ||
+        odd_strides(k_stride_t, k_stride_h, total_new, H_kv) ||
+        odd_strides(v_stride_t, v_stride_h, total_new, H_kv) ||
         ((reinterpret_cast<uintptr_t>(cu_seqlens) | reinterpret_cast<uintptr_t>(starts) |
           reinterpret_cast<uintptr_t>(index)) & 3u))
         return GQA_ERR_MISALIGNED;

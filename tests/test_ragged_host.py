@@ -145,3 +145,14 @@ def test_reference_ignores_what_is_not_visible():
     assert np.isfinite(O).all() and (O[1] == 0).all() and np.isneginf(L[1]).all()
     assert np.allclose(O[0], np.broadcast_to(v[0], (2, 64)))
     assert np.allclose(L[0], 0.5 * q[0] @ k[0, 0])
+
+
+def test_strides_of_dimensions_of_size_one_are_ignored():
+    odd = dict(q_stride_t=3, k_stride_t=5, v_stride_t=-7)
+    assert _packed(B=0, total_q=1, total_k=1, **odd) == api.GQA_OK
+    assert _tree(B=0, total=1, **odd) == api.GQA_OK
+    odd = dict(k_stride_h=5, v_stride_h=-7)
+    assert _packed(B=0, H_q=1, H_kv=1, q_stride_h=3, **odd) == api.GQA_OK
+    assert _tree(B=0, H_q=1, H_kv=1, q_stride_h=3, **odd) == api.GQA_OK
+    assert _append(B=0, H_kv=1, **odd) == api.GQA_OK
+    assert _append(B=0, total_new=1, k_stride_t=5, v_stride_t=-7) == api.GQA_OK
