@@ -695,7 +695,15 @@ def _cache(torch, k_cache, v_cache, H_kv, d, device):
     return shape[0], shape[2]
 
 
-def _outputs(torch, q, out, lse):
+def _outputs(torch, q, out, lse, stream=None):
+    if stream is not None and (out is None or lse is None):
+        # from the launch stream's pool: what the current stream still reads is not overwritten
+        with torch.cuda.stream(stream):
+            return _outputs(
+                torch, q,
+                torch.empty(q.shape, dtype=torch.bfloat16, device=q.device) if out is None else out,
+                torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
+                if lse is None else lse)
     if out is None:
         out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
     elif (out.dtype is not torch.bfloat16 or out.shape != q.shape or not out.is_contiguous()
@@ -723,6 +731,18 @@ def _raw_stream(torch, device, stream):
     return torch._C._cuda_getCurrentRawStream(device)
 
 
+def _in_use(torch, device, stream, *tensors):
+    """Tells the allocator that ``tensors`` are used on ``stream`` and on the current stream, so that
+    memory freed by one of them is not handed out while the other still works on it."""
+    current = torch.cuda.current_stream(device)
+    if stream == current:
+        return
+    for t in tensors:
+        if t is not None:
+            t.record_stream(stream)
+            t.record_stream(current)
+
+
 def prefill_packed(q, k, v, cu_seqlens, cu_seqlens_k=None, *, causal: bool = True,
                    scale: float | None = None, out=None, lse=None, stream=None):
     """Attention over packed sequences of different lengths. q [total_q,H_q,d], k/v
@@ -732,7 +752,9 @@ def prefill_packed(q, k, v, cu_seqlens, cu_seqlens_k=None, *, causal: bool = Tru
     last tokens: causal query t sees keys j <= n_k - n_q + t.
 
     Returns (o [total_q,H_q,d] bf16, lse [total_q,H_q] fp32). Rows behind the last sequence are
-    not written. The call runs on ``stream`` (default: the current stream of q's device).
+    not written. The call runs on ``stream`` (default: the current stream of q's device); waiting
+    for what the current stream still writes to the inputs, and for the results, is the caller's,
+    but memory freed on either stream is not reused before the other is done with it.
     """
     import torch
 
@@ -753,7 +775,7 @@ def prefill_packed(q, k, v, cu_seqlens, cu_seqlens_k=None, *, causal: bool = Tru
         cu_k = _ints(torch, "cu_seqlens_k", cu_seqlens_k, B + 1, dev)
     elif total_k != total_q:
         raise ValueError("k and v must have q's tokens when cu_seqlens_k is not given")
-    out, lse = _outputs(torch, q, out, lse)
+    out, lse = _outputs(torch, q, out, lse, stream)
     sc = 1.0 / math.sqrt(d) if scale is None else float(scale)
     rc = _on_device(torch, dev, lambda: lib().gqa_attn_prefill_packed(
         q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(), cu_q, cu_k, B,
@@ -761,6 +783,8 @@ def prefill_packed(q, k, v, cu_seqlens, cu_seqlens_k=None, *, causal: bool = Tru
         _raw_stream(torch, dev, stream)))
     if rc != GQA_OK:
         raise GqaError(rc, "gqa_attn_prefill_packed")
+    if stream is not None:
+        _in_use(torch, dev, stream, q, k, v, out, lse, cu_seqlens, cu_seqlens_k)
     return out, lse
 
 
@@ -806,8 +830,9 @@ def decode_tree(q, k_new, v_new, k_cache, v_cache, context_lens, *, cu_seqlens=N
             raise ValueError("tree_mask must be a contiguous int32 [total, words] tensor")
         words = tree_mask.shape[1]
         mask = _ints(torch, "tree_mask", tree_mask, total * words, dev)
-    out, lse = _outputs(torch, q, out, lse)
+    out, lse = _outputs(torch, q, out, lse, stream)
     sc = 1.0 / math.sqrt(d) if scale is None else float(scale)
+    given = workspace
     if workspace is None:
         # from the launch stream's pool: its memory is reused only behind this call
         n = lib().gqa_attn_decode_tree_workspace_size(H_q, H_kv, d, max_tokens)
@@ -825,6 +850,9 @@ def decode_tree(q, k_new, v_new, k_cache, v_cache, context_lens, *, cu_seqlens=N
         workspace.numel() * workspace.element_size(), _raw_stream(torch, dev, stream)))
     if rc != GQA_OK:
         raise GqaError(rc, "gqa_attn_decode_tree")
+    if stream is not None:
+        _in_use(torch, dev, stream, q, k_new, v_new, k_cache, v_cache, out, lse, context_lens,
+                cu_seqlens, tree_mask, given)
     return out, lse
 
 
@@ -857,6 +885,8 @@ def cache_append(k_cache, v_cache, k_new, v_new, starts, *, cu_seqlens=None, ind
         B, H_kv, d, S_max, total, total_new, ks, kh, vs, vh, _raw_stream(torch, dev, stream)))
     if rc != GQA_OK:
         raise GqaError(rc, "gqa_attn_cache_append")
+    if stream is not None:
+        _in_use(torch, dev, stream, k_cache, v_cache, k_new, v_new, starts, cu_seqlens, index)
 
 
 def check(stream=None):

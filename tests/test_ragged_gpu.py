@@ -658,3 +658,65 @@ def test_two_streams_at_once():
     for i in range(2):
         for o, lse in got[i]:
             assert torch.equal(o, want[i][0]) and torch.equal(lse, want[i][1])
+
+
+def test_memory_freed_around_a_call_on_another_stream_is_not_reused():
+    # the current stream frees the inputs of a call that waits on a side stream, and writes over
+    # whatever memory the allocator hands out next; and the results do not take memory that the
+    # current stream still reads
+    q, k, v = (_randn(500 + i, 4096, 8, 128) for i in range(3))
+    cu = _cu([4096])
+    side = torch.cuda.Stream()
+
+    def fill(value):
+        return torch.full(q.shape, value, dtype=torch.bfloat16, device="cuda")
+
+    # (every kernel has run once, on either stream: loading one may wait for the device)
+    want, want_lse = api.prefill_packed(q, k, v, cu)
+    kept = [fill(1.0) for _ in range(8)]
+    for t in kept:
+        torch.mul(want, 1, out=t)
+    for s in (torch.cuda.current_stream(), side):
+        with torch.cuda.stream(s):
+            torch.cuda._sleep(1000)
+    copies = [t.clone() for t in (q, k, v)]
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(100_000_000)
+    o, lse = api.prefill_packed(*copies, cu, stream=side)
+    del copies
+    over = [fill(float("nan")) for _ in range(8)]
+    torch.cuda.synchronize()
+    assert torch.equal(o, want) and torch.equal(lse, want_lse)
+
+    x = [fill(1.0) for _ in range(8)]
+    torch.cuda.synchronize()
+    torch.cuda._sleep(100_000_000)
+    for t, u in zip(x, kept):
+        torch.mul(t, 1, out=u)
+    del x, t
+    o, lse = api.prefill_packed(q, k, v, cu, stream=side)
+    torch.cuda.synchronize()
+    api.check()
+    assert torch.equal(o, want) and all((u == 1).all() for u in kept)
+    del over
+
+
+def test_most_rows():
+    # the largest batch: one token a row, prompts, drafts and appended tokens
+    B, d, S_max = 65535, 64, 8
+    kc = torch.zeros(B, 1, S_max, d, dtype=torch.bfloat16, device="cuda")
+    vc = torch.zeros_like(kc)
+    q, k, v = (_randn(510 + i, B, 1, d) for i in range(3))
+    ones = torch.arange(B + 1, dtype=torch.int32, device="cuda")
+    ctx = (ones[:B] % 2).contiguous()
+    o, lse = api.prefill_packed(q, k, v, ones)
+    assert torch.equal(o, v)  # a token that sees itself alone
+    # row b holds b % 2 tokens in the cache, each the row's own
+    api.cache_append(kc, vc, k, v, torch.zeros_like(ctx), cu_seqlens=ones)
+    o, lse2 = api.decode_tree(q, k, v, kc, vc, ctx, cu_seqlens=ones, max_tokens=1)
+    api.check()
+    assert torch.equal(kc[:, :, 0], k) and torch.equal(vc[:, :, 0], v)
+    assert torch.equal(o, v)  # the same value twice keeps its value
+    more = lse2.flatten() - lse.flatten() - ctx * math.log(2)
+    assert more.abs().max().item() < 1e-4  # |lse| <= 16: a few steps of 2^-20
