@@ -197,13 +197,15 @@ extern "C" const char* gqa_attn_strerror(int code) {
     switch (code) {
         case GQA_OK: return "ok";
         case GQA_ERR_INVALID_ARG: return "invalid argument";
-        case GQA_ERR_UNSUPPORTED: return "unsupported shape (d must be 64 or 128; decode: G <= 16)";
-        case GQA_ERR_MISALIGNED: return "tensor pointer not 16-byte aligned";
+        case GQA_ERR_UNSUPPORTED:
+            return "unsupported shape (d must be 64 or 128; decode: G <= 16; or a size too large)";
+        case GQA_ERR_MISALIGNED: return "tensor pointer or stride not 16-byte aligned";
         case GQA_ERR_CUDA: return "CUDA runtime or driver error";
         case GQA_ERR_DEVICE_TIMEOUT: return "a kernel's bounded wait ran out";
         case GQA_ERR_WORKSPACE:
             return "workspace too small, misaligned, or growth needed during stream capture";
-        case GQA_ERR_DEVICE_BAD_INPUT: return "a seqlen outside [0, S_max] was clamped";
+        case GQA_ERR_DEVICE_BAD_INPUT:
+            return "a length, prefix sum, slot or index out of range was clamped or left out";
         default: return "unknown error code";
     }
 }

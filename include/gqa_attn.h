@@ -61,12 +61,12 @@ typedef struct CUstream_st* cudaStream_t;
 enum {
     GQA_OK = 0,
     GQA_ERR_INVALID_ARG = -1,    /* null pointer, bad size, H_q % H_kv != 0, ... */
-    GQA_ERR_UNSUPPORTED = -2,    /* d not in {64, 128}; decode: G > 16 */
-    GQA_ERR_MISALIGNED = -3,     /* a tensor pointer is not 16-byte aligned */
+    GQA_ERR_UNSUPPORTED = -2,    /* d not in {64, 128}, decode: G > 16, a size too large */
+    GQA_ERR_MISALIGNED = -3,     /* a tensor pointer or stride is not 16-byte aligned */
     GQA_ERR_CUDA = -4,           /* a CUDA runtime/driver call failed */
     GQA_ERR_DEVICE_TIMEOUT = -5, /* a kernel's bounded wait ran out (device status) */
     GQA_ERR_WORKSPACE = -6,      /* caller workspace too small or misaligned */
-    GQA_ERR_DEVICE_BAD_INPUT = -7 /* the device saw a seqlen outside [0, S_max] */
+    GQA_ERR_DEVICE_BAD_INPUT = -7 /* a length, prefix sum, slot or index out of range */
 };
 
 /* ---------------------------------------------------------------- decode --
@@ -344,9 +344,9 @@ GQA_API int gqa_attn_prefill_partial(const uint16_t* q, const uint16_t* k, const
  * contiguous. Their token and head strides are in elements, positive
  * multiples of 8 (ignored for a dimension of size 1), so slices of a fused
  * projection and head-major tensors are taken as they are. o is contiguous
- * [tokens, H_q, d], lse contiguous fp32 [tokens, H_q] or NULL. Rows of o and
- * lse that belong to no sequence are not written. q, k, v, o are 16-byte
- * aligned.
+ * [tokens, H_q, d], lse contiguous fp32 [tokens, H_q] or NULL; neither overlaps
+ * an input. Rows of o and lse that belong to no sequence are not written. q, k,
+ * v, o are 16-byte aligned.
  *
  * Prefix sums (cu_*): device int32 [B + 1], row b holds the packed tokens
  * cu[b] .. cu[b + 1] - 1. Values that leave [0, total] or decrease are clamped
