@@ -40,7 +40,8 @@
 // items and K/V ring, as two CTAs per SM (230 / 5110: their products interleave
 // and both wait) or in one CTA with a lock around the issue (203 / 4600); the end
 // of an item behind the next item's first tile (188 / 4350); O through TMA boxes
-// (172 / 4300).
+// (172 / 4300). Against 154 / 3920: half of a tile's exponentials against the
+// maximum so far, beside the search for the new one (167 / 4290).
 
 #include <cuda_runtime.h>
 #include <math.h>
