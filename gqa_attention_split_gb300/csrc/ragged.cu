@@ -25,13 +25,16 @@
 // tensor memory, P is written over its S columns and read from there by the P V
 // product.
 //
-// What bounds it. A group's tile is a chain: S ready, softmax (about 1700
-// cycles), P V and the next S (1024 cycles of tensor work at d = 128), hand-over
-// (about 200). Two groups take turns at the tensor cores, so a pair of tiles
-// takes about 2870 cycles where the products alone would take 2048: packed 32K
-// tokens 1.50-1.53 PFLOP/s, 0.80-0.82 of the measured bf16 rate. A long context
-// under few queries is bound by HBM, a short one by latencies: launch 1 us,
-// prefix sums to first tile 4, per tile 1.5, end of an item 2, merge 4.
+// What bounds it. A group's tile is a chain: S seen, softmax (1050 to 1100 cycles,
+// 950 of them exponentials, sums and packing at the rate of the fp32 and special
+// function pipes), P V and the next S (1024 cycles of tensor work at d = 128), and
+// 600 of hand-overs (commit to waiting warps 250, each wait of the issuing thread
+// about 100 even when its barrier is complete). Two groups take turns at the tensor
+// cores, so a pair of tiles takes about 2740 cycles where the products alone would
+// take 2048: packed 32K tokens 1.50-1.58 PFLOP/s, 0.80-0.85 of the measured bf16
+// rate. A long context under few queries is bound by HBM, a short one by
+// latencies: launch 1 us, prefix sums to first tile 4, per tile 1.5, end of an
+// item 2, merge 4.
 // Measured and slower on the same box (packed 8K batch / packed 32K, against
 // 174 / 4300 us at that point): steps of 64 keys with two S buffers per group
 // (208 / 5930: S products of N = 64 run at 0.6 of the rate); one S buffer for
@@ -41,7 +44,12 @@
 // and both wait) or in one CTA with a lock around the issue (203 / 4600); the end
 // of an item behind the next item's first tile (188 / 4350); O through TMA boxes
 // (172 / 4300). Against 154 / 3920: half of a tile's exponentials against the
-// maximum so far, beside the search for the new one (167 / 4290).
+// maximum so far, beside the search for the new one (167 / 4290); two threads to a
+// query row, 16 softmax warps (178 / 4420, and 164 / 4160 with nothing exchanged
+// between the two: the pipes, not latency, are the softmax's limit); scalar in
+// place of packed fp32 arithmetic (164 / 4310); S products a tile ahead from a
+// second issuing warp, P in columns of its own (200 / 3990); the barriers of an
+// issue polled by one lane each (152 / 3920, but a batch of 8 trees 145 against 135).
 
 #include <cuda_runtime.h>
 #include <math.h>
