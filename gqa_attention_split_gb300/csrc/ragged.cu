@@ -233,8 +233,8 @@ struct Geo {
     static constexpr uint32_t kQOff = 0;  // two groups
     static constexpr uint32_t kRingOff = 2 * kTileBytes;
     static constexpr uint32_t kStageOff = kRingOff + kRingSlots * kTileBytes;  // 8 warps
-    static constexpr uint32_t kXchOff = kStageOff + 8 * kStageBytes;  // float2 [2][128]
-    static constexpr uint32_t kSeqOff = kXchOff + 2 * BM * 8;         // int2 [kSchedSeqs]
+    static constexpr uint32_t kXchOff = kStageOff + 8 * kStageBytes;  // float4 [2][128]
+    static constexpr uint32_t kSeqOff = kXchOff + 2 * BM * 16;        // int2 [kSchedSeqs]
     static constexpr uint32_t kItemOff = kSeqOff + kSchedSeqs * 8;
     static constexpr uint32_t kBarOff = kItemOff + kItemSlots * 64;
     static constexpr int kSmemBytes = 1024 + kBarOff + 512;
@@ -589,20 +589,18 @@ __device__ __forceinline__ void schedule_tree(const Params& p, Publisher& pub, i
 // ---- softmax of one tile of scores
 
 struct RowState {
-    float m, l;  // running maximum (base 2), sum of p
+    float m, l, lb;  // running maximum (base 2), sums of p and of bf16(p)
 };
 
 // P = 2^(s - m) over the tile, written as bf16 pairs over S (the operand type of
-// the P V product); returns the factor that O has to be scaled by (1: left as it
-// is). O is divided by l, the fp32 sum of the unrounded p: each p is off by half
-// a bf16 step at most, and so is O relative to sum p |v|. Dividing by the sum of
-// the rounded values, which the uniform prefill does, costs two additions for
-// every pair of keys and a tenth of the time (packed 32K 4.40 against 4.00 ms,
-// packed 8K batch 174 against 156 us) and changes O's distance from 64 bits by
-// 0 to 6% (relative 0.0017 against 0.0018 on short prompts, 0.0020 both on long
-// ones; bf16 output alone has 0.0016).
+// the P V product) and left in pk; returns the factor that O has to be scaled by
+// (1: left as it is). lse comes from l, the sum of the unrounded p, O from lb, that
+// of the rounded ones (rounded_sum): O is then a weighted mean of the V rows,
+// whose weights are off by half a bf16 step at most, and what all weights are off
+// by together drops out.
 __device__ __forceinline__ float softmax_tile(const float (&sv)[BN], RowState& st,
-                                              float scale_log2, uint64_t c2, uint32_t s_addr) {
+                                              float scale_log2, uint64_t c2, uint32_t s_addr,
+                                              uint32_t (&pk)[2][32]) {
     float mm[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) mm[i] = fmaxf(sv[i], sv[8 + i]);
@@ -622,7 +620,6 @@ __device__ __forceinline__ float softmax_tile(const float (&sv)[BN], RowState& s
     uint64_t s2[4] = {0ull, 0ull, 0ull, 0ull};
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
-        uint32_t pk[32];
 #pragma unroll
         for (int i = 0; i < 32; ++i) {
             const int c = half * 64 + 2 * i;
@@ -630,15 +627,36 @@ __device__ __forceinline__ float softmax_tile(const float (&sv)[BN], RowState& s
             f2unpack(ffma2(f2pack(sv[c], sv[c + 1]), c2, n2), x0, x1);
             const float e0 = fast_exp2(x0), e1 = fast_exp2(x1);
             s2[i & 3] = fadd2(s2[i & 3], f2pack(e0, e1));
-            pk[i] = pack_bf16x2(e0, e1);
+            pk[half][i] = pack_bf16x2(e0, e1);
         }
-        tc::tmem_st32(s_addr + half * 32, pk);
+        tc::tmem_st32(s_addr + half * 32, pk[half]);
     }
     float t[8];
 #pragma unroll
     for (int u = 0; u < 4; ++u) f2unpack(s2[u], t[2 * u], t[2 * u + 1]);
     st.l = st.l * corr + (((t[0] + t[1]) + (t[2] + t[3])) + ((t[4] + t[5]) + (t[6] + t[7])));
+    st.lb *= corr;
     return corr;
+}
+
+// Sum of a tile's rounded p. Two mixed-precision additions for every pair of keys,
+// for which the softmax has no free pipe: 5 to 8% of the time wherever they stand
+// (packed 8K batch / packed 32K / d = 64 chunks / ragged trees, us). Ahead of the wait
+// for the next S 166 / 4190 / 80 / 143; right behind the hand-over of P 168 / 4250 /
+// 83 / 147 (kTreeAlt does that: the other spills, 21 us for 19 on short drafts); beside
+// the exponentials 167 / 4230 / 85 / 148; widened by shift and mask and added in
+// pairs there 173 / 4440 / 85 / 156; as products with ones on mma.sync 202 / 5680 /
+// 103 / 199. O divided by l needs none, 153 / 3960 / 75 / 135, but its error is up to
+// 1.2 times the bound of a weighted mean on short rows, and equal V rows do not come
+// out as they are.
+__device__ __forceinline__ float rounded_sum(const uint32_t (&pk)[2][32]) {
+    float t[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < 64; ++i) {
+        t[2 * (i & 1)] = add_f32_bf16_lo(t[2 * (i & 1)], pk[i >> 5][i & 31]);
+        t[2 * (i & 1) + 1] = add_f32_bf16_hi(t[2 * (i & 1) + 1], pk[i >> 5][i & 31]);
+    }
+    return (t[0] + t[1]) + (t[2] + t[3]);
 }
 
 // ---- output: 64 bytes of each of a warp's 32 rows, through shared memory so
@@ -1097,7 +1115,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t lane_base = tmem + (uint32_t(quad * 32) << 16);
         const uint32_t col_s = col_s_of(g), col_o = col_o_of(g);
         const uint32_t stage = smem_u32(smem + Gm::kStageOff + (g * 4 + quad) * kStageBytes);
-        float2* xch = reinterpret_cast<float2*>(smem + Gm::kXchOff);
+        float4* xch = reinterpret_cast<float4*>(smem + Gm::kXchOff);
         const uint64_t c2 = f2pack(p.scale_log2, p.scale_log2);
         bool alive = true;
         int tt = 0;              // tiles this group finished: its S phases
@@ -1159,9 +1177,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                                                    : (1u << upto) - 1u);
                 }
             }
-            RowState st{-INFINITY, 0.f};
+            RowState st{-INFINITY, 0.f, 0.f};
+            uint32_t pk[2][32];  // the last tile's P, not in lb yet
 #pragma unroll 1
             for (int i = 0; i < ng && alive; ++i) {
+                if (!kAlt && act && i > 0) st.lb += rounded_sum(pk);
                 alive = wait_all(bSFull + g, tt + i);
                 if (!alive) break;
                 if (act) {
@@ -1187,7 +1207,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             for (int c = 0; c < BN; ++c) sv[c] = c < lim ? sv[c] : -INFINITY;
                         }
                     }
-                    const float corr = softmax_tile(sv, st, p.scale_log2, c2, lane_base + col_s);
+                    const float corr = softmax_tile(sv, st, p.scale_log2, c2, lane_base + col_s, pk);
                     // O is complete here: this tile's S product was issued after
                     // the previous P V of the group, and they complete in order.
                     if (i > 0 && __any_sync(0xffffffffu, corr != 1.f)) {
@@ -1215,8 +1235,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(bPFull + g));
+                if (kAlt && act) st.lb += rounded_sum(pk);
             }
             if (!alive) break;
+            if (!kAlt && act && ng > 0) st.lb += rounded_sum(pk);
             tt += ng;
 
             // ---- epilogue. Every read of O completes before this warp's next
@@ -1225,17 +1247,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             const Item e = read_item(item_addr);
             const bool two = kAlt && uniform(e.n) > 1;
             if constexpr (kAlt) {
-                xch[g * BM + row] = make_float2(st.m, st.l);
+                xch[g * BM + row] = make_float4(st.m, st.l, st.lb, 0.f);
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(bXch));
                 alive = wait_all(bXch, xk);
                 if (!alive) break;
-                const float2 a = xch[row], b = xch[BM + row];  // group 1 without tiles: -inf, 0
+                const float4 a = xch[row], b = xch[BM + row];  // group 1 without tiles: -inf, 0, 0
                 const float m = fmaxf(a.x, b.x), ms = m == -INFINITY ? 0.f : m;
                 f0 = fast_exp2(a.x - ms);
                 f1 = fast_exp2(b.x - ms);
                 st.m = m;
                 st.l = f0 * a.y + f1 * b.y;
+                st.lb = f0 * a.z + f1 * b.z;
             }
             // (what does not need O comes before the wait for it)
             const int t = (kAlt ? e.tok0 : e.tok0 + g * p.tok) + row_tok;
@@ -1247,8 +1270,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int prow = (t - e.tok0) * p.G + row_head;
             const RowPtrs rows(
                 valid && direct ? reinterpret_cast<uint8_t*>(p.o + orow * D) : nullptr, lane);
-            // l is 0 only for a row that saw no key (and NaN stays NaN)
-            const float inv = st.l == 0.f ? 0.f : 1.f / st.l;
+            // the sums are 0 only for a row that saw no key (and NaN stays NaN)
+            const float inv = st.lb == 0.f ? 0.f : 1.f / st.lb;
             if (valid && (!kAlt || g == 0)) {
                 const float lse = st.l == 0.f ? -INFINITY : (st.m + log2f(st.l)) * kLn2;
                 if (!direct)
