@@ -519,7 +519,6 @@ __device__ __forceinline__ void schedule_tree(const Params& p, Publisher& pub, i
         x = even ? team : int(min(begin, int64_t(steps)));
         end = even ? team + 1 : int(min(int64_t(steps), begin + per));
     }
-    if (bad && blockIdx.x == 0) atomicOr(p.status, kStatusBadSeqlen);
     if (!p.whole && lane == 0) p.part_info[blockIdx.x] = make_int4(0, 0, 0, 0);
     int before = 0;  // steps of the rows before b0
 #pragma unroll 1
@@ -581,6 +580,8 @@ __device__ __forceinline__ void schedule_tree(const Params& p, Publisher& pub, i
         }
         before += all;
     }
+    // (block 0 has read every row by now: above, or, when no row is cut, in this walk)
+    if (bad && blockIdx.x == 0) atomicOr(p.status, kStatusBadSeqlen);
     Item stop{};
     stop.n = -1;
     pub.put(stop, lane);
