@@ -107,6 +107,7 @@ struct Params {
     unsigned* status;
     int64_t v_st, v_sh;
     int B, H_q, H_kv, G, total_q, total_k, S_max, max_tokens, mask_words, causal;
+    int max_blocks;   // kPrompts: blocks of all rows under any valid prefix sums
     int tok;          // tokens of a group
     int team;         // decode_tree: CTAs that share a range of keys, one per token block
     int n_teams, part_rows;
@@ -327,33 +328,40 @@ __device__ __forceinline__ void schedule_prompts(const Params& p, int2* seqs, Pu
     const bool in_order = p.B > kSchedSeqs;
     const int chunk = cdiv(p.B, kSchedSeqs);
     int* before_chunk = reinterpret_cast<int*>(seqs);  // blocks before chunk c
-    int top = 0, blocks = 0;
+    int top = 0, blocks;
+    // (64 bits, and no work at all above max_blocks: rows of bad prefix sums may overlap,
+    // and then have more blocks together than there are tokens)
+    int64_t sum = 0;
     if (in_order) {
 #pragma unroll 1
         for (int c0 = 0; c0 < kSchedSeqs; c0 += 32) {
-            int n = 0;
+            int64_t n = 0;
             const int first = min(p.B, (c0 + lane) * chunk);
 #pragma unroll 4
             for (int b = first; b < min(p.B, first + chunk); ++b) n += levels(b).y;
-            int incl = n;
+            int64_t incl = n;
             for (int o = 1; o < 32; o <<= 1) {
-                const int y = __shfl_up_sync(0xffffffffu, incl, o);
+                const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
                 if (lane >= o) incl += y;
             }
-            before_chunk[c0 + lane] = blocks + incl - n;
-            blocks += __shfl_sync(0xffffffffu, incl, 31);
+            before_chunk[c0 + lane] = int(min(sum + incl - n, int64_t(p.max_blocks)));
+            sum += __shfl_sync(0xffffffffu, incl, 31);
         }
     } else {
 #pragma unroll 1
         for (int b = lane; b < p.B; b += 32) {
             const int2 s = levels(b);
             seqs[b] = s;
-            blocks += s.y;
+            sum += s.y;
             if (s.y > 0) top = max(top, p.causal ? s.x + s.y - 1 : s.x);
         }
         top = __reduce_max_sync(0xffffffffu, top);
-        blocks = __reduce_add_sync(0xffffffffu, blocks);
+        // (at most 32 rows of 2^30 blocks a lane: the low 26 bits and the rest)
+        const unsigned low = __reduce_add_sync(0xffffffffu, unsigned(sum) & 0x3ffffffu);
+        const unsigned high = __reduce_add_sync(0xffffffffu, unsigned(sum >> 26));
+        sum = (int64_t(high) << 26) + low;
     }
+    blocks = sum <= p.max_blocks ? int(sum) : 0;
     if (bad && blockIdx.x == 0) atomicOr(p.status, kStatusBadSeqlen);
     __syncwarp();
     auto above = [&](int l) {  // blocks on levels > l
@@ -1763,6 +1771,7 @@ extern "C" int gqa_attn_prefill_packed(const uint16_t* q, const uint16_t* k, con
     // at most this many blocks, however the tokens are spread over the rows
     const int64_t blocks = int64_t(total_q) / (2 * p.tok) + (B < total_q ? B : total_q);
     const int ctas = int(blocks * H_kv < sms ? blocks * H_kv : sms);
+    p.max_blocks = int(blocks);  // (below 2^31: total_q / 2 + 65535 at most)
     Maps m;
     if (!packed_maps(m, p, q, k, v, d, q_stride_t, q_stride_h, k_stride_t, k_stride_h, v_stride_t,
                      v_stride_h))

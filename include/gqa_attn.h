@@ -350,7 +350,9 @@ GQA_API int gqa_attn_prefill_partial(const uint16_t* q, const uint16_t* k, const
  *
  * Prefix sums (cu_*): device int32 [B + 1], row b holds the packed tokens
  * cu[b] .. cu[b + 1] - 1. Values that leave [0, total] or decrease are clamped
- * and reported as GQA_ERR_DEVICE_BAD_INPUT by gqa_attn_check(). B <= 65535.
+ * and reported as GQA_ERR_DEVICE_BAD_INPUT by gqa_attn_check(). (Clamped rows
+ * may overlap. gqa_attn_prefill_packed computes nothing when they hold more
+ * blocks of queries than total_q and B allow.) B <= 65535.
  * scale > 0 (as gqa_attn_prefill). The calls allocate nothing, keep nothing
  * and can be captured into graphs.
  */

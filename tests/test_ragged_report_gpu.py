@@ -45,3 +45,24 @@ def test_tree_reports_bad_rows_anywhere(S_max, row, what):
     api.decode_tree(x[0], x[1], x[1], x[2], x[2], torch.from_numpy(ctx).cuda(), cu_seqlens=good,
                     max_tokens=3)
     api.check()
+
+
+# Prefix sums that go up and down: every other row holds all tokens. With the valid ones no launch has
+# more blocks of queries than the tokens and rows allow; here it would be B / 2 times as many, past 32
+# bits in the last case. Reported, nothing computed, and the next call is as ever.
+@pytest.mark.parametrize("B,n,H_q", [(600, 500, 4), (2000, 500, 4), (65535, 300000, 128)])
+def test_packed_rows_that_overlap_are_reported_and_not_computed(B, n, H_q):
+    q = torch.empty(n, H_q, 64, dtype=torch.bfloat16, device="cuda")
+    k = torch.zeros(n, 1, 64, dtype=torch.bfloat16, device="cuda")
+    q[:500] = 0
+    out, lse = torch.empty_like(q), torch.full((n, H_q), 9.0, device="cuda")
+    cu = torch.zeros(B + 1, dtype=torch.int32, device="cuda")
+    cu[1::2] = n
+    _reported(lambda: api.prefill_packed(q, k, k, cu, out=out, lse=lse))
+    assert (lse == 9).all()
+    cu = torch.full((B + 1,), 500, dtype=torch.int32, device="cuda")
+    cu[0] = 0
+    api.prefill_packed(q, k, k, cu, out=out, lse=lse)
+    api.check()
+    want = torch.log(torch.arange(1, 501, device="cuda"))[:, None].expand(-1, H_q)
+    assert (lse[:500] - want).abs().max() < 1e-5 and (lse[500:] == 9).all()
