@@ -25,16 +25,16 @@
 // tensor memory, P is written over its S columns and read from there by the P V
 // product.
 //
-// What bounds it. A group's tile is a chain: S seen, softmax (1050 to 1100 cycles,
-// 950 of them exponentials, sums and packing at the rate of the fp32 and special
-// function pipes), P V and the next S (1024 cycles of tensor work at d = 128), and
-// 600 of hand-overs (commit to waiting warps 250, each wait of the issuing thread
-// about 100 even when its barrier is complete). Two groups take turns at the tensor
-// cores, so a pair of tiles takes about 2740 cycles where the products alone would
-// take 2048: packed 32K tokens 1.50-1.58 PFLOP/s, 0.80-0.85 of the measured bf16
-// rate. A long context under few queries is bound by HBM, a short one by
-// latencies: launch 1 us, prefix sums to first tile 4, per tile 1.5, end of an
-// item 2, merge 4.
+// What bounds it. A group's tile is a chain: S seen, softmax (1150 to 1250 cycles:
+// exponentials, sums and packing at the rate of the fp32 and special function
+// pipes, which the other group's sums share), P V and the next S (1024 cycles of
+// tensor work at d = 128, 512 at 64), and 600 of hand-overs (commit to waiting warps
+// 250, each wait of the issuing thread about 100 even when its barrier is complete).
+// Two groups take turns at the tensor cores, so a pair of tiles takes 3090 cycles at
+// d = 128 and 2630 at d = 64, where the products alone would take 2048 and 1024:
+// packed 32K tokens 1.45-1.48 PFLOP/s, 0.78-0.79 of the measured bf16 rate. A long
+// context under few queries is bound by HBM, a short one by latencies: launch 1 us,
+// prefix sums to first tile 4, per tile 1.5, end of an item 2, merge 2 to 5.
 // Measured and slower on the same box (packed 8K batch / packed 32K, against
 // 174 / 4300 us at that point): steps of 64 keys with two S buffers per group
 // (208 / 5930: S products of N = 64 run at 0.6 of the rate); one S buffer for
@@ -43,13 +43,14 @@
 // items and K/V ring, as two CTAs per SM (230 / 5110: their products interleave
 // and both wait) or in one CTA with a lock around the issue (203 / 4600); the end
 // of an item behind the next item's first tile (188 / 4350); O through TMA boxes
-// (172 / 4300). Against 154 / 3920: half of a tile's exponentials against the
-// maximum so far, beside the search for the new one (167 / 4290); two threads to a
-// query row, 16 softmax warps (178 / 4420, and 164 / 4160 with nothing exchanged
-// between the two: the pipes, not latency, are the softmax's limit); scalar in
-// place of packed fp32 arithmetic (164 / 4310); S products a tile ahead from a
-// second issuing warp, P in columns of its own (200 / 3990); the barriers of an
-// issue polled by one lane each (152 / 3920, but a batch of 8 trees 145 against 135).
+// (172 / 4300). Against 154 / 3920, with O divided by the sum of the unrounded
+// weights: half of a tile's exponentials against the maximum so far, beside the
+// search for the new one (167 / 4290); two threads to a query row, 16 softmax warps
+// (178 / 4420, and 164 / 4160 with nothing exchanged between the two: the pipes, not
+// latency, are the softmax's limit); scalar in place of packed fp32 arithmetic (164 /
+// 4310); S products a tile ahead from a second issuing warp, P in columns of its own
+// (200 / 3990); the barriers of an issue polled by one lane each (152 / 3920, but a
+// batch of 8 trees 145 against 135).
 
 #include <cuda_runtime.h>
 #include <math.h>
@@ -75,9 +76,10 @@ constexpr int kRingSlots = 4;        // K/V tiles in flight
 constexpr int kItemSlots = 4;        // work items known ahead
 constexpr int kSchedSeqs = 1024;     // sequences whose schedule is kept in shared memory
 constexpr int kTreeCtas = 152;       // most CTAs of a decode_tree launch (workspace size)
-// decode_tree: rows of at most this many tiles (a cache of 512 slots) are not cut, which saves
-// the merge (8 units of 2 tiles 8.8 us against 11.2 cut, 4 tiles 9.9 against 10.2, 9 tiles 15.6
-// against 10.6)
+// decode_tree: rows are not cut where the cache holds at most this many tiles with the drafts' own
+// (512 slots), which saves the merge (8 units of 2 tiles 8.1 us against 10.2 cut, 4 tiles 10.5
+// against 11.0, 5 tiles 12.0 against 11.2, 9 tiles 18.4 against 11.7). The host goes by the size
+// of the cache, since the lengths are on the device: short contexts in a larger cache are cut.
 constexpr int kWholeTiles = 5;
 constexpr uint32_t kBoxBytes = BM * 128;       // 128 rows x 64 bf16
 constexpr uint32_t kStageBytes = 32 * 64;      // a warp's output stage: 32 rows x 64 B
@@ -89,7 +91,7 @@ constexpr float kRescaleThreshold = 8.f;
 // kTreePair: items are blocks of 2 * tok drafted tokens, a range of the keys.
 // kTreeAlt: all drafted tokens of a row fit in one group; the two softmax
 // groups take alternate K/V tiles and are merged in the epilogue (28/4 heads,
-// 5 drafts, contexts of 64 to 9100: 18.5 us against 19.7 as kTreePair, whose
+// 5 drafts, contexts of 64 to 9100: 19.0 us against 19.9 as kTreePair, whose
 // second group would be empty).
 enum Mode { kPrompts, kTreePair, kTreeAlt };
 
@@ -469,8 +471,8 @@ __device__ __forceinline__ void schedule_prompts(const Params& p, int2* seqs, Pu
 //    is its tiles long and kItemCost steps before them, about what an item's
 //    first loads and its end cost.
 // A unit that is cut leaves partial results for the merge. (A batch of
-// 8 rows with contexts of 17 to 31007 and 1 to 64 drafts: 189 us without the
-// item cost and with one KV head in every unit, 153 with them.)
+// 8 rows with contexts of 17 to 31007 and 1 to 64 drafts: 143 us, without the
+// item cost 167, with one KV head in every unit 162.)
 constexpr int kItemCost = 2;
 
 // The CTA that holds the first part of a block of a unit describes it for the
@@ -1387,9 +1389,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 // time with all their loads in flight. A unit cut into no more parts than that is
 // merged by the 8 warps of a block for all columns at once; of more parts, two
 // warps take 16 columns each and four a quarter of the parts each. Bound by the
-// loads' latency (26 drafts on 8K tokens, 8 units in 17 parts, 14 MB: 3 us; a
-// batch of 8 trees in 2 to 4 parts, 23 MB: 140 us in all with every unit merged the
-// second way, 136 like this).
+// loads' latency. What it adds to a call in a graph: 7 drafts on 333 tokens 2.4 us,
+// 26 drafts on 8K tokens (8 units in 17 parts, 14 MB) 5.6, a batch of 8 trees in 2 to
+// 4 parts (23 MB) 12.3, two wide trees of 16 query heads to a KV head 19. (Every unit
+// merged the second way: the batch 144.1 us in all, like this 143.4.)
 constexpr int kMergeThreads = 256;
 constexpr int kMergeBatch = 4;
 

@@ -362,7 +362,10 @@ GQA_API int gqa_attn_prefill_partial(const uint16_t* q, const uint16_t* k, const
  * last n_q tokens) or all n_k of them (causal == 0).
  *   cu_k : prefix sums of the keys, or NULL: the same as cu_q (and then
  *          total_k == total_q).
- * Any lengths, zero included. H_q / H_kv <= 128. */
+ * Any lengths, zero included, up to about 90 million keys in one sequence: a
+ * block of 2 * floor(128 / G) queries (G = H_q / H_kv) runs all its keys on one
+ * CTA, and a wait of a second is reported as GQA_ERR_DEVICE_TIMEOUT. Few queries
+ * on many keys therefore use few SMs. H_q / H_kv <= 128. */
 GQA_API int gqa_attn_prefill_packed(const uint16_t* q, const uint16_t* k, const uint16_t* v,
                                     uint16_t* o, float* lse, const int32_t* cu_q,
                                     const int32_t* cu_k, int B, int H_q, int H_kv, int d,
