@@ -746,9 +746,9 @@ def _in_use(torch, device, stream, *tensors):
 def prefill_packed(q, k, v, cu_seqlens, cu_seqlens_k=None, *, causal: bool = True,
                    scale: float | None = None, out=None, lse=None, stream=None):
     """Attention over packed sequences of different lengths. q [total_q,H_q,d], k/v
-    [total_k,H_kv,d] bf16 CUDA (any token and head strides that are multiples of 8, so slices of
-    a fused projection are taken as they are); cu_seqlens, cu_seqlens_k int32 [B+1] prefix sums
-    of the query and key counts (cu_seqlens_k None: the same). The queries of a sequence are its
+    [total_k,H_kv,d] bf16 CUDA (any token and head strides that are positive multiples of 8, so
+    slices of a fused projection are taken as they are); cu_seqlens, cu_seqlens_k int32 [B+1] prefix
+    sums of the query and key counts (cu_seqlens_k None: the same). The queries of a sequence are its
     last tokens: causal query t sees keys j <= n_k - n_q + t. A block of queries runs all its keys on
     one SM: few queries on many keys are served faster by decode or decode_tree.
 
