@@ -57,6 +57,14 @@ _SIGNATURES = {
     "gqa_attn_decode_tree_workspace_size": (_S, [_I, _I, _I, _I]),
     "gqa_attn_cache_append": (_I, [_P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _L, _L,
                                    _L, _L, _P]),
+    "gqa_attn_qk_norm_rope": (_I, [_P, _P, _P, _P, _P, _P, _I, _P, _P, _P, _I, _I, _I, _I, _I, _I,
+                                   _I, _I, _F, _L, _L, _L, _L, _L, _L, _L, _L, _P]),
+    "gqa_attn_paged_append": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I,
+                                   _L, _L, _L, _L, _L, _L, _P]),
+    "gqa_attn_paged_attention": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I,
+                                      _I, _I, _I, _L, _L, _L, _L, _I, _F, _P, _S, _P]),
+    "gqa_attn_paged_attention_workspace_size": (_S, [_I, _I, _I, _I]),
+    "gqa_attn_verify_drafts": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _L, _L, _P]),
     "gqa_attn_pick_num_splits": (_I, [_I, _I, _I, _I]),
     "gqa_attn_pick_num_splits_q8": (_I, [_I, _I, _I, _I]),
     "gqa_attn_pick_num_splits_q4": (_I, [_I, _I, _I, _I]),
@@ -648,6 +656,52 @@ def gqa_attn_cache_append(k_cache, v_cache, k_new, v_new, cu_seqlens, starts, in
                                        v_stride_t, v_stride_h, stream)
 
 
+def gqa_attn_qk_norm_rope(q, k, q_out, k_out, q_weight, k_weight, weights_fp32, positions,
+                          inv_freq, sections, axes, tokens, H_q, H_kv, d, pairs, interleaved, norm,
+                          eps, q_stride_t, q_stride_h, k_stride_t, k_stride_h, qo_stride_t,
+                          qo_stride_h, ko_stride_t, ko_stride_h, stream):
+    """``sections``: a list of host ints, or None with one axis."""
+    sec = None if sections is None else (ctypes.c_int32 * len(sections))(*sections)
+    return lib().gqa_attn_qk_norm_rope(q, k, q_out, k_out, q_weight, k_weight, weights_fp32,
+                                       positions, inv_freq, sec, axes, tokens, H_q, H_kv, d, pairs,
+                                       interleaved, norm, eps, q_stride_t, q_stride_h, k_stride_t,
+                                       k_stride_h, qo_stride_t, qo_stride_h, ko_stride_t,
+                                       ko_stride_h, stream)
+
+
+def gqa_attn_paged_append(k_pages, v_pages, k_new, v_new, cu_seqlens, starts, index, block_table,
+                          B, H_kv, d, total, total_new, num_pages, page_size, table_width,
+                          k_stride_t, k_stride_h, v_stride_t, v_stride_h, k_page_stride,
+                          v_page_stride, stream):
+    return lib().gqa_attn_paged_append(k_pages, v_pages, k_new, v_new, cu_seqlens, starts, index,
+                                       block_table, B, H_kv, d, total, total_new, num_pages,
+                                       page_size, table_width, k_stride_t, k_stride_h, v_stride_t,
+                                       v_stride_h, k_page_stride, v_page_stride, stream)
+
+
+def gqa_attn_paged_attention(q, k_pages, v_pages, o, lse, cu_seqlens, kv_lens, block_table, B, H_q,
+                             H_kv, d, total, max_tokens, max_keys, num_pages, page_size,
+                             table_width, q_stride_t, q_stride_h, k_page_stride, v_page_stride,
+                             causal, scale, workspace, workspace_bytes, stream):
+    return lib().gqa_attn_paged_attention(q, k_pages, v_pages, o, lse, cu_seqlens, kv_lens,
+                                          block_table, B, H_q, H_kv, d, total, max_tokens,
+                                          max_keys, num_pages, page_size, table_width, q_stride_t,
+                                          q_stride_h, k_page_stride, v_page_stride, causal, scale,
+                                          workspace, workspace_bytes, stream)
+
+
+def gqa_attn_paged_attention_workspace_size(H_q, H_kv, d, max_tokens):
+    return lib().gqa_attn_paged_attention_workspace_size(H_q, H_kv, d, max_tokens)
+
+
+def gqa_attn_verify_drafts(target_probs, draft_probs, draft_tokens, u_accept, u_sample, cu_seqlens,
+                           accepted, next_tokens, B, total, V, target_stride, draft_stride,
+                           stream):
+    return lib().gqa_attn_verify_drafts(target_probs, draft_probs, draft_tokens, u_accept,
+                                        u_sample, cu_seqlens, accepted, next_tokens, B, total, V,
+                                        target_stride, draft_stride, stream)
+
+
 # The checks below run on every call of a serving step whose kernels take a few microseconds, so
 # they ask each tensor as little as they can (get_device is -1 for a CPU tensor).
 
@@ -888,6 +942,274 @@ def cache_append(k_cache, v_cache, k_new, v_new, starts, *, cu_seqlens=None, ind
         raise GqaError(rc, "gqa_attn_cache_append")
     if stream is not None:
         _in_use(torch, dev, stream, k_cache, v_cache, k_new, v_new, starts, cu_seqlens, index)
+
+
+def _like(torch, name, t, given, dtype, shape, stream):
+    """An output: the caller's, checked, or a new one from the launch stream's pool."""
+    if given is not None:
+        if (given.dtype is not dtype or given.shape != shape or not given.is_contiguous()
+                or given.get_device() != t.get_device()):
+            raise ValueError(f"{name} must be a contiguous {dtype} tensor of {tuple(shape)} on "
+                             f"{t.device}")
+        return given
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=t.device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=t.device)
+
+
+def _floats(torch, name, t, n, device):
+    if not isinstance(t, torch.Tensor) or t.dtype is not torch.float32 or not t.is_contiguous():
+        raise TypeError(f"{name} must be a contiguous float32 CUDA tensor")
+    if t.get_device() != device:
+        raise ValueError(f"{name} must be on cuda:{device}, got {t.device}")
+    if t.numel() != n:
+        raise ValueError(f"{name} must have {n} elements, got {t.numel()}")
+    return t.data_ptr()
+
+
+def _pages(torch, k_pages, v_pages, block_table, H_kv, d, device):
+    """Checks pages [num_pages, H_kv, page_size, d] and the block table [B, width]; returns
+    (B, num_pages, page_size, width, K page stride, V page stride)."""
+    for name, t in (("k_pages", k_pages), ("v_pages", v_pages)):
+        if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype is not torch.bfloat16:
+            raise TypeError(f"{name} must be a bfloat16 CUDA tensor")
+        if t.get_device() != device:
+            raise ValueError(f"{name} must be on cuda:{device}, got {t.device}")
+    shape = k_pages.shape
+    if (len(shape) != 4 or v_pages.shape != shape or (H_kv is not None and shape[1] != H_kv)
+            or shape[3] != d):
+        raise ValueError(f"k_pages, v_pages must be [num_pages, {H_kv or 'H_kv'}, page_size, {d}]")
+    n, heads, size, _ = shape
+    for name, t in (("k_pages", k_pages), ("v_pages", v_pages)):
+        _, sh, ss, sd = t.stride()
+        if sd != 1 or (size > 1 and ss != d) or (heads > 1 and sh != size * d):
+            raise ValueError(f"every page of {name} must be contiguous")
+    if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
+        raise TypeError("block_table must be a contiguous int32 [B, width] CUDA tensor")
+    B, width = block_table.shape
+    _ints(torch, "block_table", block_table, B * width, device)
+    return B, n, size, width, k_pages.stride(0), v_pages.stride(0)
+
+
+def qk_norm_rope(q, k, positions, inv_freq, *, q_weight=None, k_weight=None,
+                 eps: float | None = 1e-6, sections=None, interleaved: bool = False, q_out=None,
+                 k_out=None, stream=None):
+    """Norm and rotation of queries q [tokens,H_q,d] and keys k [tokens,H_kv,d] (bf16, strides as
+    prefill_packed; k None: queries alone) in one pass. Every head is divided by its root mean
+    square sqrt(mean + eps) and multiplied by q_weight / k_weight ([d] bf16 or float32, None: 1);
+    eps None leaves the norm and the weights out. Pair i of the inv_freq.numel() pairs of channels,
+    (i, i + pairs) or with interleaved (2i, 2i + 1), is then turned by positions * inv_freq[i]
+    (float32 [pairs], a multiple of 8 up to d / 2); the channels behind them are left as they are.
+
+    positions: int32 [tokens], or [axes,tokens] with sections, a tuple of the numbers of pairs that
+    each axis turns (time, height and width of images and video; at most 4). q_out, k_out may be q
+    and k themselves. Returns (q_out, k_out), new contiguous tensors by default. ``stream`` as
+    prefill_packed."""
+    import torch
+
+    qs, qh = _packed(torch, "q", q, None, None, None)
+    n, H_q, d = q.shape
+    dev = q.get_device()
+    ks = kh = kos = koh = 8
+    H_kv = 0
+    if k is not None:
+        ks, kh = _packed(torch, "k", k, None, d, dev)
+        H_kv = k.shape[1]
+        if k.shape[0] != n:
+            raise ValueError("q and k must have the same tokens")
+        if H_kv == 0:
+            raise ValueError("k has no heads")
+    elif k_out is not None or k_weight is not None:
+        raise ValueError("k_out and k_weight need k")
+    pairs = inv_freq.numel() if isinstance(inv_freq, torch.Tensor) else 0
+    freq = _floats(torch, "inv_freq", inv_freq, pairs, dev)
+    axes, sec = 1, None
+    if sections is not None:
+        axes = len(sections)
+        sec = (ctypes.c_int32 * axes)(*sections)
+    pos = _ints(torch, "positions", positions, axes * n, dev)
+    if positions.shape != ((n,) if sections is None else (axes, n)):
+        raise ValueError(f"positions must be {'[tokens]' if sections is None else '[axes, tokens]'}"
+                         f", got {tuple(positions.shape)}")
+    wide = None
+    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if w is None:
+            continue
+        if not isinstance(w, torch.Tensor) or w.dtype not in (torch.bfloat16, torch.float32):
+            raise TypeError(f"{name} must be a bfloat16 or float32 CUDA tensor")
+        if w.get_device() != dev or w.shape != (d,) or w.stride(0) != 1:
+            raise ValueError(f"{name} must be a contiguous [{d}] tensor on cuda:{dev}")
+        if wide is not None and wide != (w.dtype is torch.float32):
+            raise TypeError("q_weight and k_weight must have one type")
+        wide = w.dtype is torch.float32
+    if eps is None and wide is not None:
+        raise ValueError("weights need the norm (eps)")
+    if q_out is None:
+        q_out = _like(torch, "q_out", q, None, torch.bfloat16, q.shape, stream)
+    elif q_out.shape != q.shape:
+        raise ValueError("q_out must be shaped like q")
+    qos, qoh = _packed(torch, "q_out", q_out, H_q, d, dev)
+    if k is not None:
+        if k_out is None:
+            k_out = _like(torch, "k_out", k, None, torch.bfloat16, k.shape, stream)
+        elif k_out.shape != k.shape:
+            raise ValueError("k_out must be shaped like k")
+        kos, koh = _packed(torch, "k_out", k_out, H_kv, d, dev)
+    rc = _on_device(torch, dev, lambda: lib().gqa_attn_qk_norm_rope(
+        q.data_ptr(), _ptr(k), q_out.data_ptr(), _ptr(k_out), _ptr(q_weight), _ptr(k_weight),
+        1 if wide else 0, pos, freq, sec, axes, n, H_q, H_kv, d, pairs, 1 if interleaved else 0,
+        0 if eps is None else 1, 0.0 if eps is None else float(eps), qs, qh, ks, kh, qos, qoh, kos,
+        koh, _raw_stream(torch, dev, stream)))
+    if rc != GQA_OK:
+        raise GqaError(rc, "gqa_attn_qk_norm_rope")
+    if stream is not None:
+        _in_use(torch, dev, stream, q, k, positions, inv_freq, q_weight, k_weight, q_out, k_out)
+    return q_out, k_out
+
+
+def paged_append(k_pages, v_pages, k_new, v_new, block_table, starts, *, cu_seqlens=None,
+                 index=None, stream=None):
+    """cache_append over pages k_pages/v_pages [num_pages,H_kv,page_size,d] (each page contiguous;
+    page_size 16, 32, 64 or a multiple of 128): slot s of row b lies in page
+    block_table[b, s // page_size] (int32 [B,width])."""
+    import torch
+
+    ks, kh = _packed(torch, "k_new", k_new, None, None, None)
+    total_new, H_kv, d = k_new.shape
+    dev = k_new.get_device()
+    vs, vh = _packed(torch, "v_new", v_new, H_kv, d, dev)
+    if v_new.shape[0] != total_new:
+        raise ValueError("k_new and v_new must have the same shape")
+    B, n, size, width, kp, vp = _pages(torch, k_pages, v_pages, block_table, H_kv, d, dev)
+    first = _ints(torch, "starts", starts, B, dev)
+    total, idx, cu = total_new, None, None
+    if index is not None:
+        total = index.numel() if isinstance(index, torch.Tensor) else 0
+        idx = _ints(torch, "index", index, total, dev)
+    if cu_seqlens is not None:
+        cu = _ints(torch, "cu_seqlens", cu_seqlens, B + 1, dev)
+    elif B == 0 or total % B:
+        raise ValueError("without cu_seqlens every row has the same number of entries")
+    rc = _on_device(torch, dev, lambda: lib().gqa_attn_paged_append(
+        k_pages.data_ptr(), v_pages.data_ptr(), k_new.data_ptr(), v_new.data_ptr(), cu, first, idx,
+        block_table.data_ptr(), B, H_kv, d, total, total_new, n, size, width, ks, kh, vs, vh, kp,
+        vp, _raw_stream(torch, dev, stream)))
+    if rc != GQA_OK:
+        raise GqaError(rc, "gqa_attn_paged_append")
+    if stream is not None:
+        _in_use(torch, dev, stream, k_pages, v_pages, k_new, v_new, block_table, starts, cu_seqlens,
+                index)
+
+
+def paged_attention(q, k_pages, v_pages, block_table, kv_lens, *, cu_seqlens=None,
+                    max_tokens: int | None = None, max_keys: int | None = None,
+                    causal: bool = True, scale: float | None = None, out=None, lse=None,
+                    stream=None, workspace=None):
+    """Attention of new tokens over pages (as paged_append) that hold them already: row b has
+    kv_lens[b] keys (int32 [B]), the last of them those of its T tokens in q [total,H_q,d] (prefix
+    sums cu_seqlens int32 [B+1]; None: total / B per row). Token t sees the keys
+    j <= kv_lens[b] - T + t (causal) or all of them. A call may mix single tokens, drafted tokens in
+    a line and chunks of prompts. max_tokens bounds T; it is needed with cu_seqlens, whose values
+    stay on the device. max_keys bounds kv_lens (None: what the table holds); up to 512 saves a
+    kernel.
+
+    Returns (o [total,H_q,d] bf16, lse [total,H_q] fp32). ``workspace``: a uint8 CUDA tensor of
+    gqa_attn_paged_attention_workspace_size bytes that no overlapping call uses; by default one is
+    allocated for the call. ``stream`` as prefill_packed."""
+    import torch
+
+    qs, qh = _packed(torch, "q", q, None, None, None)
+    total, H_q, d = q.shape
+    dev = q.get_device()
+    B, n, size, width, kp, vp = _pages(torch, k_pages, v_pages, block_table, None, d, dev)
+    H_kv = k_pages.shape[1]
+    lens = _ints(torch, "kv_lens", kv_lens, B, dev)
+    cu = None
+    if cu_seqlens is not None:
+        cu = _ints(torch, "cu_seqlens", cu_seqlens, B + 1, dev)
+        if max_tokens is None:
+            raise ValueError("max_tokens is needed with cu_seqlens")
+    else:
+        if B == 0 or total % B:
+            raise ValueError("without cu_seqlens every row has total / B tokens")
+        max_tokens = max(1, total // B) if max_tokens is None else max_tokens
+    if max_keys is not None and max_keys < 1:
+        raise ValueError("max_keys must be positive")
+    out, lse = _outputs(torch, q, out, lse, stream)
+    sc = 1.0 / math.sqrt(d) if scale is None else float(scale)
+    given = workspace
+    if workspace is None:
+        # from the launch stream's pool: its memory is reused only behind this call
+        need = lib().gqa_attn_paged_attention_workspace_size(H_q, H_kv, d, max_tokens)
+        workspace = _like(torch, "workspace", q, None, torch.uint8, (need,), stream)
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be contiguous and on cuda:{dev}")
+    rc = _on_device(torch, dev, lambda: lib().gqa_attn_paged_attention(
+        q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), out.data_ptr(), lse.data_ptr(), cu,
+        lens, block_table.data_ptr(), B, H_q, H_kv, d, total, max_tokens, max_keys or 0, n, size,
+        width, qs, qh, kp, vp, 1 if causal else 0, sc, workspace.data_ptr(),
+        workspace.numel() * workspace.element_size(), _raw_stream(torch, dev, stream)))
+    if rc != GQA_OK:
+        raise GqaError(rc, "gqa_attn_paged_attention")
+    if stream is not None:
+        _in_use(torch, dev, stream, q, k_pages, v_pages, out, lse, block_table, kv_lens, cu_seqlens,
+                given)
+    return out, lse
+
+
+def verify_drafts(target_probs, draft_tokens, u_accept, u_sample, cu_seqlens=None, *,
+                  draft_probs=None, accepted=None, next_tokens=None, stream=None):
+    """Which drafted tokens stand, and the token that follows them (speculative sampling). Row b's
+    drafted tokens are packed in draft_tokens (int32 [total]; prefix sums cu_seqlens int32 [B+1],
+    None: total / B per row), their draft distributions in draft_probs [total,V] float32 (None: each
+    draft was certain), the target's in target_probs [total + B,V] float32, n + 1 for a row of n
+    drafts. Draft i stands if u_accept[i] * q(x) < p(x) (float32 [total], from [0, 1)) and all
+    before it stand; the next token is drawn with u_sample (float32 [B]) from max(p - q, 0) where
+    the first one falls, or from the last p, as the lowest token whose cumulative sum is above
+    u_sample times the sum.
+
+    Returns (accepted, next_tokens), int32 [B]. ``stream`` as prefill_packed."""
+    import torch
+
+    for name, t in (("target_probs", target_probs), ("draft_probs", draft_probs)):
+        if t is None and name == "draft_probs":
+            continue
+        if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype is not torch.float32:
+            raise TypeError(f"{name} must be a float32 CUDA tensor")
+        if t.dim() != 2 or t.shape[1] != target_probs.shape[1]:
+            raise ValueError("target_probs and draft_probs must be [rows, V]")
+        if t.stride(1) != 1 and t.shape[1] > 1:
+            raise ValueError(f"the last dimension of {name} must be contiguous")
+    dev = target_probs.get_device()
+    rows, V = target_probs.shape
+    total = draft_tokens.numel() if isinstance(draft_tokens, torch.Tensor) else 0
+    toks = _ints(torch, "draft_tokens", draft_tokens, total, dev)
+    B = rows - total
+    if B < 0:
+        raise ValueError("target_probs must have a row for every drafted token and one per row")
+    ua = _floats(torch, "u_accept", u_accept, total, dev)
+    us = _floats(torch, "u_sample", u_sample, B, dev)
+    cu = None
+    if cu_seqlens is not None:
+        cu = _ints(torch, "cu_seqlens", cu_seqlens, B + 1, dev)
+    elif B == 0 or total % B:
+        raise ValueError("without cu_seqlens every row has the same number of drafted tokens")
+    if draft_probs is not None and (draft_probs.shape[0] != total
+                                    or draft_probs.get_device() != dev):
+        raise ValueError(f"draft_probs must have {total} rows and be on cuda:{dev}")
+    accepted = _like(torch, "accepted", target_probs, accepted, torch.int32, (B,), stream)
+    next_tokens = _like(torch, "next_tokens", target_probs, next_tokens, torch.int32, (B,), stream)
+    rc = _on_device(torch, dev, lambda: lib().gqa_attn_verify_drafts(
+        target_probs.data_ptr(), _ptr(draft_probs), toks, ua, us, cu, accepted.data_ptr(),
+        next_tokens.data_ptr(), B, total, V, target_probs.stride(0),
+        draft_probs.stride(0) if draft_probs is not None else V, _raw_stream(torch, dev, stream)))
+    if rc != GQA_OK:
+        raise GqaError(rc, "gqa_attn_verify_drafts")
+    if stream is not None:
+        _in_use(torch, dev, stream, target_probs, draft_probs, draft_tokens, u_accept, u_sample,
+                cu_seqlens, accepted, next_tokens)
+    return accepted, next_tokens
 
 
 def check(stream=None):

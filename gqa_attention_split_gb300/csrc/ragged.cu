@@ -93,7 +93,14 @@ constexpr float kRescaleThreshold = 8.f;
 // groups take alternate K/V tiles and are merged in the epilogue (28/4 heads,
 // 5 drafts, contexts of 64 to 9100: 19.0 us against 19.9 as kTreePair, whose
 // second group would be empty).
-enum Mode { kPrompts, kTreePair, kTreeAlt };
+// kPagedPair: items are blocks of 2 * tok tokens of a row, a range of the row's
+// keys, which all lie in pages.
+// kPagedAlt: the same where all tokens of a row fit in one group, with the tiles
+// taken in turn as in kTreeAlt.
+enum Mode { kPrompts, kTreePair, kTreeAlt, kPagedPair, kPagedAlt };
+constexpr bool tree_mode(int m) { return m == kTreePair || m == kTreeAlt; }
+constexpr bool paged_mode(int m) { return m == kPagedPair || m == kPagedAlt; }
+constexpr bool alt_mode(int m) { return m == kTreeAlt || m == kPagedAlt; }
 
 struct Params {
     const uint16_t* v;            // packed V, read again only for values that are not finite
@@ -113,7 +120,13 @@ struct Params {
     int tok;          // tokens of a group
     int team;         // decode_tree: CTAs that share a range of keys, one per token block
     int n_teams, part_rows;
-    int whole;        // decode_tree: no (row, KV head) is cut
+    int whole;        // decode_tree, paged_attention: no unit is cut
+    // paged_attention: ctx holds the rows' key counts, S_max is the most of them
+    const int32_t* table;         // [B, table_width]: the pages of each row
+    const uint16_t* v_pages;      // V pages, read again only for values that are not finite
+    int64_t v_page;               // elements from one V page to the next
+    int table_width, page_size, num_pages;
+    int single;       // no row has more than one block of tokens
     float scale_log2;
     int inject_timeout;  // test hook: block 0 withholds its first Q copy
 };
@@ -178,23 +191,23 @@ __device__ __forceinline__ int tree_tiles(int T, int ctx) {
 
 // ---- limits of an item, as every role needs them
 
-// Own keys visible to token t (kPrompts).
+// Own keys visible to token t (kPrompts, kPaged*).
 __device__ __forceinline__ int token_limit(const Params& p, const Item& w, int t) {
     return p.causal ? clampi(w.off + t + 1, 0, w.n_own) : w.n_own;
 }
 // Own keys that every row of group g sees / that some row of it sees.
 template <int kMode>
 __device__ __forceinline__ int group_first(const Params& p, const Item& w, int g) {
-    return kMode == kPrompts ? token_limit(p, w, w.tok0 + g * p.tok) : 0;
+    return !tree_mode(kMode) ? token_limit(p, w, w.tok0 + g * p.tok) : 0;
 }
 template <int kMode>
 __device__ __forceinline__ int group_last(const Params& p, const Item& w, int g) {
-    return kMode == kPrompts ? token_limit(p, w, min(w.T, w.tok0 + (g + 1) * p.tok) - 1) : w.n_own;
+    return !tree_mode(kMode) ? token_limit(p, w, min(w.T, w.tok0 + (g + 1) * p.tok) - 1) : w.n_own;
 }
 // Keys of tile jj that some row of group g sees (1..128).
 template <int kMode>
 __device__ __forceinline__ int tile_keys(const Params& p, const Item& w, int jj, int g) {
-    if (kMode != kPrompts && jj < w.c_t) return min(BN, w.ctx - jj * BN);
+    if (tree_mode(kMode) && jj < w.c_t) return min(BN, w.ctx - jj * BN);
     return clampi(group_last<kMode>(p, w, g) - (jj - w.c_t) * BN, 0, BN);
 }
 // The same value in every lane, in a form that the compiler knows to be so:
@@ -206,7 +219,7 @@ __device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, 
 // it) sees whole: no mask, no repair, all 128 keys.
 template <int kMode>
 __device__ __forceinline__ int plain_tiles(const Params& p, const Item& w, int g) {
-    const int whole = (kMode == kPrompts ? group_first<kMode>(p, w, g) : w.ctx) / BN;
+    const int whole = (!tree_mode(kMode) ? group_first<kMode>(p, w, g) : w.ctx) / BN;
     return clampi(whole - w.j0, 0, w.n);
 }
 // The keys of V tile jj that the P V products read are [0, end). Those from
@@ -216,11 +229,11 @@ struct Repair {
 };
 template <int kMode>
 __device__ __forceinline__ Repair repair_of(const Params& p, const Item& w, int jj) {
-    const int last = kMode == kPrompts && w.n1 > 0 ? 1 : 0;  // the group that sees more
+    const int last = !tree_mode(kMode) && w.n1 > 0 ? 1 : 0;  // the group that sees more
     Repair r;
     r.keys = tile_keys<kMode>(p, w, jj, last);
     r.end = (r.keys + 15) & ~15;
-    r.seen = kMode != kPrompts && jj < w.c_t
+    r.seen = tree_mode(kMode) && jj < w.c_t
                  ? r.keys
                  : clampi(group_first<kMode>(p, w, 0) - (jj - w.c_t) * BN, 0, r.keys);
     return r;
@@ -597,6 +610,261 @@ __device__ __forceinline__ void schedule_tree(const Params& p, Publisher& pub, i
     pub.put(stop, lane);
 }
 
+// paged_attention. A unit is a block of tokens of a row against one KV head: tiles
+// 0 .. N - 1 of 128 keys, N from the keys that its last token sees. The units lie in
+// one line, rows one behind the other, their KV heads, their blocks; a unit is as long
+// as its keys and kPagedItemCost of them. The line is cut into equal shares, one to a
+// CTA, so that a step with chunks, drafts and single tokens at once is balanced
+// whatever its lengths. Where a cut falls inside a unit it moves to the nearest
+// boundary of tiles. The blocks' lengths in the line grow evenly (a causal limit) up
+// to the last, so sums over them have a closed form and nothing is stored.
+// When every row has one block only and the units can be cut into equal parts, one
+// part to a CTA at most, that is done instead (see schedule_tree).
+constexpr int kPagedItemCost = kItemCost * BN;
+constexpr int kPagedShare = 3 * BN;  // least length of a share: two tiles of any unit it crosses
+
+struct PagedRow {
+    int q0, T, n, blocks;
+    int64_t line;  // length of its blocks against one KV head
+};
+__device__ __forceinline__ int64_t paged_limit(const Params& p, const PagedRow& r, int i) {
+    if (!p.causal || i + 1 >= r.blocks) return r.n;
+    return max(0, r.n - r.T + (i + 1) * 2 * p.tok);
+}
+// Length of the first k blocks of a row.
+__device__ __forceinline__ int64_t paged_line(const Params& p, const PagedRow& r, int k) {
+    int64_t sum = int64_t(k) * kPagedItemCost;
+    if (!p.causal) return sum + int64_t(k) * r.n;
+    const int64_t block = 2 * p.tok, off = r.n - r.T;
+    if (k == r.blocks && k > 0) {
+        sum += r.n;
+        --k;
+    }
+    // the blocks before `none` see no key
+    const int64_t none = off < 0 ? min(-off / block, int64_t(k)) : 0;
+    return sum + (k - none) * off + block * (int64_t(k) * (k + 1) - none * (none + 1)) / 2;
+}
+__device__ __forceinline__ PagedRow paged_row(const Params& p, int b, bool& bad) {
+    PagedRow r{0, 0, 0, 0, 0};
+    if (b >= p.B) return r;
+    const int keys = p.ctx[b];
+    row_range(p.cu_q, p.B, p.total_q, b, r.q0, r.T, bad);
+    if (r.T > p.max_tokens) {
+        r.T = p.max_tokens;
+        bad = true;
+    }
+    r.n = clampi(keys, 0, p.S_max);
+    bad = bad || r.n != keys;
+    r.blocks = cdiv(r.T, 2 * p.tok);
+    r.line = paged_line(p, r, r.blocks);
+    return r;
+}
+
+__device__ __forceinline__ int64_t warp_sum64(int64_t x) {
+    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    return x;
+}
+
+__device__ __forceinline__ void schedule_paged(const Params& p, Publisher& pub, int lane) {
+    bool bad = false;
+    const int ctas = gridDim.x, cta = blockIdx.x;
+    if (!p.whole && lane == 0) p.part_info[cta] = make_int4(0, 0, 0, 0);
+    const PagedRow row_0 = paged_row(p, lane, bad);  // the first 32 rows stay in registers
+    auto row_of = [&](int b0) { return b0 == 0 ? row_0 : paged_row(p, b0 + lane, bad); };
+    int64_t total = 0;
+    int tiles = 0, units = 0;
+    for (int b0 = 0; b0 < p.B; b0 += 32) {
+        const PagedRow r = row_of(b0);
+        total += r.line * p.H_kv;
+        units += r.blocks * p.H_kv;
+        if (p.single) tiles += r.blocks * cdiv(r.n, BN) * p.H_kv;
+    }
+    total = warp_sum64(total);
+    if (bad && cta == 0) atomicOr(p.status, kStatusBadSeqlen);
+    // Units in equal parts, at most one to a CTA?
+    int even = 0;
+    if (p.single && !p.whole) {
+        tiles = __reduce_add_sync(0xffffffffu, tiles);
+        units = __reduce_add_sync(0xffffffffu, units);
+        if (units <= ctas) {
+            const int most = max(1, cdiv(tiles, ctas));
+            int parts = 0;
+            for (int b0 = 0; b0 < p.B; b0 += 32) {
+                const PagedRow r = row_of(b0);
+                parts += r.blocks * p.H_kv * max(1, cdiv(cdiv(r.n, BN), most));
+            }
+            if (__reduce_add_sync(0xffffffffu, parts) <= ctas) even = most;
+        }
+    }
+    // This CTA's share [x, end) of the line (whole, even: of the numbered units or parts).
+    const int64_t shares = max(int64_t(1), min(int64_t(ctas), total / kPagedShare));
+    const bool counted = p.whole || even;
+    const int64_t x0 = counted ? cta : cta < shares ? total * cta / shares : total;
+    const int64_t x1 = p.whole ? INT64_MAX : even ? cta + 1
+                       : cta < shares             ? total * (cta + 1) / shares
+                                                  : total;
+    int64_t x = x0, before = 0;  // length of the rows before b0
+    for (int b0 = 0; b0 < p.B && x < x1; b0 += 32) {
+        const PagedRow mine = row_of(b0);
+        const int per_unit = even ? max(1, cdiv(cdiv(mine.n, BN), even)) : 1;  // parts
+        const int64_t len = counted ? int64_t(mine.blocks) * p.H_kv * per_unit : mine.line * p.H_kv;
+        int64_t sum = len;  // inclusive prefix sum over the lanes
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t y = __shfl_up_sync(0xffffffffu, sum, o);
+            if (lane >= o) sum += y;
+        }
+        const int64_t all = __shfl_sync(0xffffffffu, sum, 31);
+        while (x < x1 && x < before + all) {
+            const int src = __ffs(__ballot_sync(0xffffffffu, before + sum > x)) - 1;
+            PagedRow r;
+            r.q0 = __shfl_sync(0xffffffffu, mine.q0, src);
+            r.T = __shfl_sync(0xffffffffu, mine.T, src);
+            r.n = __shfl_sync(0xffffffffu, mine.n, src);
+            r.blocks = __shfl_sync(0xffffffffu, mine.blocks, src);
+            r.line = __shfl_sync(0xffffffffu, mine.line, src);
+            const int cuts = __shfl_sync(0xffffffffu, per_unit, src);
+            const int64_t start = before + __shfl_sync(0xffffffffu, sum - len, src);
+            const int64_t at = x - start;
+            Item w{};
+            w.b = b0 + src;
+            int block, parts = 1;
+            int64_t s = 0;  // (line) start of the unit
+            if (counted) {
+                const int unit = int(at / cuts);
+                w.kvh = unit / r.blocks;
+                block = unit % r.blocks;
+            } else {
+                w.kvh = int(at / r.line);
+                const int64_t rest = at - w.kvh * r.line;
+                int lo = 0, hi = r.blocks;  // the block with line(lo) <= rest < line(lo + 1)
+                while (hi - lo > 1) {
+                    const int mid = (lo + hi) >> 1;
+                    if (paged_line(p, r, mid) <= rest) lo = mid;
+                    else hi = mid;
+                }
+                block = lo;
+                s = start + w.kvh * r.line + paged_line(p, r, block);
+            }
+            const int limit = int(paged_limit(p, r, block));
+            const int tiles_of = cdiv(limit, BN);
+            int j1 = tiles_of;
+            bool take = true;
+            if (p.whole) {
+                x += ctas;
+            } else if (even) {
+                const int i = int(at % cuts);
+                w.j0 = int(int64_t(tiles_of) * i / cuts);
+                j1 = int(int64_t(tiles_of) * (i + 1) / cuts);
+                parts = cuts;
+                ++x;
+            } else {
+                const int64_t keys_at = s + kPagedItemCost, stop = keys_at + limit;
+                // tiles of the unit before a cut at y
+                auto before_cut = [&](int64_t y) {
+                    if (y >= stop) return tiles_of;
+                    const int64_t t = (y - keys_at + BN / 2) >> 7;
+                    return int(min(max(t, int64_t(0)), int64_t(tiles_of)));
+                };
+                w.j0 = before_cut(x0);
+                j1 = before_cut(x1);
+                if (tiles_of == 0) {
+                    take = s >= x0;  // the CTA in whose share it begins
+                } else {
+                    take = j1 > w.j0;
+                    // the shares that hold its first and its last tile: the first c
+                    // whose end, floor(total (c + 1) / shares), is not before the cut
+                    auto share_of = [&](int64_t y) {
+                        return (y * shares + total - 1) / total - 1;
+                    };
+                    const int64_t first = share_of(min(keys_at + BN / 2, stop));
+                    const int64_t last =
+                        share_of(min(keys_at + int64_t(tiles_of) * BN - BN / 2, stop));
+                    parts = int(last - first) + 1;
+                }
+                x = stop;  // the next unit of the line
+            }
+            w.q_row = r.q0;
+            w.T = r.T;
+            w.n_own = r.n;
+            w.off = r.n - r.T;
+            w.tok0 = block * 2 * p.tok;
+            w.n = j1 - w.j0;
+            w.n0 = clampi(cdiv(group_last<kPagedPair>(p, w, 0), BN) - w.j0, 0, w.n);
+            w.n1 = w.tok0 + p.tok < w.T ? w.n : 0;
+            if (!take || (w.n == 0 && tiles_of > 0)) continue;
+            // slot 2c + 1 holds the first part of a unit, 2c another one
+            w.dst = parts == 1 ? -1 : 2 * cta + (w.j0 == 0);
+            if (parts > 1 && w.j0 == 0 && lane == 0)
+                p.part_info[cta] =
+                    make_int4(w.q_row + w.tok0, min(w.T - w.tok0, 2 * p.tok) * p.G, w.kvh, parts);
+            if (!pub.put(w, lane)) return;
+        }
+        before += all;
+    }
+    Item end{};
+    end.n = -1;
+    pub.put(end, lane);
+}
+
+// Copies the K and V tiles of an item from their pages into the ring: a box of a page
+// (or 128 keys of it) and 64 columns for each lane, so that a tile of 16-key pages is in
+// flight with one instruction. The ids of up to 32 pages are read one window ahead of
+// their use. Keys behind the row's last page are not read: what their place in the tile
+// holds gives scores that are masked, and the P V product does not reach them. A page
+// id out of range gives zeros and is reported.
+template <int kBoxes>
+__device__ __forceinline__ void load_pages(const Params& p, const Item& w, int n, int lane,
+                                           const CUtensorMap* tmap_k, const CUtensorMap* tmap_v,
+                                           uint64_t policy, uint64_t* bars, uint32_t ring,
+                                           uint32_t tile_bytes, int r, int& issued, bool& alive) {
+    const int rows = min(p.page_size, BN);       // keys of a box
+    const int per_tile = BN / rows;              // boxes of a tile and 64 columns
+    const int per_page = max(1, p.page_size / BN);  // tiles of a page
+    const int first = per_page > 1 ? w.j0 / per_page : w.j0 * per_tile;
+    const int pages = cdiv(w.n_own, p.page_size);
+    const int32_t* table = p.table + size_t(w.b) * p.table_width;
+    auto fetch = [&](int window) {
+        const int i = first + window * 32 + lane;
+        return i < pages ? table[i] : 0;
+    };
+    const int box = lane % per_tile, half = lane / per_tile;
+    int window = 0, ids = fetch(0), next = fetch(1);
+#pragma unroll 1
+    for (int j = 0; j < n && alive; ++j) {
+        const int jj = w.j0 + j;
+        const int at = (per_page > 1 ? jj / per_page : jj * per_tile) - first;
+        if ((at >> 5) != window) {
+            ++window;
+            ids = next;
+            next = fetch(window + 1);
+        }
+        int page = __shfl_sync(0xffffffffu, ids, (at + box) & 31);
+        const int slot = per_page > 1 ? jj % per_page * BN : 0;
+        const int boxes = min(per_tile, cdiv(w.n_own - jj * BN, rows));
+        if (page < 0 || page >= p.num_pages) {
+            if (box < boxes && half < kBoxes) atomicOr(p.status, kStatusBadSeqlen);
+            page = p.num_pages;  // outside the tensor: zeros
+        }
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv) {
+            const int ri = r + 2 * j + kv, s = ri % kRingSlots;
+            const uint32_t full = smem_u32(&bars[bSlotFull + s]);
+            if (lane == 0) {
+                if (ri >= kRingSlots)
+                    alive = mbar_wait_bounded(smem_u32(&bars[bSlotEmpty + s]),
+                                              ((ri / kRingSlots) - 1) & 1, p.status);
+                if (alive) mbar_arrive_expect_tx(full, uint32_t(boxes * rows * 128 * kBoxes));
+            }
+            alive = __all_sync(0xffffffffu, alive);
+            if (!alive) break;
+            if (box < boxes && half < kBoxes)
+                tma_load_4d(ring + s * tile_bytes + half * kBoxBytes + box * rows * 128,
+                            kv ? tmap_v : tmap_k, half * 64, slot, w.kvh, page, full, policy);
+            issued = ri + 1;
+        }
+    }
+}
+
 // ---- softmax of one tile of scores
 
 struct RowState {
@@ -706,7 +974,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                   const __grid_constant__ CUtensorMap tmap_vc, const Params p) {
     using Gm = Geo<D>;
     constexpr uint32_t kTileBytes = Gm::kTileBytes;
-    constexpr bool kTree = kMode != kPrompts, kAlt = kMode == kTreeAlt;
+    constexpr bool kTree = tree_mode(kMode), kPaged = paged_mode(kMode), kAlt = alt_mode(kMode);
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                ~uintptr_t(1023));
@@ -753,9 +1021,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc::fence_after_sync();
     if (threadIdx.x == 0) {
         tma_prefetch_desc(&tmap_q);
-        tma_prefetch_desc(&tmap_k);
-        tma_prefetch_desc(&tmap_v);
-        if (kTree) {
+        if (!kPaged) {
+            tma_prefetch_desc(&tmap_k);
+            tma_prefetch_desc(&tmap_v);
+        }
+        if (kTree || kPaged) {
             tma_prefetch_desc(&tmap_kc);
             tma_prefetch_desc(&tmap_vc);
         }
@@ -789,7 +1059,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         // A context streams through L2 once (for all members of a team at the same
         // time): it leaves room for what is read again, code and partial results
         // among it.
-        const uint64_t once = l2_policy_evict_first();
+        // Pages are read once when no row has a second block of tokens.
+        const uint64_t once =
+            kPaged && !p.single ? l2_policy_evict_normal() : l2_policy_evict_first();
         int r = 0, q_loads = 0;  // ring items and Q loads before this item
         int issued = 0;          // ring items this lane issued
         bool withheld = false;
@@ -816,7 +1088,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                      bar(bQFull));
                 }
 #pragma unroll 1
-                for (int i = 0; i < 2 * n && alive; ++i) {  // K_0, V_0, K_1, V_1, ...
+                for (int i = 0; !kPaged && i < 2 * n && alive; ++i) {  // K_0, V_0, K_1, V_1, ...
                     const int ri = r + i, s = ri % kRingSlots;
                     if (ri >= kRingSlots)
                         alive = mbar_wait_bounded(bar(bSlotEmpty + s), ((ri / kRingSlots) - 1) & 1,
@@ -836,6 +1108,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     issued = ri + 1;
                 }
+            }
+            if constexpr (kPaged) {
+                alive = __all_sync(0xffffffffu, alive);
+                load_pages<Gm::kBoxes>(p, w, n, lane, &tmap_kc, &tmap_vc, once, bars, smem_u32(smem + Gm::kRingOff),
+                                       kTileBytes, r, issued, alive);
             }
             if (!withheld) ++q_loads;
             if (!__all_sync(0xffffffffu, alive) || withheld) break;
@@ -898,11 +1175,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             // drafted tokens' tile (decode_tree) may count with fewer
             const int plain = uniform(plain_tiles<kMode>(p, w, 0));
             const int j_own = uniform(w.c_t - w.j0);
-            const int k0 = uniform(kMode == kPrompts ? tile_keys<kMode>(p, w, n0 - 1, 0) : w.n_own);
-            const int k1 = uniform(kMode == kPrompts ? tile_keys<kMode>(p, w, n1 - 1, 1)
-                                                     : w.ctx - (w.c_t - 1) * BN);
+            const int k0 = uniform(
+                kTree ? w.n_own : tile_keys<kMode>(p, w, w.j0 + (kAlt ? n : n0) - 1, 0));
+            const int k1 = uniform(kTree ? w.ctx - (w.c_t - 1) * BN
+                                         : tile_keys<kMode>(p, w, w.j0 + n1 - 1, 1));
             auto keys_of = [&](int j, int g) {
-                if (kMode == kPrompts) return j + 1 < (g ? n1 : n0) ? BN : (g ? k1 : k0);
+                if (kPaged && kAlt) return j + 1 < n ? BN : k0;
+                if (!kTree) return j + 1 < (g ? n1 : n0) ? BN : (g ? k1 : k0);
                 return j < plain ? BN : (j < j_own ? k1 : k0);
             };
             // The repair of V tile j may start once V tile j - 2, which had its
@@ -1035,6 +1314,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         Publisher pub{smem + Gm::kItemOff, bars, p.status};
         if constexpr (kTree)
             schedule_tree<kMode>(p, pub, lane);
+        else if constexpr (kPaged)
+            schedule_paged(p, pub, lane);
         else
             schedule_prompts(p, reinterpret_cast<int2*>(smem + Gm::kSeqOff), pub, lane);
       } else {
@@ -1156,8 +1437,21 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int ng = uniform(kAlt ? (w.n + 1 - g) >> 1 : (g ? w.n1 : w.n0));
             // some row of this warp is valid
             const bool act = __any_sync(0xffffffffu, row_tok < count);
-            if (kMode == kPrompts && ng == 0) {  // queries that see no key
+            if (kPaged && !kAlt && ng == 0 && w.dst >= 0) {  // ... in this part of the keys
                 if (row_tok < count) {
+                    const int prow = (g * p.tok + row_tok) * p.G + row_head;
+                    float4* dst = reinterpret_cast<float4*>(p.part_o) +
+                                  size_t(w.dst) * (D / 4) * p.part_rows + prow;
+#pragma unroll 1
+                    for (int i = 0; i < D / 4; ++i)
+                        dst[size_t(i) * p.part_rows] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    p.part_lse[size_t(w.dst) * p.part_rows + prow] = -INFINITY;
+                }
+                done_with_item();
+                continue;
+            }
+            if (!kTree && (kAlt ? w.n : ng) == 0) {  // queries that see no key
+                if (row_tok < count && (!kAlt || g == 0)) {
                     const size_t orow = (size_t(w.q_row) + tok0 + row_tok) * p.H_q +
                                         w.kvh * p.G + row_head;
                     uint4* dst = reinterpret_cast<uint4*>(p.o + orow * D);
@@ -1170,7 +1464,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             // Keys of tile i that this row sees, for the tiles from `plain` on:
             // c < last - 128 i. The drafted tokens' tile goes by the bits.
-            const int plain = uniform(plain_tiles<kMode>(p, w, kTree ? 0 : g));
+            const int plain = uniform(plain_tiles<kMode>(p, w, kTree || kAlt ? 0 : g));
             const int last = (kTree ? w.ctx : token_limit(p, w, tok0 + row_tok)) - w.j0 * BN;
             const int own_tile = kTree ? uniform(w.c_t - w.j0) : 0;
             uint32_t bits[4] = {0, 0, 0, 0};  // drafted tokens this row sees
@@ -1274,9 +1568,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             // (what does not need O comes before the wait for it)
             const int t = (kAlt ? e.tok0 : e.tok0 + g * p.tok) + row_tok;
             const bool valid = row_tok < p.tok && t < e.T;
-            const bool own = e.j0 + e.n > e.c_t;  // the item has the row's own tokens
+            const bool own = kPaged || e.j0 + e.n > e.c_t;  // the item has the row's own tokens
             const size_t orow = (size_t(e.q_row) + t) * p.H_q + e.kvh * p.G + row_head;
-            const bool direct = !kTree || uniform(e.dst) < 0;
+            const bool direct = (!kTree && !kPaged) || uniform(e.dst) < 0;
             // row of the item's token block
             const int prow = (t - e.tok0) * p.G + row_head;
             const RowPtrs rows(
@@ -1322,16 +1616,30 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (odd && valid) {
                         // values that are not finite among the keys that not every
                         // row sees: those that this row sees are added here
-                        const int k_end = kTree ? e.n_own : token_limit(p, e, t);
+                        int k_end = kTree ? e.n_own : token_limit(p, e, t);
+                        int k = kTree ? 0 : group_first<kMode>(p, e, 0);
+                        if (kPaged) {  // of this item's tiles
+                            k = max(k, e.j0 * BN);
+                            k_end = min(k_end, (e.j0 + e.n) * BN);
+                        }
 #pragma unroll 1
-                        for (int k = kTree ? 0 : group_first<kMode>(p, e, 0); k < k_end; ++k) {
+                        for (; k < k_end; ++k) {
                             if (kTree) {
                                 const uint32_t word = k < 32 ? bits[0] : k < 64 ? bits[1]
                                                     : k < 96 ? bits[2] : bits[3];
                                 if (!((word >> (k & 31)) & 1)) continue;
                             }
-                            const uint16_t* vr = p.v + (int64_t(e.k_row) + k) * p.v_st +
-                                                 e.kvh * p.v_sh + c * 32;
+                            const uint16_t* vr;
+                            if constexpr (kPaged) {
+                                const int page =
+                                    p.table[size_t(e.b) * p.table_width + k / p.page_size];
+                                if (page < 0 || page >= p.num_pages) continue;
+                                vr = p.v_pages + page * p.v_page +
+                                     (size_t(e.kvh) * p.page_size + k % p.page_size) * D + c * 32;
+                            } else {
+                                vr = p.v + (int64_t(e.k_row) + k) * p.v_st + e.kvh * p.v_sh +
+                                     c * 32;
+                            }
 #pragma unroll
                             for (int i = 0; i < 32; ++i) {
                                 const uint32_t bf = vr[i];
@@ -1643,6 +1951,10 @@ struct AppendParams {
     unsigned* status;
     int64_t k_st, k_sh, v_st, v_sh;
     int B, H_kv, d, S_max, total, total_new;
+    // paged_append: the rows' pages; elements from one page to the next
+    const int32_t* table;
+    int table_width, page_size, num_pages;
+    int64_t k_page, v_page;
 };
 
 // One warp per entry: K and V of one token, every head, four 16-byte pieces of
@@ -1651,7 +1963,7 @@ struct AppendParams {
 // for a few tokens, by the chain launch, prefix sums, start, copy (2.7 us in a graph).
 constexpr int kAppendWarps = 8;
 
-template <int D>
+template <int D, bool kPaged>
 __global__ void __launch_bounds__(kAppendWarps * 32) append_kernel(const AppendParams p) {
     grid_launch_dependents();
     grid_wait_primary();
@@ -1694,14 +2006,23 @@ __global__ void __launch_bounds__(kAppendWarps * 32) append_kernel(const AppendP
     if (mine) {
         const int64_t slot = int64_t(p.starts[b]) + i;
         const int src = p.index ? p.index[e] : e;
-        if (slot < 0 || slot >= p.S_max || src < 0 || src >= p.total_new) {
+        bool fits = slot >= 0 && slot < p.S_max && src >= 0 && src < p.total_new;
+        int page = 0;
+        if (kPaged && fits) {
+            page = p.table[size_t(b) * p.table_width + slot / p.page_size];
+            fits = page >= 0 && page < p.num_pages;
+        }
+        if (!fits) {
             bad = true;
         } else {
             constexpr int kPieces = D / 8, kBatch = 4;
             const uint16_t* k_src = p.k + src * p.k_st;
             const uint16_t* v_src = p.v + src * p.v_st;
-            const size_t base = (size_t(b) * p.H_kv * p.S_max + slot) * D;
-            const size_t head = size_t(p.S_max) * D;
+            const size_t base = kPaged ? size_t(slot % p.page_size) * D
+                                       : (size_t(b) * p.H_kv * p.S_max + slot) * D;
+            const size_t head = size_t(kPaged ? p.page_size : p.S_max) * D;
+            uint16_t* const kc = p.kc + (kPaged ? page * p.k_page : 0);
+            uint16_t* const vc = p.vc + (kPaged ? page * p.v_page : 0);
             const int n = p.H_kv * kPieces;
 #pragma unroll 1
             for (int v0 = lane; v0 < n; v0 += 32 * kBatch) {
@@ -1719,8 +2040,8 @@ __global__ void __launch_bounds__(kAppendWarps * 32) append_kernel(const AppendP
                     const int v = v0 + 32 * u;
                     if (v >= n) break;
                     const size_t dst = base + v / kPieces * head + v % kPieces * 8;
-                    *reinterpret_cast<uint4*>(p.kc + dst) = kx[u];
-                    *reinterpret_cast<uint4*>(p.vc + dst) = vx[u];
+                    *reinterpret_cast<uint4*>(kc + dst) = kx[u];
+                    *reinterpret_cast<uint4*>(vc + dst) = vx[u];
                 }
             }
         }
@@ -1904,8 +2225,172 @@ extern "C" int gqa_attn_cache_append(uint16_t* k_cache, uint16_t* v_cache, const
     if (!status) return GQA_ERR_CUDA;
     const AppendParams p{k_cache, v_cache, k_new, v_new, cu_seqlens, starts, index, status,
                          k_stride_t, k_stride_h, v_stride_t, v_stride_h, B, H_kv, d, S_max,
-                         total, total_new};
-    return launch(d == 128 ? append_kernel<128> : append_kernel<64>,
+                         total, total_new, nullptr, 0, 0, 0, 0, 0};
+    return launch(d == 128 ? append_kernel<128, false> : append_kernel<64, false>,
+                  unsigned((total + kAppendWarps - 1) / kAppendWarps), kAppendWarps * 32, 0,
+                  stream, p) == cudaSuccess
+               ? GQA_OK
+               : GQA_ERR_CUDA;
+}
+
+namespace gqa {
+namespace ragged {
+namespace {
+
+// Pages hold 16, 32, 64 or a multiple of 128 keys: a tile of 128 keys is then whole
+// pages or lies in one. Page strides as TMA wants them.
+int check_pages(const void* k_pages, const void* v_pages, const void* table, int B, int H_kv, int d,
+                int num_pages, int page_size, int table_width, int64_t k_page_stride,
+                int64_t v_page_stride) {
+    if (num_pages < 0 || page_size < 1 || table_width < 0) return GQA_ERR_INVALID_ARG;
+    if (page_size % 128 != 0 && page_size != 16 && page_size != 32 && page_size != 64)
+        return GQA_ERR_UNSUPPORTED;
+    if (int64_t(table_width) * page_size >= (int64_t(1) << 31) ||
+        int64_t(H_kv) * page_size >= (int64_t(1) << 31))
+        return GQA_ERR_UNSUPPORTED;
+    const int64_t page = int64_t(H_kv) * page_size * d, lim = int64_t(1) << 39;
+    if (num_pages > 1 && (k_page_stride < page || v_page_stride < page || k_page_stride >= lim ||
+                          v_page_stride >= lim))
+        return GQA_ERR_INVALID_ARG;
+    if ((num_pages > 1 && ((k_page_stride | v_page_stride) & 7)) || !aligned16(k_pages) ||
+        !aligned16(v_pages) || (reinterpret_cast<uintptr_t>(table) & 3u))
+        return GQA_ERR_MISALIGNED;
+    return GQA_OK;
+}
+
+}  // namespace
+}  // namespace ragged
+}  // namespace gqa
+
+extern "C" size_t gqa_attn_paged_attention_workspace_size(int H_q, int H_kv, int d,
+                                                          int max_tokens) {
+    if (H_q <= 0 || H_kv <= 0 || H_q % H_kv || (d != 64 && d != 128) || max_tokens < 1 ||
+        H_q / H_kv > 128)
+        return 0;
+    const ragged::TreePlan t = ragged::tree_plan(H_q / H_kv, max_tokens);
+    return size_t(ragged::kTreeCtas) * (16 + size_t(2) * t.part_rows * (d + 1) * 4);
+}
+
+extern "C" int gqa_attn_paged_attention(
+    const uint16_t* q, const uint16_t* k_pages, const uint16_t* v_pages, uint16_t* o, float* lse,
+    const int32_t* cu_seqlens, const int32_t* kv_lens, const int32_t* block_table, int B, int H_q,
+    int H_kv, int d, int total, int max_tokens, int max_keys, int num_pages, int page_size,
+    int table_width, int64_t q_stride_t, int64_t q_stride_h, int64_t k_page_stride,
+    int64_t v_page_stride, int causal, float scale, void* workspace, size_t workspace_bytes,
+    cudaStream_t stream) {
+    using namespace ragged;
+    int rc = check_common(q, k_pages, v_pages, o, lse, B, H_q, H_kv, d, scale);
+    if (rc != GQA_OK) return rc;
+    const bool empty = B == 0 || total == 0;  // nothing to do: the tensors may be null
+    if (total < 0 || max_tokens < 1 || max_keys < 0 || (!empty && (!q || !o || !kv_lens)) ||
+        (!empty && num_pages > 0 && (!k_pages || !v_pages)) ||
+        (!empty && table_width > 0 && !block_table) ||
+        (B > 0 && !cu_seqlens && (total % B != 0 || total / B > max_tokens)))
+        return GQA_ERR_INVALID_ARG;
+    if (H_q / H_kv > 128) return GQA_ERR_UNSUPPORTED;
+    rc = check_pages(k_pages, v_pages, block_table, B, H_kv, d, num_pages, page_size, table_width,
+                     k_page_stride, v_page_stride);
+    if (rc != GQA_OK) return rc;
+    if (bad_strides(q_stride_t, q_stride_h, total, H_q)) return GQA_ERR_INVALID_ARG;
+    if (odd_strides(q_stride_t, q_stride_h, total, H_q) ||
+        ((reinterpret_cast<uintptr_t>(cu_seqlens) | reinterpret_cast<uintptr_t>(kv_lens)) & 3u))
+        return GQA_ERR_MISALIGNED;
+    if (!empty && (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) ||
+                   workspace_bytes <
+                       gqa_attn_paged_attention_workspace_size(H_q, H_kv, d, max_tokens)))
+        return GQA_ERR_WORKSPACE;
+    if (empty) return GQA_OK;
+    const int sms = num_sms();
+    const TreePlan plan = tree_plan(H_q / H_kv, max_tokens);
+    Params p{};
+    p.o = o; p.lse = lse;
+    p.cu_q = cu_seqlens; p.ctx = kv_lens;
+    p.status = status_word();
+    if (!p.status || sms <= 0) return GQA_ERR_CUDA;
+    p.B = B; p.H_q = H_q; p.H_kv = H_kv; p.G = H_q / H_kv; p.total_q = total;
+    p.table = block_table; p.table_width = table_width; p.page_size = page_size;
+    p.num_pages = num_pages; p.v_pages = v_pages; p.v_page = num_pages > 1 ? v_page_stride : 0;
+    const int slots = num_pages > 0 ? table_width * page_size : 0;
+    p.S_max = max_keys > 0 && max_keys < slots ? max_keys : slots;
+    p.max_tokens = max_tokens;
+    p.causal = causal != 0;
+    p.tok = plan.tok; p.team = 1; p.part_rows = plan.part_rows;
+    p.single = max_tokens <= 2 * plan.tok;
+    p.scale_log2 = scale * kLog2e;
+    p.inject_timeout = take_injected_timeout() ? 1 : 0;
+    // no more CTAs than there can be tiles, or units that are not cut
+    const int64_t row_tiles = (int64_t(p.S_max) + BN - 1) / BN + 1;
+    p.whole = row_tiles <= kWholeTiles;
+    const int64_t blocks = int64_t(total) / (2 * plan.tok) + (B < total ? B : total);
+    const int64_t shares = blocks * H_kv * (p.whole ? 1 : row_tiles);
+    const int most = sms < kTreeCtas ? sms : kTreeCtas;
+    const int ctas = int(shares < most ? shares : most);
+    p.n_teams = ctas;
+    p.part_info = static_cast<int4*>(workspace);
+    p.part_o = reinterpret_cast<float*>(p.part_info + kTreeCtas);
+    p.part_lse = p.part_o + size_t(2) * ctas * p.part_rows * d;
+    Maps m;
+    if (!packed_maps(m, p, q, nullptr, nullptr, d, q_stride_t, q_stride_h, 0, 0, 0, 0))
+        return GQA_ERR_CUDA;
+    if (num_pages > 0) {
+        const uint32_t rows = page_size < BN ? page_size : BN;
+        const int64_t page = int64_t(H_kv) * page_size * d;
+        if (encode_tmap_pages_bf16(&m.kc, k_pages, d, page_size, H_kv, num_pages,
+                                   num_pages > 1 ? k_page_stride : page, rows) != cudaSuccess ||
+            encode_tmap_pages_bf16(&m.vc, v_pages, d, page_size, H_kv, num_pages,
+                                   num_pages > 1 ? v_page_stride : page, rows) != cudaSuccess)
+            return GQA_ERR_CUDA;
+    }
+    int rl;
+    if (d == 128)
+        rl = plan.alt ? launch_ragged<128, kPagedAlt>(m, p, ctas, stream)
+                      : launch_ragged<128, kPagedPair>(m, p, ctas, stream);
+    else
+        rl = plan.alt ? launch_ragged<64, kPagedAlt>(m, p, ctas, stream)
+                      : launch_ragged<64, kPagedPair>(m, p, ctas, stream);
+    if (rl != GQA_OK || p.whole || ctas == 1) return rl;
+    const int64_t tasks = int64_t(ctas) * ((p.part_rows + 31) / 32) * (d / 32);
+    const unsigned grid = unsigned(tasks < 2 * kTreeCtas ? tasks : 2 * kTreeCtas);
+    return launch(d == 128 ? merge_kernel<128> : merge_kernel<64>, grid, kMergeThreads, 0, stream,
+                  p) == cudaSuccess
+               ? GQA_OK
+               : GQA_ERR_CUDA;
+}
+
+extern "C" int gqa_attn_paged_append(
+    uint16_t* k_pages, uint16_t* v_pages, const uint16_t* k_new, const uint16_t* v_new,
+    const int32_t* cu_seqlens, const int32_t* starts, const int32_t* index,
+    const int32_t* block_table, int B, int H_kv, int d, int total, int total_new, int num_pages,
+    int page_size, int table_width, int64_t k_stride_t, int64_t k_stride_h, int64_t v_stride_t,
+    int64_t v_stride_h, int64_t k_page_stride, int64_t v_page_stride, cudaStream_t stream) {
+    using namespace ragged;
+    const bool empty = B == 0 || total == 0;
+    if ((!empty && (!k_pages || !v_pages || !starts || !block_table)) || B < 0 || B > 65535 ||
+        H_kv <= 0 || total < 0 || total_new < 0 || (total_new > 0 && (!k_new || !v_new)) ||
+        (!index && total > total_new) || (B > 0 && !cu_seqlens && total % B != 0))
+        return GQA_ERR_INVALID_ARG;
+    if (d != 64 && d != 128) return GQA_ERR_UNSUPPORTED;
+    const int rc = check_pages(k_pages, v_pages, block_table, B, H_kv, d, num_pages, page_size,
+                               table_width, k_page_stride, v_page_stride);
+    if (rc != GQA_OK) return rc;
+    if (bad_strides(k_stride_t, k_stride_h, total_new, H_kv) ||
+        bad_strides(v_stride_t, v_stride_h, total_new, H_kv))
+        return GQA_ERR_INVALID_ARG;
+    if (!aligned16(k_new) || !aligned16(v_new) ||
+        odd_strides(k_stride_t, k_stride_h, total_new, H_kv) ||
+        odd_strides(v_stride_t, v_stride_h, total_new, H_kv) ||
+        ((reinterpret_cast<uintptr_t>(cu_seqlens) | reinterpret_cast<uintptr_t>(starts) |
+          reinterpret_cast<uintptr_t>(index)) & 3u))
+        return GQA_ERR_MISALIGNED;
+    if (empty) return GQA_OK;
+    unsigned* status = status_word();
+    if (!status) return GQA_ERR_CUDA;
+    const AppendParams p{k_pages, v_pages, k_new, v_new, cu_seqlens, starts, index, status,
+                         k_stride_t, k_stride_h, v_stride_t, v_stride_h, B, H_kv, d,
+                         table_width * page_size, total, total_new, block_table, table_width,
+                         page_size, num_pages, num_pages > 1 ? k_page_stride : 0,
+                         num_pages > 1 ? v_page_stride : 0};
+    return launch(d == 128 ? append_kernel<128, true> : append_kernel<64, true>,
                   unsigned((total + kAppendWarps - 1) / kAppendWarps), kAppendWarps * 32, 0,
                   stream, p) == cudaSuccess
                ? GQA_OK

@@ -168,6 +168,22 @@ cudaError_t encode_tmap_3d_bf16_strided(CUtensorMap* map, const void* base, uint
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
+cudaError_t encode_tmap_pages_bf16(CUtensorMap* map, const void* base, uint64_t d,
+                                   uint64_t page_size, uint64_t heads, uint64_t pages,
+                                   uint64_t page_stride, uint32_t box_rows) {
+    PFN_cuTensorMapEncodeTiled_v12000 enc = encoder();
+    if (!enc) return cudaErrorSymbolNotFound;
+    cuuint64_t dims[4] = {d, page_size, heads, pages};
+    cuuint64_t strides[3] = {d * 2, page_size * d * 2, page_stride * 2};  // bytes
+    cuuint32_t box[4] = {64, box_rows, 1, 1};
+    cuuint32_t estr[4] = {1, 1, 1, 1};
+    CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims,
+                     strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                     CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
 // Test hook (gqa_attn_debug_inject_timeout): launches left to inject.
 static std::atomic<int> g_inject_timeout{0};
 

@@ -60,6 +60,13 @@ cudaError_t encode_tmap_3d_bf16_strided(CUtensorMap* map, const void* base, uint
                                         uint64_t outer_stride, uint32_t box_mid,
                                         uint32_t box_outer);
 
+// 4-D bf16 tensor map over KV pages [pages, heads, page_size, d], pages page_stride
+// elements (a multiple of 8) apart and contiguous within; 128-byte swizzle, box of 64
+// columns of box_rows keys of one head of one page.
+cudaError_t encode_tmap_pages_bf16(CUtensorMap* map, const void* base, uint64_t d,
+                                   uint64_t page_size, uint64_t heads, uint64_t pages,
+                                   uint64_t page_stride, uint32_t box_rows);
+
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 }  // namespace gqa

@@ -429,6 +429,122 @@ GQA_API int gqa_attn_cache_append(uint16_t* k_cache, uint16_t* v_cache, const ui
                                   int64_t k_stride_h, int64_t v_stride_t, int64_t v_stride_h,
                                   cudaStream_t stream);
 
+/* ---------------------------------------------------------- paged caches --
+ * A serving step over a cache whose tokens lie in pages: the norm and rotation
+ * of the step's queries and keys, appending them to the pages, attention over
+ * the pages, and the verification of drafted tokens. No page has a
+ * counterpart. Packed tensors, prefix sums, error reports and graphs as in the
+ * ragged calls above; what is written does not overlap what is read, except
+ * where said. */
+
+/* Every head of q [tokens, H_q, d] and k [tokens, H_kv, d] is divided by its
+ * root mean square (norm != 0), multiplied by a weight and rotated by its
+ * token's position:
+ *   z_c = x_c / sqrt(mean_c x_c^2 + eps) * w_c       (norm == 0: z = x)
+ *   y_1 = z_1 cos a - z_2 sin a,  y_2 = z_2 cos a + z_1 sin a
+ * for each of `pairs` pairs of channels with a = position * inv_freq[pair]:
+ * channels (i, i + pairs), or (2i, 2i + 1) with interleaved != 0. Channels from
+ * 2 * pairs on are not rotated. Rounded to bf16 once, at the end.
+ *   positions : device int32 [axes, tokens], any values; the angle is exact to
+ *               about 2^-22 turns over their whole range.
+ *   inv_freq  : device fp32 [pairs], finite.
+ *   axes      : 1, or up to 4 (time, height, width of images and video), where
+ *               axis a turns the next sections[a] pairs (host int32 [axes],
+ *               summing to pairs; read during the call).
+ *   weights   : device [d], bf16 or (weights_fp32 != 0) fp32; NULL: 1. Not
+ *               read when norm == 0.
+ *   strides   : of q, k (in) and q_out, k_out: positive multiples of 8; an
+ *               output's rows do not overlap. q_out == q and k_out == k with
+ *               the same strides work in place.
+ *   H_kv      : 0 for queries alone (k, k_out are then not used).
+ * pairs is a multiple of 8 up to d / 2; d in {64, 128}; eps >= 0. */
+GQA_API int gqa_attn_qk_norm_rope(
+    const uint16_t* q, const uint16_t* k, uint16_t* q_out, uint16_t* k_out, const void* q_weight,
+    const void* k_weight, int weights_fp32, const int32_t* positions, const float* inv_freq,
+    const int32_t* sections, int axes, int tokens, int H_q, int H_kv, int d, int pairs,
+    int interleaved, int norm, float eps, int64_t q_stride_t, int64_t q_stride_h,
+    int64_t k_stride_t, int64_t k_stride_h, int64_t qo_stride_t, int64_t qo_stride_h,
+    int64_t ko_stride_t, int64_t ko_stride_h, cudaStream_t stream);
+
+/* Pages: k_pages, v_pages [num_pages, H_kv, page_size, d] bf16, each page
+ * contiguous, k_page_stride and v_page_stride elements from one to the next
+ * (multiples of 8, at least a page). page_size is 16, 32, 64 or a multiple of
+ * 128. Slot s of row b lies in page block_table[b * table_width + s / page_size],
+ * at s % page_size; entries that no slot in use needs are not read. A page may
+ * stand in several rows (a shared prefix). table_width * page_size < 2^31.
+ *
+ * gqa_attn_paged_append is gqa_attn_cache_append over pages: entry i of row b
+ * (token e = cu_seqlens[b] + i of k_new, v_new, or token index[e]) goes to slot
+ * starts[b] + i. An entry whose slot lies outside [0, table_width * page_size),
+ * whose page lies outside [0, num_pages) or whose index lies outside
+ * [0, total_new) is not written and reported as GQA_ERR_DEVICE_BAD_INPUT by
+ * gqa_attn_check(). No two entries of a call go to one slot of a page. */
+GQA_API int gqa_attn_paged_append(
+    uint16_t* k_pages, uint16_t* v_pages, const uint16_t* k_new, const uint16_t* v_new,
+    const int32_t* cu_seqlens, const int32_t* starts, const int32_t* index,
+    const int32_t* block_table, int B, int H_kv, int d, int total, int total_new, int num_pages,
+    int page_size, int table_width, int64_t k_stride_t, int64_t k_stride_h, int64_t v_stride_t,
+    int64_t v_stride_h, int64_t k_page_stride, int64_t v_page_stride, cudaStream_t stream);
+
+/* Attention of new tokens over the pages, which hold them already: row b has
+ * kv_lens[b] keys (device int32 [B]) in its pages, the last of which are those
+ * of its T tokens in q. Token t sees the keys j <= kv_lens[b] - T + t (causal
+ * != 0) or all kv_lens[b] of them. T is 1 for ordinary decoding, a few for a
+ * line of drafted tokens, thousands for a chunk of a prompt; a call may mix
+ * them. The keys of long rows are cut over the CTAs and merged.
+ *   cu_seqlens : prefix sums of the tokens, or NULL: total / B per row.
+ *   max_tokens : no row has more tokens; a longer one is cut there and reported
+ *                as GQA_ERR_DEVICE_BAD_INPUT. It chooses the kernel: one token
+ *                per row with max_tokens = 1 runs fastest.
+ *   max_keys   : no row has more keys, or 0: table_width * page_size. A length
+ *                outside [0, max_keys] is clamped and reported. Small values
+ *                (512 and fewer) save the merge.
+ *   workspace  : 256-byte aligned device memory of at least
+ *                gqa_attn_paged_attention_workspace_size() bytes, as for
+ *                gqa_attn_decode_tree.
+ * A page id in use outside [0, num_pages) is reported the same way, and what
+ * the row's output holds is then not defined. H_q / H_kv <= 128. The same
+ * inputs give the same bits; where a row is cut, and so its last bits, depends
+ * on the other rows' lengths. */
+GQA_API int gqa_attn_paged_attention(
+    const uint16_t* q, const uint16_t* k_pages, const uint16_t* v_pages, uint16_t* o, float* lse,
+    const int32_t* cu_seqlens, const int32_t* kv_lens, const int32_t* block_table, int B, int H_q,
+    int H_kv, int d, int total, int max_tokens, int max_keys, int num_pages, int page_size,
+    int table_width, int64_t q_stride_t, int64_t q_stride_h, int64_t k_page_stride,
+    int64_t v_page_stride, int causal, float scale, void* workspace, size_t workspace_bytes,
+    cudaStream_t stream);
+
+/* Bytes of workspace for gqa_attn_paged_attention (0 on invalid sizes). */
+GQA_API size_t gqa_attn_paged_attention_workspace_size(int H_q, int H_kv, int d, int max_tokens);
+
+/* Verification of drafted tokens (speculative sampling) from given random
+ * numbers. Row b has n drafted tokens x_i = draft_tokens[cu[b] + i] with draft
+ * probabilities q_i (row cu[b] + i of draft_probs) and n + 1 target
+ * distributions p_i (row cu[b] + b + i of target_probs), both fp32 of V values.
+ * x_i stands if u_accept * q_i(x_i) < p_i(x_i) and every one before it stands;
+ * accepted[b] is the number that stand, k. next_tokens[b] is drawn from
+ *   w = max(p_k - q_k, 0) (k < n), or p_n (k == n):
+ * the lowest v with w_0 + .. + w_v > u_sample[b] * (w_0 + .. + w_(V-1)), the
+ * last v with w_v > 0 where there is none. The products, differences and sums
+ * are those of 64-bit arithmetic (to about 2^-44 of a row's sum).
+ *   draft_probs : NULL: each drafted token was certain (q = 1 there, 0
+ *                 elsewhere), as from a greedy draft or a look-up.
+ *   u_accept [total], u_sample [B] : fp32, from [0, 1).
+ *   cu_seqlens  : prefix sums of the drafted tokens, or NULL: total / B each.
+ *   strides     : elements from one distribution to the next, at least V
+ *                 (multiples of 4 with 16-byte aligned tables are read faster).
+ *   accepted, next_tokens : int32 [B].
+ * Values that are not above 0 (NaN included) count as 0. Where max(p - q, 0) is
+ * 0 throughout, w = p. Where w has no value above 0 or an infinite sum, next_tokens is -1, and
+ * that is reported as GQA_ERR_DEVICE_BAD_INPUT, as is a token outside [0, V),
+ * which does not stand. */
+GQA_API int gqa_attn_verify_drafts(const float* target_probs, const float* draft_probs,
+                                   const int32_t* draft_tokens, const float* u_accept,
+                                   const float* u_sample, const int32_t* cu_seqlens,
+                                   int32_t* accepted, int32_t* next_tokens, int B, int total,
+                                   int V, int64_t target_stride, int64_t draft_stride,
+                                   cudaStream_t stream);
+
 /* ------------------------------------------------------ plan / scheduler --
  * Integer helpers the kernels use, exported so tests can compare them with
  * independent derivations bit for bit. Host-only; no GPU needed.
