@@ -36,14 +36,23 @@ cudaError_t launch(void (*kern)(A...), dim3 grid, int threads, int cluster, cuda
 //   z_c = x_c / sqrt(mean_c x_c^2 + eps) * w_c                  (each head of q and k)
 //   y_1 = z_1 cos a - z_2 sin a,  y_2 = z_2 cos a + z_1 sin a   (each pair of channels)
 //
-// with a = position * inv_freq. Rounded to bf16 once, at the end. A head is 8 channels
-// a lane, so a warp takes 2 heads (d = 128) or 4 (d = 64) at a time. cos and sin of the
-// block's tokens are computed once, into shared memory; a lane multiplies those of its
-// channels with its weights once per token, and then needs two products for a channel.
-constexpr int kNormThreads = 256;
+// with a = position * inv_freq. Rounded to bf16 once, at the end. A lane holds two chunks
+// of 8 channels of a head, chosen so that they are the two sides of 8 pairs: nothing but
+// the sum of squares goes between lanes, and a warp takes 4 heads (d = 128) or 8 (d = 64)
+// at a time. cos and sin of the block's tokens are computed once, into shared memory; a
+// lane multiplies them with its weights once per token, and then needs two products for
+// a channel.
+//
+// Bound by HBM for many tokens (8203 tokens of 64/8 heads, d = 128, 302 MB: 52.6 us, 5.75
+// TB/s, 0.86 of the measured copy rate), by the chain launch, angles, heads for few (8 tokens
+// 2.8 us in a graph). Measured for the many / for 5000 tokens of 28/4 heads (19.4): one
+// chunk a lane, partners by shuffle, 69 / 28 (180 instructions a warp for two heads); blocks
+// of 256 threads 56 / 22; registers capped at 80 to fit a sixth block, with spills, 57 / 20;
+// one head's loads in flight 61 / 22; two tokens to a block of four warps 55 / 21.
+constexpr int kNormThreads = 128;
 constexpr int kNormWarps = kNormThreads / 32;
 constexpr int kMaxAxes = 4;
-constexpr int kNormBatch = 4;  // heads' loads in flight a lane
+constexpr int kNormBatch = 2;  // heads of a lane whose loads are in flight
 
 struct NormParams {
     const uint16_t *q, *k;
@@ -54,145 +63,219 @@ struct NormParams {
     int64_t q_st, q_sh, k_st, k_sh, qo_st, qo_sh, ko_st, ko_sh;
     int tokens, H_q, H_kv, pairs, wide_weights;
     int section_end[kMaxAxes];   // first pair behind each axis' section
-    int block_tokens;            // 1, 2, 4 or 8 tokens of a block
+    int block_tokens;            // 1, 2 or 4 tokens of a block
     float eps;
 };
 
-// cos and sin of position * frequency. The angle has up to 55 bits: it is taken in
-// turns, in 64 bits, and only what is left of the last whole turn is rounded to 32
-// (a far position's angle rounded to 32 bits first would be off by 2^-24 of itself).
+// cos and sin of position * frequency, with the angle in turns as a 64-bit fixed-point
+// fraction: whole turns fall out of the product as its overflow, so far positions lose
+// nothing (an angle of 10^6 radians rounded to 32 bits would be off by 0.03). The
+// fraction of one position's angle is m 2^e / (2 pi) with m, e of the 32-bit frequency,
+// from the first 64 bits of 1 / (2 pi): off by 2^-65 for frequencies up to 1, so by
+// 2^-34 turns at 2^31 positions. (64-bit floating point has a sixty-fourth of the
+// 32-bit rate here.) Frequencies below 2^24.
 __device__ __forceinline__ float2 rotation(int position, float freq) {
-    const double turns = double(position) * double(freq) * 0.15915494309189535;  // 1 / (2 pi)
-    const float part = float(turns - rint(turns));  // -0.5 .. 0.5
-    float2 r;
-    sincospif(2.f * part, &r.y, &r.x);
+    constexpr unsigned long long kInv2Pi = 0xa2f9836e4e441529ull;  // 2^66 / (2 pi)
+    const unsigned bits = __float_as_uint(freq), exp = (bits >> 23) & 0xffu;
+    const unsigned long long m = (bits & 0x7fffffu) | (exp ? 0x800000u : 0u);
+    const int shift = 152 - int(exp ? exp : 1u);  // 2 - e
+    const unsigned long long hi = __umul64hi(m, kInv2Pi), lo = m * kInv2Pi;
+    unsigned long long per = 0;  // turns of one position, 2^64 to a turn
+    if (shift >= 64) per = shift < 128 ? hi >> (shift - 64) : 0;
+    else if (shift > 0) per = (hi << (64 - shift)) | (lo >> shift);
+    if (bits >> 31) per = 0ull - per;
+    const unsigned long long turns = per * static_cast<unsigned long long>(int64_t(position));
+    float2 r;  // the nearest whole turn taken off: [-1/2, 1/2) turns, in halves
+    sincospif(float(int(turns >> 32)) * 0x1p-31f, &r.y, &r.x);
     return r;
 }
 
 template <int D, bool kNorm, bool kInterleaved>
-__global__ void __launch_bounds__(kNormThreads) norm_rope_kernel(const NormParams p) {
-    constexpr int kHeadLanes = D / 8, kHeads = 32 / kHeadLanes;  // of a warp
-    __shared__ float2 turn[kNormWarps][D / 2];
+__global__ void __launch_bounds__(kNormThreads, 5) norm_rope_kernel(const NormParams p) {
+    constexpr int kHeadLanes = D / 16, kHeads = 32 / kHeadLanes;  // of a warp
+    __shared__ __align__(16) float cos_s[kNormWarps][D / 2], sin_s[kNormWarps][D / 2];
+    __shared__ __align__(16) float weights[2][D];
     grid_launch_dependents();
     grid_wait_primary();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int t0 = blockIdx.x * p.block_tokens;
+    // the block's warps share its tokens; blockIdx.y shares a token's heads further
+    const int per_token = kNormWarps / p.block_tokens;
+    const int mine = warp / per_token;  // which of the block's tokens
+    const int t = t0 + mine;
+    const bool live = t < p.tokens;
+    const int worker = blockIdx.y * per_token + warp % per_token;
+    const int workers = per_token * gridDim.y;
+    const int l = lane % kHeadLanes, sub = lane / kHeadLanes;
+    // This lane's chunks of 8 channels. With S = pairs / 8 the chunks 0 .. S - 1 and S ..
+    // 2 S - 1 are the two sides of the pairs (not interleaved); those behind are not turned.
+    const int S = p.pairs / 8;
+    const bool turned = l < S;
+    const int chunk_a = turned ? l : S + l;
+    const int chunk_b = turned ? l + S : l + kHeadLanes;
+
+    struct Rows {
+        const uint16_t* x;
+        int64_t step;
+        int h;
+    };
+    auto load = [&](const Rows& r, int heads, uint4& a, uint4& b) {
+        if (r.h < heads) {
+            a = *reinterpret_cast<const uint4*>(r.x + chunk_a * 8);
+            b = *reinterpret_cast<const uint4*>(r.x + chunk_b * 8);
+        } else {
+            a = b = make_uint4(0, 0, 0, 0);
+        }
+    };
+    auto rows_of = [&](const uint16_t* x, int64_t st, int64_t sh) {
+        const int h = worker * kHeads + sub;
+        return Rows{x + t * st + h * sh, workers * kHeads * sh, h};
+    };
+    uint4 va[kNormBatch], vb[kNormBatch];
+    auto load_batch = [&](Rows& r, int heads) {
+#pragma unroll
+        for (int u = 0; u < kNormBatch; ++u) {
+            load(r, heads, va[u], vb[u]);
+            r.x += r.step;
+            r.h += workers * kHeads;
+        }
+    };
+    // the first heads are on their way while the angles are computed
+    Rows rq = rows_of(p.q, p.q_st, p.q_sh);
+    load_batch(rq, live ? p.H_q : 0);
+
     for (int i = threadIdx.x; i < p.block_tokens * (D / 2); i += kNormThreads) {
-        const int pair = i % (D / 2), t = t0 + i / (D / 2);
-        if (pair >= p.pairs || t >= p.tokens) continue;
+        const int pair = i % (D / 2), tok = i / (D / 2), at = t0 + tok;
+        if (pair >= p.pairs || at >= p.tokens) continue;
         int axis = 0;
 #pragma unroll
         for (int a = 0; a < kMaxAxes - 1; ++a) axis += pair >= p.section_end[a];
-        turn[i / (D / 2)][pair] = rotation(p.positions[int64_t(axis) * p.tokens + t],
-                                           p.inv_freq[pair]);
+        const float2 r = rotation(p.positions[int64_t(axis) * p.tokens + at], p.inv_freq[pair]);
+        cos_s[tok][pair] = r.x;
+        sin_s[tok][pair] = r.y;
+    }
+    if constexpr (kNorm) {
+        for (int i = threadIdx.x; i < 2 * D; i += kNormThreads) {
+            const void* w = i < D ? p.qw : p.kw;
+            const int ch = i % D;
+            weights[i / D][ch] =
+                !w               ? 1.f
+                : p.wide_weights ? static_cast<const float*>(w)[ch]
+                                 : __uint_as_float(
+                                       uint32_t(static_cast<const uint16_t*>(w)[ch]) << 16);
+        }
     }
     __syncthreads();
-    // the block's warps share its tokens; blockIdx.y shares a token's heads further
-    const int per_token = kNormWarps / p.block_tokens;
-    const int t = t0 + warp / per_token;
-    if (t >= p.tokens) return;
-    const int worker = blockIdx.y * per_token + warp % per_token;
-    const int workers = per_token * gridDim.y;
-    const int c = lane % kHeadLanes;  // channels 8 c .. 8 c + 7
-    // the lane that holds the partners of this lane's channels (kInterleaved: itself)
-    const int span = p.pairs / 8;
-    const bool turned = 8 * c < 2 * p.pairs, second = c >= span;
-    const int partner = kInterleaved || !turned ? lane : second ? lane - span : lane + span;
+    if (!live) return;
 
-#pragma unroll 1
-    for (int part = 0; part < 2; ++part) {
-        const uint16_t* x = (part ? p.k : p.q) + t * (part ? p.k_st : p.q_st) + c * 8;
-        uint16_t* y = (part ? p.ko : p.qo) + t * (part ? p.ko_st : p.qo_st) + c * 8;
-        const int64_t xh = part ? p.k_sh : p.q_sh, yh = part ? p.ko_sh : p.qo_sh;
-        const int heads = part ? p.H_kv : p.H_q;
-        if (worker * kHeads >= heads) continue;
-        // y = r (own x + other x_partner)
-        float own[8], other[8];
-        {
-            const void* w = part ? p.kw : p.qw;
-            auto weight = [&](int ch) {
-                return !kNorm || !w ? 1.f
-                       : p.wide_weights
-                           ? static_cast<const float*>(w)[ch]
-                           : __uint_as_float(uint32_t(static_cast<const uint16_t*>(w)[ch]) << 16);
-            };
+    auto part = [&](int which, Rows rows, int heads, uint16_t* y, int64_t y_st, int64_t y_sh) {
+        // Pairs (first, second) of this lane and what they are multiplied with:
+        //   y_first = r (fc first - ss second),  y_second = r (sc second + fs first)
+        float fc[8], ss[8], sc[8], fs[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int ch = 8 * c + i;
-                own[i] = weight(ch);
-                other[i] = 0.f;
-                if (!turned) continue;
-                const int pair = kInterleaved ? ch >> 1 : second ? ch - p.pairs : ch;
-                const bool up = kInterleaved ? i & 1 : second;
-                const int mate = kInterleaved ? ch ^ 1 : second ? pair : ch + p.pairs;
-                const float2 cs = turn[warp / per_token][pair];
-                own[i] *= cs.x;
-                other[i] = weight(mate) * (up ? cs.y : -cs.y);
-            }
+        for (int j = 0; j < 8; ++j) {
+            const int ch1 = kInterleaved ? (j < 4 ? chunk_a : chunk_b) * 8 + (j & 3) * 2
+                                         : chunk_a * 8 + j;
+            const int ch2 = kInterleaved ? ch1 + 1 : chunk_b * 8 + j;
+            const float w1 = kNorm ? weights[which][ch1] : 1.f;
+            const float w2 = kNorm ? weights[which][ch2] : 1.f;
+            const int pair = kInterleaved ? ch1 >> 1 : ch1;
+            const float c = turned ? cos_s[mine][pair] : 1.f;
+            const float s = turned ? sin_s[mine][pair] : 0.f;
+            fc[j] = w1 * c;
+            ss[j] = -w2 * s;
+            sc[j] = w2 * c;
+            fs[j] = w1 * s;
         }
-        const int sub = lane / kHeadLanes;
+        int h = worker * kHeads + sub;
+        uint16_t* out = y + t * y_st + h * y_sh;
+        const int64_t out_step = workers * kHeads * y_sh;
 #pragma unroll 1
-        for (int h0 = worker; h0 * kHeads < heads; h0 += workers * kNormBatch) {
-            uint4 v[kNormBatch];
+        for (int h0 = worker * kHeads; h0 < heads;) {
 #pragma unroll
             for (int u = 0; u < kNormBatch; ++u) {
-                const int h = (h0 + u * workers) * kHeads + sub;
-                v[u] = h < heads ? *reinterpret_cast<const uint4*>(x + h * xh)
-                                 : make_uint4(0, 0, 0, 0);
-            }
-#pragma unroll
-            for (int u = 0; u < kNormBatch; ++u) {
-                if ((h0 + u * workers) * kHeads >= heads) break;
-                const uint32_t raw[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
-                float a[8], b[8];
+                if (h0 >= heads) break;
+                const uint32_t ra[4] = {va[u].x, va[u].y, va[u].z, va[u].w};
+                const uint32_t rb[4] = {vb[u].x, vb[u].y, vb[u].z, vb[u].w};
+                load(rows, heads, va[u], vb[u]);
+                rows.x += rows.step;
+                rows.h += workers * kHeads;
+                float f[8], s[8];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    a[2 * i] = __uint_as_float(raw[i] << 16);
-                    a[2 * i + 1] = __uint_as_float(raw[i] & 0xffff0000u);
+                    const float a0 = __uint_as_float(ra[i] << 16);
+                    const float a1 = __uint_as_float(ra[i] & 0xffff0000u);
+                    const float b0 = __uint_as_float(rb[i] << 16);
+                    const float b1 = __uint_as_float(rb[i] & 0xffff0000u);
                     if constexpr (kInterleaved) {
-                        b[2 * i] = a[2 * i + 1];
-                        b[2 * i + 1] = a[2 * i];
+                        f[i] = a0; s[i] = a1; f[4 + i] = b0; s[4 + i] = b1;
                     } else {
-                        const uint32_t m = __shfl_sync(0xffffffffu, raw[i], partner);
-                        b[2 * i] = __uint_as_float(m << 16);
-                        b[2 * i + 1] = __uint_as_float(m & 0xffff0000u);
+                        f[2 * i] = a0; f[2 * i + 1] = a1; s[2 * i] = b0; s[2 * i + 1] = b1;
                     }
                 }
-                float r = 1.f;
+                uint64_t r2 = f2pack(1.f, 1.f);
                 if constexpr (kNorm) {
-                    float s0 = 0.f, s1 = 0.f;
+                    uint64_t q0 = 0ull, q1 = 0ull;
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        s0 = fmaf(a[2 * i], a[2 * i], s0);
-                        s1 = fmaf(a[2 * i + 1], a[2 * i + 1], s1);
+                        const uint64_t x = f2pack(f[2 * i], f[2 * i + 1]);
+                        const uint64_t z = f2pack(s[2 * i], s[2 * i + 1]);
+                        q0 = ffma2(x, x, q0);
+                        q1 = ffma2(z, z, q1);
                     }
-                    float s = s0 + s1;
+                    float s0, s1;
+                    f2unpack(fadd2(q0, q1), s0, s1);
+                    float sum = s0 + s1;
 #pragma unroll
                     for (int o = kHeadLanes / 2; o > 0; o >>= 1)
-                        s += __shfl_xor_sync(0xffffffffu, s, o);
-                    r = rsqrtf(s * (1.f / D) + p.eps);
+                        sum += __shfl_xor_sync(0xffffffffu, sum, o);
+                    const float r = rsqrtf(sum * (1.f / D) + p.eps);
+                    r2 = f2pack(r, r);
                 }
-                uint32_t out[4];
+                float yf[8], ys[8];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    float z[2];
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const int k = 2 * i + e;
-                        z[e] = own[k] * a[k];
-                        // (channels that are not turned take nothing of another's infinity)
-                        if (turned) z[e] = fmaf(other[k], b[k], z[e]);
-                        if constexpr (kNorm) z[e] *= r;
+                    const int j = 2 * i;
+                    const uint64_t x = f2pack(f[j], f[j + 1]), z = f2pack(s[j], s[j + 1]);
+                    uint64_t a = fmul2(f2pack(fc[j], fc[j + 1]), x);
+                    uint64_t b = fmul2(f2pack(sc[j], sc[j + 1]), z);
+                    // (channels that are not turned take nothing of another's infinity)
+                    if (turned) {
+                        a = ffma2(f2pack(ss[j], ss[j + 1]), z, a);
+                        b = ffma2(f2pack(fs[j], fs[j + 1]), x, b);
                     }
-                    out[i] = pack_bf16x2(z[0], z[1]);
+                    if constexpr (kNorm) {
+                        a = fmul2(a, r2);
+                        b = fmul2(b, r2);
+                    }
+                    f2unpack(a, yf[j], yf[j + 1]);
+                    f2unpack(b, ys[j], ys[j + 1]);
                 }
-                const int h = (h0 + u * workers) * kHeads + sub;
-                if (h < heads)
-                    *reinterpret_cast<uint4*>(y + h * yh) =
-                        make_uint4(out[0], out[1], out[2], out[3]);
+                if (h < heads) {
+                    uint32_t wa[4], wb[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        wa[i] = kInterleaved ? pack_bf16x2(yf[i], ys[i])
+                                             : pack_bf16x2(yf[2 * i], yf[2 * i + 1]);
+                        wb[i] = kInterleaved ? pack_bf16x2(yf[4 + i], ys[4 + i])
+                                             : pack_bf16x2(ys[2 * i], ys[2 * i + 1]);
+                    }
+                    *reinterpret_cast<uint4*>(out + chunk_a * 8) =
+                        make_uint4(wa[0], wa[1], wa[2], wa[3]);
+                    *reinterpret_cast<uint4*>(out + chunk_b * 8) =
+                        make_uint4(wb[0], wb[1], wb[2], wb[3]);
+                }
+                out += out_step;
+                h += workers * kHeads;
+                h0 += workers * kHeads;
             }
         }
-    }
+    };
+    part(0, rq, p.H_q, p.qo, p.qo_st, p.qo_sh);
+    if (worker * kHeads >= p.H_kv) return;
+    Rows rk = rows_of(p.k, p.k_st, p.k_sh);
+    load_batch(rk, p.H_kv);
+    part(1, rk, p.H_kv, p.ko, p.ko_st, p.ko_sh);
 }
 
 // ------------------------------------------------------------ drafted tokens
@@ -207,9 +290,10 @@ __global__ void __launch_bounds__(kNormThreads) norm_rope_kernel(const NormParam
 // memory, and the CTA in whose piece the token lies reads one warp's piece again.
 //
 // Rounding. The token has to be the one that the sum in 64 bits gives, but 64-bit
-// arithmetic is slow here (the adds of a batch of 48 rows would take about five times as long as its
-// bytes): a lane adds its terms in two 32-bit words, the difference p - q and every sum
-// with the exact error of its rounding, and only the lanes' results are added in 64 bits.
+// arithmetic runs at a sixty-fourth of the 32-bit rate: with it in every thread a row took 29 us
+// and a batch of 48 rows 58. A lane adds its terms in two 32-bit words, the difference
+// p - q and every sum with the exact error of its rounding, lanes and warps are added the
+// same way, and one warp adds the warps' and the CTAs' sums in 64 bits.
 constexpr int kVerifyThreads = 512;
 constexpr int kVerifyWarps = kVerifyThreads / 32;
 constexpr int kMaxCluster = 16;
@@ -232,6 +316,7 @@ struct Sum2 {
         lo += ((hi - (s - t)) + (x - t)) + err;
         hi = s;
     }
+    __device__ __forceinline__ double value() const { return double(hi) + double(lo); }
 };
 // The term of one element: max(p - q, 0) as a 32-bit value and the error of its rounding.
 __device__ __forceinline__ void add_difference(Sum2& s, float p, float q) {
@@ -243,15 +328,40 @@ __device__ __forceinline__ void add_plain(Sum2& s, float p) {
     if (p > 0.f) s.add(p, 0.f);
 }
 
+// Where a sum over the lanes passes a threshold: x >= 0 is a lane's part, incl its
+// inclusive prefix sum and base what comes before. The first lane whose sum is above
+// limit, or the last lane with any part (rounding kept the sum below); before: the sum
+// up to that lane. For whole warps.
+__device__ __forceinline__ int passing_lane(double x, double incl, double base, double limit,
+                                            double& before) {
+    const unsigned some = __ballot_sync(0xffffffffu, x > 0.0);
+    const unsigned above = __ballot_sync(0xffffffffu, x > 0.0 && base + incl > limit);
+    const int at = above ? __ffs(above) - 1 : 31 - __clz(some | 1u);
+    const double prev = __shfl_sync(0xffffffffu, incl, max(at - 1, 0));
+    before = at > 0 ? base + prev : base;
+    return at;
+}
+__device__ __forceinline__ double inclusive16(double x, int lane) {
+    for (int o = 1; o < 16; o <<= 1) {
+        const double y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+    }
+    return x;
+}
+
 __device__ __forceinline__ void st_dsmem_f64(uint32_t addr, double v) {
     asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(addr), "d"(v) : "memory");
 }
 
 __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyParams p) {
-    __shared__ int first_fall, found, last_some;
-    __shared__ double warp_sum[2][kVerifyWarps];
+    static_assert(kVerifyWarps == 16 && kMaxCluster == 16, "inclusive16");
+    __shared__ int first_fall;
+    __shared__ float2 warp_sum[kVerifyWarps];
     __shared__ double cta_sum[2][kMaxCluster];  // written by the cluster's CTAs
-    __shared__ double scan[kVerifyWarps];
+    // what one warp finds for all: the CTA (-1: nothing to draw from) and the warp where
+    // the sum passes the threshold, the sum before that warp
+    __shared__ int owner_cta, owner_warp;
+    __shared__ double owner_before;
     grid_launch_dependents();
     grid_wait_primary();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -270,11 +380,7 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyPara
         n = p.total / p.B;
         first = b * n;
     }
-    if (threadIdx.x == 0) {
-        first_fall = n;
-        found = 0x7fffffff;
-        last_some = -1;
-    }
+    if (threadIdx.x == 0) first_fall = n;
     __syncthreads();
     for (int i = threadIdx.x; i < n; i += kVerifyThreads) {
         const int x = p.tokens[first + i];
@@ -344,104 +450,99 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyPara
 #pragma unroll
             for (int u = 0; u < kBatch; ++u) add(u & 1, v + 32 * u + lane, x[u], y[u]);
         }
-        double sum = (double(s[0].hi) + double(s[1].hi)) + (double(s[0].lo) + double(s[1].lo));
-        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        if (lane == 0) warp_sum[round][warp] = sum;
+        s[0].add(s[1].hi, s[1].lo);
+        for (int o = 16; o > 0; o >>= 1) {
+            const float hi = __shfl_xor_sync(0xffffffffu, s[0].hi, o);
+            const float lo = __shfl_xor_sync(0xffffffffu, s[0].lo, o);
+            s[0].add(hi, lo);
+        }
+        if (lane == 0) warp_sum[warp] = make_float2(s[0].hi, s[0].lo);
         __syncthreads();
-        double mine = 0.0;  // every thread adds in the same order
-        for (int i = 0; i < kVerifyWarps; ++i) mine += warp_sum[round][i];
+        double part = 0.0, incl = 0.0;  // warp 0, one lane per warp of the CTA
+        if (warp == 0) {
+            if (lane < kVerifyWarps) part = double(warp_sum[lane].x) + double(warp_sum[lane].y);
+            incl = inclusive16(part, lane);
+            const double mine = __shfl_sync(0xffffffffu, incl, kVerifyWarps - 1);
+            if (cluster == 1) {
+                if (lane == 0) cta_sum[round][0] = mine;
+                __syncwarp();
+            } else if (lane < cluster) {
+                st_dsmem_f64(map_to_rank(smem_u32(&cta_sum[round][rank]), lane), mine);
+            }
+        }
         if (cluster > 1) {
-            if (threadIdx.x < cluster)
-                st_dsmem_f64(map_to_rank(smem_u32(&cta_sum[round][rank]), threadIdx.x), mine);
             cluster_arrive_release();
             cluster_wait_acquire();
-        } else {
-            if (threadIdx.x == 0) cta_sum[round][0] = mine;
-            __syncthreads();
         }
-        double total = 0.0;
-        for (int i = 0; i < cluster; ++i) total += cta_sum[round][i];
-        if (total > 0.0 && total < INFINITY) {
-            // the CTA, then the warp's piece in which the sum passes the threshold (the
-            // last one with any weight if rounding keeps it below)
-            const double limit = double(p.u_sample[b]) * total;
-            double before = 0.0;
-            int owner = -1, last = 0;
-            double owner_before = 0.0, last_before = 0.0;
-            for (int i = 0; i < cluster; ++i) {
-                const double c = cta_sum[round][i];
-                if (c > 0.0) {
-                    last = i;
-                    last_before = before;
-                }
-                if (owner < 0 && before + c > limit) {
-                    owner = i;
-                    owner_before = before;
-                }
-                before += c;
+        double limit = 0.0;
+        if (warp == 0) {
+            const double c = lane < cluster ? cta_sum[round][lane] : 0.0;
+            const double c_incl = inclusive16(c, lane);
+            const double total = __shfl_sync(0xffffffffu, c_incl, kMaxCluster - 1);
+            limit = double(p.u_sample[b]) * total;
+            double before;
+            const int cta = passing_lane(c, c_incl, 0.0, limit, before);
+            double warp_before = 0.0;
+            const int w = passing_lane(part, incl, before, limit, warp_before);
+            if (lane == 0) {
+                owner_cta = total > 0.0 && total < INFINITY ? cta : -1;
+                owner_warp = w;
+                owner_before = warp_before;
             }
-            if (owner < 0) {
-                owner = last;
-                owner_before = last_before;
+        }
+        __syncthreads();
+        if (owner_cta >= 0) {
+            if (owner_cta != rank) return;
+            // that warp's piece again: a sixteenth of it for each warp, a run of
+            // consecutive elements for each lane
+            const int share = p.piece / kVerifyWarps, each = (share + 31) / 32;
+            const int64_t from =
+                (int64_t(rank) * kVerifyWarps + owner_warp) * p.piece + warp * share;
+            const int64_t stop = min(int64_t(p.V), from + share);
+            const int lo = int(min(stop, from + lane * each));
+            const int hi = int(min(stop, from + lane * each + each));
+            Sum2 run;
+            for (int e = lo; e < hi; ++e) {
+                if (qr) add_difference(run, pr[e], qr[e]);
+                else if (e != gone) add_plain(run, pr[e]);
             }
-            if (owner != rank) return;
-            before = owner_before;
-            owner = -1;
-            last = 0;
-            for (int i = 0; i < kVerifyWarps; ++i) {
-                const double c = warp_sum[round][i];
-                if (c > 0.0) {
-                    last = i;
-                    last_before = before;
-                }
-                if (owner < 0 && before + c > limit) {
-                    owner = i;
-                    owner_before = before;
-                }
-                before += c;
-            }
-            if (owner < 0) {
-                owner = last;
-                owner_before = last_before;
-            }
-            // that piece again, a run of consecutive elements for each thread
-            const int64_t from = (int64_t(rank) * kVerifyWarps + owner) * p.piece;
-            const int each = (p.piece + kVerifyThreads - 1) / kVerifyThreads;
-            const int lo = int(min(int64_t(p.V), from + int64_t(threadIdx.x) * each));
-            const int hi = int(min(min(int64_t(p.V), from + p.piece), int64_t(lo) + each));
-            auto term = [&](int e) {
-                if (e == gone) return 0.0;
-                const double d = double(pr[e]) - (qr ? double(qr[e]) : 0.0);
-                return d > 0.0 ? d : 0.0;
-            };
-            double run = 0.0;
-            for (int e = lo; e < hi; ++e) run += term(e);
-            double incl = run;
+            Sum2 upto = run;
             for (int o = 1; o < 32; o <<= 1) {
-                const double y = __shfl_up_sync(0xffffffffu, incl, o);
-                if (lane >= o) incl += y;
+                const float yh = __shfl_up_sync(0xffffffffu, upto.hi, o);
+                const float yl = __shfl_up_sync(0xffffffffu, upto.lo, o);
+                if (lane >= o) upto.add(yh, yl);
             }
-            if (lane == 31) scan[warp] = incl;
+            const double base = owner_before;
+            if (lane == 31) warp_sum[warp] = make_float2(upto.hi, upto.lo);
             __syncthreads();
-            double at = owner_before;
-            for (int i = 0; i < warp; ++i) at += scan[i];
-            at += incl - run;
-            if (run > 0.0) {
-                int some = lo;
-                for (int e = lo; e < hi; ++e) {
-                    const double w = term(e);
-                    if (w <= 0.0) continue;
-                    some = e;
-                    at += w;
-                    if (at > limit) {
-                        atomicMin(&found, e);
-                        break;
-                    }
+            if (warp == 0) {
+                if (lane < kVerifyWarps) part = double(warp_sum[lane].x) + double(warp_sum[lane].y);
+                double before;
+                const int w =
+                    passing_lane(part, inclusive16(part, lane), base, limit, before);
+                if (lane == 0) {
+                    owner_warp = w;
+                    owner_before = before;
+                    cta_sum[0][0] = limit;
                 }
-                atomicMax(&last_some, some);
             }
             __syncthreads();
-            if (threadIdx.x == 0) p.next[b] = found != 0x7fffffff ? found : last_some;
+            if (warp != owner_warp) return;
+            limit = cta_sum[0][0];
+            double at;
+            const int l = passing_lane(run.value(), upto.value(), owner_before, limit, at);
+            if (lane == l) {
+                int token = lo;
+                for (int e = lo; e < hi; ++e) {
+                    if (e == gone) continue;
+                    const double w = double(pr[e]) - (qr ? double(qr[e]) : 0.0);
+                    if (!(w > 0.0)) continue;
+                    token = e;
+                    at += w;
+                    if (at > limit) break;
+                }
+                p.next[b] = token;
+            }
             return;
         }
         if (!qr && gone < 0) break;
@@ -540,10 +641,10 @@ extern "C" int gqa_attn_qk_norm_rope(
     p.qo_st = fix(qo_stride_t, tokens); p.qo_sh = fix(qo_stride_h, H_q);
     p.ko_st = fix(ko_stride_t, tokens); p.ko_sh = fix(ko_stride_h, H_kv);
     p.tokens = tokens; p.H_q = H_q; p.H_kv = H_kv; p.pairs = pairs; p.eps = eps;
-    const int rounds = (H_q * (d / 8) + 31) / 32;  // of one warp for a token's query heads
-    int block_tokens = 4, split = 1;
+    const int rounds = (H_q * (d / 16) + 31) / 32;  // of one warp for a token's query heads
+    int block_tokens = kNormWarps, split = 1;
     while (block_tokens > 1 && tokens < block_tokens * 4 * sms) block_tokens /= 2;
-    while (tokens * split < 2 * sms && split * 8 < rounds) ++split;
+    while (tokens * split < 2 * sms && split * kNormWarps < rounds) ++split;
     p.block_tokens = block_tokens;
     const dim3 grid(unsigned((tokens + block_tokens - 1) / block_tokens), unsigned(split));
     return (d == 128 ? launch_norm<128>(p, norm != 0, interleaved != 0, grid, stream)
