@@ -72,7 +72,7 @@ constexpr int kMaxTreeTokens = 128;  // drafted tokens of a row: one tile of key
 constexpr int BM = kPrefillBlockM;   // rows of a group
 constexpr int BN = kPrefillBlockN;   // keys of a tile
 constexpr int kThreads = 384;
-constexpr int kRingSlots = 4;        // K/V tiles in flight
+constexpr int kMaxRing = 12;         // K/V tiles in flight, at most (see Geo)
 constexpr int kItemSlots = 4;        // work items known ahead
 constexpr int kSchedSeqs = 1024;     // sequences whose schedule is kept in shared memory
 constexpr int kTreeCtas = 152;       // most CTAs of a decode_tree launch (workspace size)
@@ -93,14 +93,17 @@ constexpr float kRescaleThreshold = 8.f;
 // groups take alternate K/V tiles and are merged in the epilogue (28/4 heads,
 // 5 drafts, contexts of 64 to 9100: 19.0 us against 19.9 as kTreePair, whose
 // second group would be empty).
-// kPagedPair: items are blocks of 2 * tok tokens of a row, a range of the row's
-// keys, which all lie in pages.
-// kPagedAlt: the same where all tokens of a row fit in one group, with the tiles
-// taken in turn as in kTreeAlt.
-enum Mode { kPrompts, kTreePair, kTreeAlt, kPagedPair, kPagedAlt };
+// kPaged: items are blocks of 2 * tok tokens of a row, a range of the row's keys,
+// which all lie in pages. A block of up to tok tokens (a single token beside a chunk of
+// a prompt) runs as in kTreeAlt, the others as in kTreePair.
+// kPagedAlt: the same where no row has more than tok tokens: with room for one group of
+// queries only, the ring of K/V tiles is deeper.
+// kPagedFew: and no more than kFewRows rows of the products (tokens x G).
+enum Mode { kPrompts, kTreePair, kTreeAlt, kPaged, kPagedAlt, kPagedFew };
+constexpr int kFewRows = 32;
 constexpr bool tree_mode(int m) { return m == kTreePair || m == kTreeAlt; }
-constexpr bool paged_mode(int m) { return m == kPagedPair || m == kPagedAlt; }
-constexpr bool alt_mode(int m) { return m == kTreeAlt || m == kPagedAlt; }
+constexpr bool paged_mode(int m) { return m == kPaged || m == kPagedAlt || m == kPagedFew; }
+constexpr bool alt_mode(int m) { return m == kTreeAlt || m == kPagedAlt || m == kPagedFew; }
 
 struct Params {
     const uint16_t* v;            // packed V, read again only for values that are not finite
@@ -127,6 +130,8 @@ struct Params {
     int64_t v_page;               // elements from one V page to the next
     int table_width, page_size, num_pages;
     int single;       // no row has more than one block of tokens
+    int alt;          // nor more than one group of them
+    int q_tok;        // tokens of a Q box: tok, or fewer where no row has as many
     float scale_log2;
     int inject_timeout;  // test hook: block 0 withholds its first Q copy
 };
@@ -147,7 +152,7 @@ struct __align__(16) Item {
     int k_row;   // packed index of the row's first own key
     int off;     // own key of token 0 (keys minus queries)
     int n_own;   // own keys
-    int pad;
+    int alt;     // kPaged: one group of rows, the tiles in turn
 };
 static_assert(sizeof(Item) == 64, "four 16-byte copies");
 
@@ -241,17 +246,29 @@ __device__ __forceinline__ Repair repair_of(const Params& p, const Item& w, int 
 
 // ---- shared memory
 
-template <int D>
+template <int D, int kMode>
 struct Geo {
     static_assert(D == 64 || D == 128, "head dim");
     static constexpr int kBoxes = D / 64;
     static constexpr uint32_t kTileBytes = kBoxes * kBoxBytes;
-    static constexpr uint32_t kQOff = 0;  // two groups
-    static constexpr uint32_t kRingOff = 2 * kTileBytes;
-    static constexpr uint32_t kStageOff = kRingOff + kRingSlots * kTileBytes;  // 8 warps
+    // Q: two groups, or one, or the first rows of one (the products read on behind them,
+    // into the ring, for rows that nobody uses)
+    static constexpr uint32_t kQBoxBytes = kMode == kPagedFew ? kFewRows * 128 : kBoxBytes;
+    static constexpr uint32_t kQBytes = kBoxes * kQBoxBytes;
+    static constexpr int kQGroups = kMode == kPagedAlt || kMode == kPagedFew ? 1 : 2;
+    // K/V tiles in flight: for paged caches as many as fit. (A decode step of 32 rows waits
+    // for HBM: see the figures at load_pages.)
+    static constexpr int kRing = !paged_mode(kMode)    ? 4
+                                 : kMode == kPagedFew ? (D == 128 ? 6 : 12)
+                                 : kMode == kPagedAlt ? (D == 128 ? 5 : 10)
+                                                      : (D == 128 ? 4 : 10);
+    static_assert(kRing <= kMaxRing, "barriers");
+    static constexpr uint32_t kQOff = 0;
+    static constexpr uint32_t kRingOff = kQGroups * kQBytes;
+    static constexpr uint32_t kStageOff = kRingOff + kRing * kTileBytes;  // 8 warps
     static constexpr uint32_t kXchOff = kStageOff + 8 * kStageBytes;  // float4 [2][128]
     static constexpr uint32_t kSeqOff = kXchOff + 2 * BM * 16;        // int2 [kSchedSeqs]
-    static constexpr uint32_t kItemOff = kSeqOff + kSchedSeqs * 8;
+    static constexpr uint32_t kItemOff = kSeqOff + (paged_mode(kMode) ? 0 : kSchedSeqs * 8);
     static constexpr uint32_t kBarOff = kItemOff + kItemSlots * 64;
     static constexpr int kSmemBytes = 1024 + kBarOff + 512;
     static_assert(kSmemBytes <= 232448, "more dynamic shared memory than one CTA may have");
@@ -275,9 +292,9 @@ __device__ __forceinline__ uint32_t col_o_of(int g) { return 256u + uint32_t(g) 
 enum Bar {
     bQFull = 0,                            // Q of an item landed
     bQEmpty,                               // the item's last S products completed
-    bSlotFull,                             // x kRingSlots
-    bSlotEmpty = bSlotFull + kRingSlots,   // x kRingSlots
-    bSFull = bSlotEmpty + kRingSlots,      // x2: S_g ready
+    bSlotFull,                             // x Geo::kRing
+    bSlotEmpty = bSlotFull + kMaxRing,     // x Geo::kRing
+    bSFull = bSlotEmpty + kMaxRing,        // x2: S_g ready
     bPFull = bSFull + 2,                   // x2: P_g ready (4 warps)
     bODone = bPFull + 2,                   // x2: O_g final
     bItemFull = bODone + 2,                // x kItemSlots
@@ -613,7 +630,8 @@ __device__ __forceinline__ void schedule_tree(const Params& p, Publisher& pub, i
 // paged_attention. A unit is a block of tokens of a row against one KV head: tiles
 // 0 .. N - 1 of 128 keys, N from the keys that its last token sees. The units lie in
 // one line, rows one behind the other, their KV heads, their blocks; a unit is as long
-// as its keys and kPagedItemCost of them. The line is cut into equal shares, one to a
+// as its keys, twice where it has two groups of rows (which take twice as long), and
+// kPagedItemCost. The line is cut into equal shares, one to a
 // CTA, so that a step with chunks, drafts and single tokens at once is balanced
 // whatever its lengths. Where a cut falls inside a unit it moves to the nearest
 // boundary of tiles. The blocks' lengths in the line grow evenly (a causal limit) up
@@ -621,7 +639,7 @@ __device__ __forceinline__ void schedule_tree(const Params& p, Publisher& pub, i
 // When every row has one block only and the units can be cut into equal parts, one
 // part to a CTA at most, that is done instead (see schedule_tree).
 constexpr int kPagedItemCost = kItemCost * BN;
-constexpr int kPagedShare = 3 * BN;  // least length of a share: two tiles of any unit it crosses
+constexpr int kPagedShare = 6 * BN;  // least length of a share: two tiles of any unit it crosses
 
 struct PagedRow {
     int q0, T, n, blocks;
@@ -631,18 +649,22 @@ __device__ __forceinline__ int64_t paged_limit(const Params& p, const PagedRow& 
     if (!p.causal || i + 1 >= r.blocks) return r.n;
     return max(0, r.n - r.T + (i + 1) * 2 * p.tok);
 }
+// Block i has one group of rows only.
+__device__ __forceinline__ bool paged_alt(const Params& p, const PagedRow& r, int i) {
+    return p.alt || r.T - i * 2 * p.tok <= p.tok;
+}
 // Length of the first k blocks of a row.
 __device__ __forceinline__ int64_t paged_line(const Params& p, const PagedRow& r, int k) {
     int64_t sum = int64_t(k) * kPagedItemCost;
-    if (!p.causal) return sum + int64_t(k) * r.n;
-    const int64_t block = 2 * p.tok, off = r.n - r.T;
     if (k == r.blocks && k > 0) {
-        sum += r.n;
         --k;
+        sum += paged_alt(p, r, k) ? int64_t(r.n) : 2 * int64_t(r.n);
     }
+    if (!p.causal) return sum + 2 * int64_t(k) * r.n;
+    const int64_t block = 2 * p.tok, off = r.n - r.T;
     // the blocks before `none` see no key
     const int64_t none = off < 0 ? min(-off / block, int64_t(k)) : 0;
-    return sum + (k - none) * off + block * (int64_t(k) * (k + 1) - none * (none + 1)) / 2;
+    return sum + 2 * (k - none) * off + block * (int64_t(k) * (k + 1) - none * (none + 1));
 }
 __device__ __forceinline__ PagedRow paged_row(const Params& p, int b, bool& bad) {
     PagedRow r{0, 0, 0, 0, 0};
@@ -758,11 +780,14 @@ __device__ __forceinline__ void schedule_paged(const Params& p, Publisher& pub, 
                 parts = cuts;
                 ++x;
             } else {
-                const int64_t keys_at = s + kPagedItemCost, stop = keys_at + limit;
+                const int twice = paged_alt(p, r, block) ? 0 : 1;
+                const int64_t keys_at = s + kPagedItemCost;
+                const int64_t stop = keys_at + (int64_t(limit) << twice);
+                const int64_t half = (BN / 2) << twice;  // of a tile
                 // tiles of the unit before a cut at y
                 auto before_cut = [&](int64_t y) {
                     if (y >= stop) return tiles_of;
-                    const int64_t t = (y - keys_at + BN / 2) >> 7;
+                    const int64_t t = (y - keys_at + half) >> (7 + twice);
                     return int(min(max(t, int64_t(0)), int64_t(tiles_of)));
                 };
                 w.j0 = before_cut(x0);
@@ -776,9 +801,9 @@ __device__ __forceinline__ void schedule_paged(const Params& p, Publisher& pub, 
                     auto share_of = [&](int64_t y) {
                         return (y * shares + total - 1) / total - 1;
                     };
-                    const int64_t first = share_of(min(keys_at + BN / 2, stop));
+                    const int64_t first = share_of(min(keys_at + half, stop));
                     const int64_t last =
-                        share_of(min(keys_at + int64_t(tiles_of) * BN - BN / 2, stop));
+                        share_of(min(keys_at + 2 * half * tiles_of - half, stop));
                     parts = int(last - first) + 1;
                 }
                 x = stop;  // the next unit of the line
@@ -788,8 +813,9 @@ __device__ __forceinline__ void schedule_paged(const Params& p, Publisher& pub, 
             w.n_own = r.n;
             w.off = r.n - r.T;
             w.tok0 = block * 2 * p.tok;
+            w.alt = paged_alt(p, r, block);
             w.n = j1 - w.j0;
-            w.n0 = clampi(cdiv(group_last<kPagedPair>(p, w, 0), BN) - w.j0, 0, w.n);
+            w.n0 = clampi(cdiv(group_last<kPaged>(p, w, 0), BN) - w.j0, 0, w.n);
             w.n1 = w.tok0 + p.tok < w.T ? w.n : 0;
             if (!take || (w.n == 0 && tiles_of > 0)) continue;
             // slot 2c + 1 holds the first part of a unit, 2c another one
@@ -806,17 +832,31 @@ __device__ __forceinline__ void schedule_paged(const Params& p, Publisher& pub, 
     pub.put(end, lane);
 }
 
+// Ring position, counted from the item's first, of its V tile j, of n tiles. The tiles
+// are loaded in the order in which their slots come free: K_0 V_0 K_1 V_1 .. where two
+// groups share them, K_0 K_1 V_0 K_2 V_1 .. where the groups take turns (paged caches).
+template <int kMode>
+__device__ __forceinline__ int v_position(int j, int n, bool alt) {
+    return paged_mode(kMode) && alt ? min(2 * j + 2, 2 * n - 1) : 2 * j + 1;
+}
+template <int kMode>
+__device__ __forceinline__ int k_position(int j, bool alt) {
+    return paged_mode(kMode) && alt ? max(2 * j - 1, 0) : 2 * j;
+}
+
 // Copies the K and V tiles of an item from their pages into the ring: a box of a page
 // (or 128 keys of it) and 64 columns for each lane, so that a tile of 16-key pages is in
 // flight with one instruction. The ids of up to 32 pages are read one window ahead of
 // their use. Keys behind the row's last page are not read: what their place in the tile
 // holds gives scores that are masked, and the P V product does not reach them. A page
 // id out of range gives zeros and is reported.
-template <int kBoxes>
-__device__ __forceinline__ void load_pages(const Params& p, const Item& w, int n, int lane,
-                                           const CUtensorMap* tmap_k, const CUtensorMap* tmap_v,
-                                           uint64_t policy, uint64_t* bars, uint32_t ring,
-                                           uint32_t tile_bytes, int r, int& issued, bool& alive) {
+template <int D, int kMode>
+__device__ __forceinline__ void load_pages(const Params& p, const Item& w, int n, bool alt,
+                                           int lane, const CUtensorMap* tmap_k,
+                                           const CUtensorMap* tmap_v, uint64_t policy,
+                                           uint64_t* bars, uint32_t ring, int r, int& issued,
+                                           bool& alive) {
+    using Gm = Geo<D, kMode>;
     const int rows = min(p.page_size, BN);       // keys of a box
     const int per_tile = BN / rows;              // boxes of a tile and 64 columns
     const int per_page = max(1, p.page_size / BN);  // tiles of a page
@@ -828,40 +868,49 @@ __device__ __forceinline__ void load_pages(const Params& p, const Item& w, int n
         return i < pages ? table[i] : 0;
     };
     const int box = lane % per_tile, half = lane / per_tile;
+    // The current window is that of the last V tile; K tiles run at most two tiles
+    // (16 pages) ahead of it.
     int window = 0, ids = fetch(0), next = fetch(1);
 #pragma unroll 1
-    for (int j = 0; j < n && alive; ++j) {
+    for (int i = 0; i < 2 * n && alive; ++i) {
+        int kv, j;
+        if (alt) {
+            j = i & 1 ? (i + 1) >> 1 : max(i - 2, 0) >> 1;
+            kv = i & 1 ? j >= n : i > 0;
+            j = min(j, n - 1);
+        } else {
+            kv = i & 1;
+            j = i >> 1;
+        }
         const int jj = w.j0 + j;
         const int at = (per_page > 1 ? jj / per_page : jj * per_tile) - first;
-        if ((at >> 5) != window) {
+        if (kv && (at >> 5) != window) {
             ++window;
             ids = next;
             next = fetch(window + 1);
         }
-        int page = __shfl_sync(0xffffffffu, ids, (at + box) & 31);
+        int page = __shfl_sync(0xffffffffu, (at >> 5) == window ? ids : next, (at + box) & 31);
         const int slot = per_page > 1 ? jj % per_page * BN : 0;
         const int boxes = min(per_tile, cdiv(w.n_own - jj * BN, rows));
+        const bool mine = box < boxes && half < Gm::kBoxes;
         if (page < 0 || page >= p.num_pages) {
-            if (box < boxes && half < kBoxes) atomicOr(p.status, kStatusBadSeqlen);
+            if (mine) atomicOr(p.status, kStatusBadSeqlen);
             page = p.num_pages;  // outside the tensor: zeros
         }
-#pragma unroll
-        for (int kv = 0; kv < 2; ++kv) {
-            const int ri = r + 2 * j + kv, s = ri % kRingSlots;
-            const uint32_t full = smem_u32(&bars[bSlotFull + s]);
-            if (lane == 0) {
-                if (ri >= kRingSlots)
-                    alive = mbar_wait_bounded(smem_u32(&bars[bSlotEmpty + s]),
-                                              ((ri / kRingSlots) - 1) & 1, p.status);
-                if (alive) mbar_arrive_expect_tx(full, uint32_t(boxes * rows * 128 * kBoxes));
-            }
-            alive = __all_sync(0xffffffffu, alive);
-            if (!alive) break;
-            if (box < boxes && half < kBoxes)
-                tma_load_4d(ring + s * tile_bytes + half * kBoxBytes + box * rows * 128,
-                            kv ? tmap_v : tmap_k, half * 64, slot, w.kvh, page, full, policy);
-            issued = ri + 1;
+        const int ri = r + i, s = ri % Gm::kRing;
+        const uint32_t full = smem_u32(&bars[bSlotFull + s]);
+        if (lane == 0) {
+            if (ri >= Gm::kRing)
+                alive = mbar_wait_bounded(smem_u32(&bars[bSlotEmpty + s]),
+                                          ((ri / Gm::kRing) - 1) & 1, p.status);
+            if (alive) mbar_arrive_expect_tx(full, uint32_t(boxes * rows * 128 * Gm::kBoxes));
         }
+        alive = __all_sync(0xffffffffu, alive);
+        if (!alive) break;
+        if (mine)
+            tma_load_4d(ring + s * Gm::kTileBytes + half * kBoxBytes + box * rows * 128,
+                        kv ? tmap_v : tmap_k, half * 64, slot, w.kvh, page, full, policy);
+        issued = ri + 1;
     }
 }
 
@@ -972,9 +1021,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                   const __grid_constant__ CUtensorMap tmap_v,
                   const __grid_constant__ CUtensorMap tmap_kc,
                   const __grid_constant__ CUtensorMap tmap_vc, const Params p) {
-    using Gm = Geo<D>;
+    using Gm = Geo<D, kMode>;
     constexpr uint32_t kTileBytes = Gm::kTileBytes;
-    constexpr bool kTree = tree_mode(kMode), kPaged = paged_mode(kMode), kAlt = alt_mode(kMode);
+    constexpr int kRing = Gm::kRing;
+    constexpr bool kTree = tree_mode(kMode), kPages = paged_mode(kMode), kAlt = alt_mode(kMode);
+    // items of one group, whose tiles the two softmax groups take in turn
+    auto alt_item = [](const Item& w) {
+        if constexpr (kMode == kPaged) return uniform(w.alt) != 0;
+        else return kAlt;
+    };
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                ~uintptr_t(1023));
@@ -991,7 +1046,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (threadIdx.x == 0) {
         mbar_init(bar(bQFull), 1);
         mbar_init(bar(bQEmpty), 1);
-        for (int s = 0; s < kRingSlots; ++s) {
+        for (int s = 0; s < kRing; ++s) {
             mbar_init(bar(bSlotFull + s), 1);
             mbar_init(bar(bSlotEmpty + s), 1);
         }
@@ -1021,11 +1076,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc::fence_after_sync();
     if (threadIdx.x == 0) {
         tma_prefetch_desc(&tmap_q);
-        if (!kPaged) {
+        if (!kPages) {
             tma_prefetch_desc(&tmap_k);
             tma_prefetch_desc(&tmap_v);
         }
-        if (kTree || kPaged) {
+        if (kTree || kPages) {
             tma_prefetch_desc(&tmap_kc);
             tma_prefetch_desc(&tmap_vc);
         }
@@ -1037,7 +1092,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int wg = warp >> 2;
 
     auto ring_wait = [&](int r) {
-        return mbar_wait_bounded(bar(bSlotFull + r % kRingSlots), (r / kRingSlots) & 1, p.status);
+        return mbar_wait_bounded(bar(bSlotFull + r % kRing), (r / kRing) & 1, p.status);
     };
 
     if (wg == 0) {
@@ -1061,7 +1116,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // among it.
         // Pages are read once when no row has a second block of tokens.
         const uint64_t once =
-            kPaged && !p.single ? l2_policy_evict_normal() : l2_policy_evict_first();
+            kPages && !p.single ? l2_policy_evict_normal() : l2_policy_evict_first();
         int r = 0, q_loads = 0;  // ring items and Q loads before this item
         int issued = 0;          // ring items this lane issued
         bool withheld = false;
@@ -1080,18 +1135,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                     alive = mbar_wait_bounded(bar(bQEmpty), (q_loads - 1) & 1, p.status);
                 if (alive && !withheld) {
                     const int groups = !kAlt && w.tok0 + p.tok < w.T ? 2 : 1;
-                    mbar_arrive_expect_tx(bar(bQFull), groups * Gm::kBoxes * p.G * p.tok * 128);
+                    mbar_arrive_expect_tx(bar(bQFull),
+                                          groups * Gm::kBoxes * p.G * p.q_tok * 128);
                     for (int g = 0; g < groups; ++g)
                         for (int hh = 0; hh < Gm::kBoxes; ++hh)
-                            tma_load(smem_u32(smem + Gm::kQOff + g * kTileBytes) + hh * kBoxBytes,
+                            tma_load(smem_u32(smem + Gm::kQOff + g * kTileBytes) +
+                                         hh * Gm::kQBoxBytes,
                                      &tmap_q, hh * 64, w.kvh * p.G, w.q_row + w.tok0 + g * p.tok,
                                      bar(bQFull));
                 }
 #pragma unroll 1
-                for (int i = 0; !kPaged && i < 2 * n && alive; ++i) {  // K_0, V_0, K_1, V_1, ...
-                    const int ri = r + i, s = ri % kRingSlots;
-                    if (ri >= kRingSlots)
-                        alive = mbar_wait_bounded(bar(bSlotEmpty + s), ((ri / kRingSlots) - 1) & 1,
+                for (int i = 0; !kPages && i < 2 * n && alive; ++i) {  // K_0, V_0, K_1, V_1, ...
+                    const int ri = r + i, s = ri % kRing;
+                    if (ri >= kRing)
+                        alive = mbar_wait_bounded(bar(bSlotEmpty + s), ((ri / kRing) - 1) & 1,
                                                   p.status);
                     if (!alive) break;
                     const int jj = w.j0 + (i >> 1);
@@ -1109,10 +1166,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     issued = ri + 1;
                 }
             }
-            if constexpr (kPaged) {
+            if constexpr (kPages) {
                 alive = __all_sync(0xffffffffu, alive);
-                load_pages<Gm::kBoxes>(p, w, n, lane, &tmap_kc, &tmap_vc, once, bars, smem_u32(smem + Gm::kRingOff),
-                                       kTileBytes, r, issued, alive);
+                load_pages<D, kMode>(p, w, n, alt_item(w), lane, &tmap_kc, &tmap_vc, once, bars,
+                                     smem_u32(smem + Gm::kRingOff), r, issued, alive);
             }
             if (!withheld) ++q_loads;
             if (!__all_sync(0xffffffffu, alive) || withheld) break;
@@ -1121,20 +1178,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         // Every copy still in flight lands before the CTA exits.
         if (lane == 0) {
             if (q_loads > 0) mbar_wait_bounded(bar(bQFull), (q_loads - 1) & 1, p.status);
-            for (int i = max(0, issued - kRingSlots); i < issued; ++i) ring_wait(i);
+            for (int i = max(0, issued - kRing); i < issued; ++i) ring_wait(i);
         }
       } else if (warp == 1) {
         // -------------------------------------------------------- MMA issuer
         const uint32_t idesc_s = tc::idesc_bf16_f32(BM, BN, false);
         const uint32_t idesc_pv = tc::idesc_bf16_f32(BM, D, true);
         auto slot_addr = [&](int i) {
-            return smem_u32(smem + Gm::kRingOff + (i % kRingSlots) * kTileBytes);
+            return smem_u32(smem + Gm::kRingOff + (i % kRing) * kTileBytes);
         };
         const uint64_t qdesc0 = tc::sdesc_sw128(smem_u32(smem + Gm::kQOff), 16, 1024);
         const uint64_t qdesc1 = tc::sdesc_sw128(smem_u32(smem + Gm::kQOff + kTileBytes), 16, 1024);
         // S_g = Q K^T with K in ring item ri (kTreeAlt: both groups hold the same rows)
-        auto issue_s = [&](int g, int ri) {
-            const uint64_t qdesc = !kAlt && g ? qdesc1 : qdesc0;
+        auto issue_s = [&](int g, int ri, bool one_group = alt_mode(kMode)) {
+            const uint64_t qdesc = !one_group && g ? qdesc1 : qdesc0;
             const uint64_t kdesc = tc::sdesc_sw128(slot_addr(ri), 16, 1024);
             const uint32_t qlo = uint32_t(qdesc), qhi = uint32_t(qdesc >> 32);
             const uint32_t klo = uint32_t(kdesc), khi = uint32_t(kdesc >> 32);
@@ -1143,7 +1200,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int kk = 1; kk < D / 16; ++kk) {
                 const uint32_t o = ((kk >> 2) * kBoxBytes + (kk & 3) * 32) >> 4;
-                tc::mma_ss_lo<1>(dst, qlo + o, qhi, klo + o, khi, idesc_s);
+                const uint32_t oq = ((kk >> 2) * Gm::kQBoxBytes + (kk & 3) * 32) >> 4;
+                tc::mma_ss_lo<1>(dst, qlo + oq, qhi, klo + o, khi, idesc_s);
             }
             tc::commit(bar(bSFull + g));
         };
@@ -1169,18 +1227,19 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int n = uniform(w.n);
             if (n < 0) break;
             if (n == 0) continue;
-            const int n0 = kAlt ? (n + 1) >> 1 : uniform(w.n0), n1 = kAlt ? n >> 1 : uniform(w.n1);
+            const bool alt = alt_item(w);
+            const int n0 = alt ? (n + 1) >> 1 : uniform(w.n0), n1 = alt ? n >> 1 : uniform(w.n1);
             // tiles before `plain` need no repair and count with all their keys;
             // the last tile of a group (kPrompts), the context's last and the
             // drafted tokens' tile (decode_tree) may count with fewer
             const int plain = uniform(plain_tiles<kMode>(p, w, 0));
             const int j_own = uniform(w.c_t - w.j0);
             const int k0 = uniform(
-                kTree ? w.n_own : tile_keys<kMode>(p, w, w.j0 + (kAlt ? n : n0) - 1, 0));
+                kTree ? w.n_own : tile_keys<kMode>(p, w, w.j0 + (alt ? n : n0) - 1, 0));
             const int k1 = uniform(kTree ? w.ctx - (w.c_t - 1) * BN
                                          : tile_keys<kMode>(p, w, w.j0 + n1 - 1, 1));
             auto keys_of = [&](int j, int g) {
-                if (kPaged && kAlt) return j + 1 < n ? BN : k0;
+                if (kPages && alt) return j + 1 < n ? BN : k0;
                 if (!kTree) return j + 1 < (g ? n1 : n0) ? BN : (g ? k1 : k0);
                 return j < plain ? BN : (j < j_own ? k1 : k0);
             };
@@ -1197,25 +1256,66 @@ __global__ void __launch_bounds__(kThreads, 1)
             bool alive = true;
             // Tiles that both groups run whole and that are not a group's last:
             // no conditions between the issues, which are on the critical path.
-            const int fast = kAlt ? 0 : min(plain, min(n0, n1) - 1);
+            const int fast = alt ? 0 : min(plain, min(n0, n1) - 1);
             if (lane == 0) {
                 if (fast <= 0) {
                     ask(0);
-                    ask(1);
+                    // (a ring of four: K_0 has the slot of V_1 before it)
+                    if (!kPages || !alt) ask(1);
                 }
                 alive = mbar_wait_bounded(bar(bQFull), qi & 1, p.status) && ring_wait(r);
+                if (kPages && alt && alive) ask(1);
             }
             if (lane == 0 && alive) {
               tc::fence_after_sync();
-              if constexpr (kAlt) {
+              if (kPages && alt) {
+                // Each product waits for its own operands only: K and V come from HBM at
+                // the pace of the whole GPU, and a slot given back early is loaded early.
+                issue_s(0, r, true);
+                tc::commit(bar(bSlotEmpty + r % kRing));
+                if (n > 1) {
+                    alive = ring_wait(r + 1);
+                    if (alive) {
+                        tc::fence_after_sync();
+                        issue_s(1, r + 1, true);
+                        tc::commit(bar(bSlotEmpty + (r + 1) % kRing));
+                    }
+                }
+                if (n <= 2) tc::commit(bar(bQEmpty));
+#pragma unroll 1
+                for (int j = 0; j < n && alive; ++j) {
+                    const int g = j & 1;
+                    const int rv = r + v_position<kMode>(j, n, true);
+                    const int rk = r + k_position<kMode>(j + 2, true);
+                    alive = ring_wait(rv) && repaired(j);
+                    if (!alive) break;
+                    ask(j + 2);
+                    alive = mbar_wait_bounded(bar(bPFull + g), ((g ? t1 : t0) + (j >> 1)) & 1,
+                                              p.status);
+                    if (!alive) break;
+                    tc::fence_after_sync();
+                    issue_pv(g, rv, j < 2, keys_of(j, 0));
+                    tc::commit(bar(bSlotEmpty + rv % kRing));
+                    if (j + 2 < n) {
+                        alive = ring_wait(rk);
+                        if (!alive) break;
+                        tc::fence_after_sync();
+                        issue_s(g, rk, true);  // K_{j+2}
+                        tc::commit(bar(bSlotEmpty + rk % kRing));
+                        if (j + 3 == n) tc::commit(bar(bQEmpty));
+                    } else {
+                        tc::commit(bar(bODone + g));
+                    }
+                }
+              } else if constexpr (kAlt) {
                 issue_s(0, r);
-                tc::commit(bar(bSlotEmpty + r % kRingSlots));
+                tc::commit(bar(bSlotEmpty + r % kRing));
                 if (n > 1) {
                     alive = ring_wait(r + 2);
                     if (alive) {
                         tc::fence_after_sync();
                         issue_s(1, r + 2);
-                        tc::commit(bar(bSlotEmpty + (r + 2) % kRingSlots));
+                        tc::commit(bar(bSlotEmpty + (r + 2) % kRing));
                     }
                 }
                 if (n <= 2) tc::commit(bar(bQEmpty));
@@ -1230,10 +1330,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (!alive) break;
                     tc::fence_after_sync();
                     issue_pv(g, rv, j < 2, keys_of(j, 0));
-                    tc::commit(bar(bSlotEmpty + rv % kRingSlots));
+                    tc::commit(bar(bSlotEmpty + rv % kRing));
                     if (j + 2 < n) {
                         issue_s(g, rv + 3);  // K_{j+2}
-                        tc::commit(bar(bSlotEmpty + (rv + 3) % kRingSlots));
+                        tc::commit(bar(bSlotEmpty + (rv + 3) % kRing));
                         if (j + 3 == n) tc::commit(bar(bQEmpty));
                     } else {
                         tc::commit(bar(bODone + g));
@@ -1244,7 +1344,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 auto last_user = [&](int t) { return t < n1 ? 1 : 0; };
                 if (n0 > 0) issue_s(0, r);
                 if (n1 > 0) issue_s(1, r);
-                tc::commit(bar(bSlotEmpty + r % kRingSlots));
+                tc::commit(bar(bSlotEmpty + r % kRing));
                 if (n == 1) tc::commit(bar(bQEmpty));
                 int j = 0;
 #pragma unroll 1
@@ -1260,9 +1360,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (!alive) break;
                     tc::fence_after_sync();
                     issue_pv(1, rv, j == 0, kAllKeys);
-                    tc::commit(bar(bSlotEmpty + rv % kRingSlots));
+                    tc::commit(bar(bSlotEmpty + rv % kRing));
                     issue_s(1, rv + 1);
-                    tc::commit(bar(bSlotEmpty + (rv + 1) % kRingSlots));
+                    tc::commit(bar(bSlotEmpty + (rv + 1) % kRing));
                     if (j + 2 == n) tc::commit(bar(bQEmpty));
                 }
                 if (j > 0 && alive) {
@@ -1284,11 +1384,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (!alive) break;
                         tc::fence_after_sync();
                         issue_pv(g, rv, j == 0, keys_of(j, g));
-                        if (g == last_user(j)) tc::commit(bar(bSlotEmpty + rv % kRingSlots));
+                        if (g == last_user(j)) tc::commit(bar(bSlotEmpty + rv % kRing));
                         if (j + 1 < n_g) {
                             issue_s(g, rv + 1);
                             if (g == last_user(j + 1)) {
-                                tc::commit(bar(bSlotEmpty + (rv + 1) % kRingSlots));
+                                tc::commit(bar(bSlotEmpty + (rv + 1) % kRing));
                                 if (j + 2 == n) tc::commit(bar(bQEmpty));
                             }
                         } else {
@@ -1314,7 +1414,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         Publisher pub{smem + Gm::kItemOff, bars, p.status};
         if constexpr (kTree)
             schedule_tree<kMode>(p, pub, lane);
-        else if constexpr (kPaged)
+        else if constexpr (kPages)
             schedule_paged(p, pub, lane);
         else
             schedule_prompts(p, reinterpret_cast<int2*>(smem + Gm::kSeqOff), pub, lane);
@@ -1332,13 +1432,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (w.n < 0) break;
             for (int j = plain_tiles<kMode>(p, w, 0); j < w.n && alive; ++j) {
                 const Repair fix = repair_of<kMode>(p, w, w.j0 + j);
-                const int ri = r + 2 * j + 1;
+                const int ri = r + v_position<kMode>(j, w.n, alt_item(w));
                 alive = __all_sync(0xffffffffu,
                                    mbar_wait_bounded(bar(bFixAsk + (f & 1)), (f >> 1) & 1,
                                                      p.status)) &&
                         __all_sync(0xffffffffu, ring_wait(ri));
                 if (!alive) break;
-                const uint32_t tile = smem_u32(smem + Gm::kRingOff + (ri % kRingSlots) * kTileBytes);
+                const uint32_t tile = smem_u32(smem + Gm::kRingOff + (ri % kRing) * kTileBytes);
                 // Four 16-byte pieces a lane at a time; a piece without a halfword
                 // whose exponent is all ones (x has none if no lane of
                 // ~x & (0x7f80, 0x7f80) is 0) is left as it is.
@@ -1412,6 +1512,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool alive = true;
         int tt = 0;              // tiles this group finished: its S phases
         int done0 = 0, done1 = 0;  // O_0, O_1 phases (kTreeAlt reads both, else its own)
+        auto done_phases = [&](const Item& w) {  // kPaged: an item's, for both
+            if constexpr (kMode == kPaged) {
+                done0 += alt_item(w) ? w.n > 0 : w.n0 > 0;
+                done1 += alt_item(w) ? w.n > 1 : w.n1 > 0;
+            }
+        };
         int xk = 0;
         auto wait_all = [&](int b, int phase) {
             return bool(__all_sync(0xffffffffu, mbar_wait_bounded(bar(b), phase & 1, p.status)));
@@ -1428,16 +1534,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                 smem_u32(smem + Gm::kItemOff + (it % kItemSlots) * sizeof(Item));
             const Item w = read_item(item_addr);
             if (uniform(w.n) < 0) break;
-            const int tok0 = kAlt ? w.tok0 : w.tok0 + g * p.tok;
+            const bool alt = alt_item(w);
+            const int tok0 = alt ? w.tok0 : w.tok0 + g * p.tok;
             const int count = uniform(min(p.tok, w.T - tok0));  // tokens of this group
             if (count <= 0) {
+                done_phases(w);
                 done_with_item();
                 continue;
             }
-            const int ng = uniform(kAlt ? (w.n + 1 - g) >> 1 : (g ? w.n1 : w.n0));
+            const int ng = uniform(alt ? (w.n + 1 - g) >> 1 : (g ? w.n1 : w.n0));
             // some row of this warp is valid
             const bool act = __any_sync(0xffffffffu, row_tok < count);
-            if (kPaged && !kAlt && ng == 0 && w.dst >= 0) {  // ... in this part of the keys
+            if (kPages && !alt && ng == 0 && w.dst >= 0) {  // ... in this part of the keys
                 if (row_tok < count) {
                     const int prow = (g * p.tok + row_tok) * p.G + row_head;
                     float4* dst = reinterpret_cast<float4*>(p.part_o) +
@@ -1447,11 +1555,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                         dst[size_t(i) * p.part_rows] = make_float4(0.f, 0.f, 0.f, 0.f);
                     p.part_lse[size_t(w.dst) * p.part_rows + prow] = -INFINITY;
                 }
+                done_phases(w);
                 done_with_item();
                 continue;
             }
-            if (!kTree && (kAlt ? w.n : ng) == 0) {  // queries that see no key
-                if (row_tok < count && (!kAlt || g == 0)) {
+            if (!kTree && (alt ? w.n : ng) == 0) {  // queries that see no key
+                if (row_tok < count && (!alt || g == 0)) {
                     const size_t orow = (size_t(w.q_row) + tok0 + row_tok) * p.H_q +
                                         w.kvh * p.G + row_head;
                     uint4* dst = reinterpret_cast<uint4*>(p.o + orow * D);
@@ -1459,12 +1568,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int i = 0; i < D / 8; ++i) dst[i] = make_uint4(0, 0, 0, 0);
                     if (p.lse) p.lse[orow] = -INFINITY;
                 }
+                done_phases(w);
                 done_with_item();
                 continue;
             }
             // Keys of tile i that this row sees, for the tiles from `plain` on:
             // c < last - 128 i. The drafted tokens' tile goes by the bits.
-            const int plain = uniform(plain_tiles<kMode>(p, w, kTree || kAlt ? 0 : g));
+            const int plain = uniform(plain_tiles<kMode>(p, w, kTree || alt ? 0 : g));
             const int last = (kTree ? w.ctx : token_limit(p, w, tok0 + row_tok)) - w.j0 * BN;
             const int own_tile = kTree ? uniform(w.c_t - w.j0) : 0;
             uint32_t bits[4] = {0, 0, 0, 0};  // drafted tokens this row sees
@@ -1486,7 +1596,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t pk[2][32];  // the last tile's P, not in lb yet
 #pragma unroll 1
             for (int i = 0; i < ng && alive; ++i) {
-                if (!kAlt && act && i > 0) st.lb += rounded_sum(pk);
+                if (!alt && act && i > 0) st.lb += rounded_sum(pk);
                 alive = wait_all(bSFull + g, tt + i);
                 if (!alive) break;
                 if (act) {
@@ -1500,7 +1610,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int e = 0; e < 32; ++e) sv[c * 32 + e] = __uint_as_float(x[e]);
                     }
                     tc::tmem_wait_ld();
-                    const int j = kAlt ? 2 * i + g : i;
+                    const int j = alt ? 2 * i + g : i;
                     if (j >= plain) {
                         if (kTree && j >= own_tile) {
 #pragma unroll
@@ -1540,18 +1650,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(bPFull + g));
-                if (kAlt && act) st.lb += rounded_sum(pk);
+                if (alt && act) st.lb += rounded_sum(pk);
             }
             if (!alive) break;
-            if (!kAlt && act && ng > 0) st.lb += rounded_sum(pk);
+            if (!alt && act && ng > 0) st.lb += rounded_sum(pk);
             tt += ng;
 
             // ---- epilogue. Every read of O completes before this warp's next
             // P arrive, which is what lets the next item overwrite O.
             float f0 = 1.f, f1 = 0.f;  // weights of O_0 and O_1 (kTreeAlt)
             const Item e = read_item(item_addr);
-            const bool two = kAlt && uniform(e.n) > 1;
-            if constexpr (kAlt) {
+            const bool two = alt && uniform(e.n) > 1;
+            if (alt) {
                 xch[g * BM + row] = make_float4(st.m, st.l, st.lb, 0.f);
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(bXch));
@@ -1566,42 +1676,42 @@ __global__ void __launch_bounds__(kThreads, 1)
                 st.lb = f0 * a.z + f1 * b.z;
             }
             // (what does not need O comes before the wait for it)
-            const int t = (kAlt ? e.tok0 : e.tok0 + g * p.tok) + row_tok;
+            const int t = (alt ? e.tok0 : e.tok0 + g * p.tok) + row_tok;
             const bool valid = row_tok < p.tok && t < e.T;
-            const bool own = kPaged || e.j0 + e.n > e.c_t;  // the item has the row's own tokens
+            const bool own = kPages || e.j0 + e.n > e.c_t;  // the item has the row's own tokens
             const size_t orow = (size_t(e.q_row) + t) * p.H_q + e.kvh * p.G + row_head;
-            const bool direct = (!kTree && !kPaged) || uniform(e.dst) < 0;
+            const bool direct = (!kTree && !kPages) || uniform(e.dst) < 0;
             // row of the item's token block
             const int prow = (t - e.tok0) * p.G + row_head;
             const RowPtrs rows(
                 valid && direct ? reinterpret_cast<uint8_t*>(p.o + orow * D) : nullptr, lane);
             // the sums are 0 only for a row that saw no key (and NaN stays NaN)
             const float inv = st.lb == 0.f ? 0.f : 1.f / st.lb;
-            if (valid && (!kAlt || g == 0)) {
+            if (valid && (!alt || g == 0)) {
                 const float lse = st.l == 0.f ? -INFINITY : (st.m + log2f(st.l)) * kLn2;
                 if (!direct)
                     p.part_lse[size_t(e.dst) * p.part_rows + prow] = lse;
                 else if (p.lse)
                     p.lse[orow] = lse;
             }
-            if constexpr (kAlt) {
+            if (alt) {
                 alive = wait_all(bODone, done0) && (!two || wait_all(bODone + 1, done1));
-                done1 += two;
+                if (kMode != kPaged) done1 += two;
             } else {
-                alive = wait_all(bODone + g, done0);
+                alive = wait_all(bODone + g, kMode == kPaged && g ? done1 : done0);
             }
             if (!alive) break;
-            ++done0;
+            if (kMode != kPaged) ++done0;
             if (act) {
                 tc::fence_after_sync();
                 const bool odd = *odd_values != 0 && own;
-                const int c_begin = kAlt ? g * (D / 64) : 0;
-                const int c_end = kAlt ? (g + 1) * (D / 64) : D / 32;
+                const int c_begin = alt ? g * (D / 64) : 0;
+                const int c_end = alt ? (g + 1) * (D / 64) : D / 32;
 #pragma unroll 1
                 for (int c = c_begin; c < c_end; ++c) {
                     uint32_t x[32];
-                    tc::tmem_ld32(lane_base + (kAlt ? col_o_of(0) : col_o) + c * 32, x);
-                    if constexpr (kAlt) {
+                    tc::tmem_ld32(lane_base + (alt ? col_o_of(0) : col_o) + c * 32, x);
+                    if (alt) {
                         if (two) {
                             uint32_t y[32];
                             tc::tmem_ld32(lane_base + col_o_of(1) + c * 32, y);
@@ -1618,7 +1728,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         // row sees: those that this row sees are added here
                         int k_end = kTree ? e.n_own : token_limit(p, e, t);
                         int k = kTree ? 0 : group_first<kMode>(p, e, 0);
-                        if (kPaged) {  // of this item's tiles
+                        if (kPages) {  // of this item's tiles
                             k = max(k, e.j0 * BN);
                             k_end = min(k_end, (e.j0 + e.n) * BN);
                         }
@@ -1630,7 +1740,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 if (!((word >> (k & 31)) & 1)) continue;
                             }
                             const uint16_t* vr;
-                            if constexpr (kPaged) {
+                            if constexpr (kPages) {
                                 const int page =
                                     p.table[size_t(e.b) * p.table_width + k / p.page_size];
                                 if (page < 0 || page >= p.num_pages) continue;
@@ -1670,7 +1780,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
             }
-            if constexpr (kAlt) {
+            if (alt) {
                 // both groups have read O_0, O_1 and xch
                 tc::fence_before_sync();
                 __syncwarp();
@@ -1679,6 +1789,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!alive) break;
                 ++xk;
             }
+            done_phases(e);
             done_with_item();
         }
     }
@@ -1877,11 +1988,11 @@ int launch_ragged(const Maps& m, const Params& p, int ctas, cudaStream_t stream)
     const int dev = current_device();
     if (device_attrs_pending(attr_done, dev)) {
         if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 Geo<D>::kSmemBytes) != cudaSuccess)
+                                 (Geo<D, kMode>::kSmemBytes)) != cudaSuccess)
             return GQA_ERR_CUDA;
         device_attrs_mark(attr_done, dev);
     }
-    return launch(kern, unsigned(ctas), kThreads, Geo<D>::kSmemBytes, stream, m.q, m.k, m.v, m.kc,
+    return launch(kern, unsigned(ctas), kThreads, (Geo<D, kMode>::kSmemBytes), stream, m.q, m.k, m.v, m.kc,
                   m.vc, p) == cudaSuccess
                ? GQA_OK
                : GQA_ERR_CUDA;
@@ -1895,7 +2006,7 @@ bool packed_maps(Maps& m, const Params& p, const uint16_t* q, const uint16_t* k,
     // a dimension of size 1 has no stride of its own
     auto fix = [](int64_t s, int64_t n) { return n > 1 ? uint64_t(s) : uint64_t(8); };
     if (encode_tmap_3d_bf16_strided(&m.q, q, d, p.H_q, p.total_q, fix(q_sh, p.H_q),
-                                    fix(q_st, p.total_q), p.G, p.tok) != cudaSuccess)
+                                    fix(q_st, p.total_q), p.G, p.q_tok) != cudaSuccess)
         return false;
     m.k = m.v = m.kc = m.vc = m.q;  // never read unless set
     if (p.total_k == 0) return true;
@@ -2089,7 +2200,7 @@ extern "C" int gqa_attn_prefill_packed(const uint16_t* q, const uint16_t* k, con
     p.v_st = v_stride_t; p.v_sh = v_stride_h;
     p.B = B; p.H_q = H_q; p.H_kv = H_kv; p.G = H_q / H_kv; p.total_q = total_q; p.total_k = total_k;
     p.causal = causal != 0;
-    p.tok = BM / p.G;
+    p.tok = p.q_tok = BM / p.G;
     p.scale_log2 = scale * kLog2e;
     p.inject_timeout = take_injected_timeout() ? 1 : 0;
     // at most this many blocks, however the tokens are spread over the rows
@@ -2160,7 +2271,7 @@ extern "C" int gqa_attn_decode_tree(
     p.B = B; p.H_q = H_q; p.H_kv = H_kv; p.G = H_q / H_kv; p.total_q = total; p.total_k = total;
     p.S_max = S_max; p.max_tokens = max_tokens; p.mask_words = mask_words;
     p.causal = 1;
-    p.tok = plan.tok; p.team = plan.team; p.part_rows = plan.part_rows;
+    p.tok = p.q_tok = plan.tok; p.team = plan.team; p.part_rows = plan.part_rows;
     p.scale_log2 = scale * kLog2e;
     p.inject_timeout = take_injected_timeout() ? 1 : 0;
     // no more teams than there can be tiles, or units that are not cut
@@ -2316,6 +2427,8 @@ extern "C" int gqa_attn_paged_attention(
     p.causal = causal != 0;
     p.tok = plan.tok; p.team = 1; p.part_rows = plan.part_rows;
     p.single = max_tokens <= 2 * plan.tok;
+    p.alt = plan.alt;
+    p.q_tok = plan.alt ? max_tokens : plan.tok;
     p.scale_log2 = scale * kLog2e;
     p.inject_timeout = take_injected_timeout() ? 1 : 0;
     // no more CTAs than there can be tiles, or units that are not cut
@@ -2341,13 +2454,15 @@ extern "C" int gqa_attn_paged_attention(
                                    num_pages > 1 ? v_page_stride : page, rows) != cudaSuccess)
             return GQA_ERR_CUDA;
     }
-    int rl;
-    if (d == 128)
-        rl = plan.alt ? launch_ragged<128, kPagedAlt>(m, p, ctas, stream)
-                      : launch_ragged<128, kPagedPair>(m, p, ctas, stream);
-    else
-        rl = plan.alt ? launch_ragged<64, kPagedAlt>(m, p, ctas, stream)
-                      : launch_ragged<64, kPagedPair>(m, p, ctas, stream);
+    const bool few = plan.alt && max_tokens * p.G <= kFewRows;
+    auto run = [&](auto dim) {
+        constexpr int D = decltype(dim)::value;
+        return few        ? launch_ragged<D, kPagedFew>(m, p, ctas, stream)
+               : plan.alt ? launch_ragged<D, kPagedAlt>(m, p, ctas, stream)
+                          : launch_ragged<D, kPaged>(m, p, ctas, stream);
+    };
+    const int rl = d == 128 ? run(std::integral_constant<int, 128>{})
+                            : run(std::integral_constant<int, 64>{});
     if (rl != GQA_OK || p.whole || ctas == 1) return rl;
     const int64_t tasks = int64_t(ctas) * ((p.part_rows + 31) / 32) * (d / 32);
     const unsigned grid = unsigned(tasks < 2 * kTreeCtas ? tasks : 2 * kTreeCtas);
