@@ -14,6 +14,7 @@ or ``__graft_entry__.build()``); loading fails loudly otherwise.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 import threading
@@ -944,18 +945,33 @@ def cache_append(k_cache, v_cache, k_new, v_new, starts, *, cu_seqlens=None, ind
         _in_use(torch, dev, stream, k_cache, v_cache, k_new, v_new, starts, cu_seqlens, index)
 
 
-def _like(torch, name, t, given, dtype, shape, stream):
-    """An output: the caller's, checked, or a new one from the launch stream's pool."""
-    if given is not None:
-        if (given.dtype is not dtype or given.shape != shape or not given.is_contiguous()
-                or given.get_device() != t.get_device()):
-            raise ValueError(f"{name} must be a contiguous {dtype} tensor of {tuple(shape)} on "
-                             f"{t.device}")
-        return given
+def _empty(torch, t, shape, dtype, stream):
+    """New memory beside t, from the launch stream's pool: what the current stream still reads is
+    not overwritten."""
     if stream is None:
         return torch.empty(shape, dtype=dtype, device=t.device)
     with torch.cuda.stream(stream):
         return torch.empty(shape, dtype=dtype, device=t.device)
+
+
+def _counts(torch, name, t, given, n):
+    if (given.dtype is not torch.int32 or given.shape != (n,) or not given.is_contiguous()
+            or given.get_device() != t.get_device()):
+        raise ValueError(f"{name} must be a contiguous int32 [{n}] tensor on {t.device}")
+    return given
+
+
+def _weight(torch, name, t, d, device):
+    if not isinstance(t, torch.Tensor) or t.dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"{name} must be a bfloat16 or float32 CUDA tensor")
+    if t.get_device() != device or t.shape != (d,) or t.stride(0) != 1:
+        raise ValueError(f"{name} must be a contiguous [{d}] tensor on cuda:{device}")
+    return t.dtype is torch.float32
+
+
+@functools.lru_cache(maxsize=256)
+def _paged_workspace(H_q, H_kv, d, max_tokens):
+    return lib().gqa_attn_paged_attention_workspace_size(H_q, H_kv, d, max_tokens)
 
 
 def _floats(torch, name, t, n, device):
@@ -1024,43 +1040,48 @@ def qk_norm_rope(q, k, positions, inv_freq, *, q_weight=None, k_weight=None,
         raise ValueError("k_out and k_weight need k")
     pairs = inv_freq.numel() if isinstance(inv_freq, torch.Tensor) else 0
     freq = _floats(torch, "inv_freq", inv_freq, pairs, dev)
-    axes, sec = 1, None
-    if sections is not None:
+    if sections is None:
+        axes, sec, want = 1, None, (n,)
+    else:
         axes = len(sections)
-        sec = (ctypes.c_int32 * axes)(*sections)
+        sec, want = (ctypes.c_int32 * axes)(*sections), (axes, n)
     pos = _ints(torch, "positions", positions, axes * n, dev)
-    if positions.shape != ((n,) if sections is None else (axes, n)):
+    if positions.shape != want:
         raise ValueError(f"positions must be {'[tokens]' if sections is None else '[axes, tokens]'}"
                          f", got {tuple(positions.shape)}")
-    wide = None
-    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
-        if w is None:
-            continue
-        if not isinstance(w, torch.Tensor) or w.dtype not in (torch.bfloat16, torch.float32):
-            raise TypeError(f"{name} must be a bfloat16 or float32 CUDA tensor")
-        if w.get_device() != dev or w.shape != (d,) or w.stride(0) != 1:
-            raise ValueError(f"{name} must be a contiguous [{d}] tensor on cuda:{dev}")
-        if wide is not None and wide != (w.dtype is torch.float32):
+    qw = kw = wide = None
+    if q_weight is not None:
+        wide = _weight(torch, "q_weight", q_weight, d, dev)
+        qw = q_weight.data_ptr()
+    if k_weight is not None:
+        wide_k = _weight(torch, "k_weight", k_weight, d, dev)
+        if wide is not None and wide != wide_k:
             raise TypeError("q_weight and k_weight must have one type")
-        wide = w.dtype is torch.float32
+        wide, kw = wide_k, k_weight.data_ptr()
     if eps is None and wide is not None:
         raise ValueError("weights need the norm (eps)")
     if q_out is None:
-        q_out = _like(torch, "q_out", q, None, torch.bfloat16, q.shape, stream)
-    elif q_out.shape != q.shape:
-        raise ValueError("q_out must be shaped like q")
-    qos, qoh = _packed(torch, "q_out", q_out, H_q, d, dev)
+        q_out = _empty(torch, q, q.shape, torch.bfloat16, stream)
+        qos, qoh = H_q * d, d
+    else:
+        if q_out.shape != q.shape:
+            raise ValueError("q_out must be shaped like q")
+        qos, qoh = _packed(torch, "q_out", q_out, H_q, d, dev)
+    k_ptr = ko_ptr = None
     if k is not None:
         if k_out is None:
-            k_out = _like(torch, "k_out", k, None, torch.bfloat16, k.shape, stream)
-        elif k_out.shape != k.shape:
-            raise ValueError("k_out must be shaped like k")
-        kos, koh = _packed(torch, "k_out", k_out, H_kv, d, dev)
+            k_out = _empty(torch, k, k.shape, torch.bfloat16, stream)
+            kos, koh = H_kv * d, d
+        else:
+            if k_out.shape != k.shape:
+                raise ValueError("k_out must be shaped like k")
+            kos, koh = _packed(torch, "k_out", k_out, H_kv, d, dev)
+        k_ptr, ko_ptr = k.data_ptr(), k_out.data_ptr()
     rc = _on_device(torch, dev, lambda: lib().gqa_attn_qk_norm_rope(
-        q.data_ptr(), _ptr(k), q_out.data_ptr(), _ptr(k_out), _ptr(q_weight), _ptr(k_weight),
-        1 if wide else 0, pos, freq, sec, axes, n, H_q, H_kv, d, pairs, 1 if interleaved else 0,
-        0 if eps is None else 1, 0.0 if eps is None else float(eps), qs, qh, ks, kh, qos, qoh, kos,
-        koh, _raw_stream(torch, dev, stream)))
+        q.data_ptr(), k_ptr, q_out.data_ptr(), ko_ptr, qw, kw, 1 if wide else 0, pos, freq, sec,
+        axes, n, H_q, H_kv, d, pairs, 1 if interleaved else 0, 0 if eps is None else 1,
+        0.0 if eps is None else eps, qs, qh, ks, kh, qos, qoh, kos, koh,
+        _raw_stream(torch, dev, stream)))
     if rc != GQA_OK:
         raise GqaError(rc, "gqa_attn_qk_norm_rope")
     if stream is not None:
@@ -1141,8 +1162,8 @@ def paged_attention(q, k_pages, v_pages, block_table, kv_lens, *, cu_seqlens=Non
     given = workspace
     if workspace is None:
         # from the launch stream's pool: its memory is reused only behind this call
-        need = lib().gqa_attn_paged_attention_workspace_size(H_q, H_kv, d, max_tokens)
-        workspace = _like(torch, "workspace", q, None, torch.uint8, (need,), stream)
+        workspace = _empty(torch, q, _paged_workspace(H_q, H_kv, d, max_tokens), torch.uint8,
+                           stream)
     elif workspace.get_device() != dev or not workspace.is_contiguous():
         raise ValueError(f"workspace must be contiguous and on cuda:{dev}")
     rc = _on_device(torch, dev, lambda: lib().gqa_attn_paged_attention(
@@ -1198,8 +1219,10 @@ def verify_drafts(target_probs, draft_tokens, u_accept, u_sample, cu_seqlens=Non
     if draft_probs is not None and (draft_probs.shape[0] != total
                                     or draft_probs.get_device() != dev):
         raise ValueError(f"draft_probs must have {total} rows and be on cuda:{dev}")
-    accepted = _like(torch, "accepted", target_probs, accepted, torch.int32, (B,), stream)
-    next_tokens = _like(torch, "next_tokens", target_probs, next_tokens, torch.int32, (B,), stream)
+    accepted = (_empty(torch, target_probs, B, torch.int32, stream) if accepted is None
+                else _counts(torch, "accepted", target_probs, accepted, B))
+    next_tokens = (_empty(torch, target_probs, B, torch.int32, stream) if next_tokens is None
+                   else _counts(torch, "next_tokens", target_probs, next_tokens, B))
     rc = _on_device(torch, dev, lambda: lib().gqa_attn_verify_drafts(
         target_probs.data_ptr(), _ptr(draft_probs), toks, ua, us, cu, accepted.data_ptr(),
         next_tokens.data_ptr(), B, total, V, target_probs.stride(0),

@@ -129,6 +129,7 @@ struct Params {
     const uint16_t* v_pages;      // V pages, read again only for values that are not finite
     int64_t v_page;               // elements from one V page to the next
     int table_width, page_size, num_pages;
+    int loaders;      // warps that copy pages: 1, or 2 (the scheduling warp too)
     int single;       // no row has more than one block of tokens
     int alt;          // nor more than one group of them
     int q_tok;        // tokens of a Q box: tok, or fewer where no row has as many
@@ -311,10 +312,16 @@ constexpr int kItemReaders = 3 + 8;  // TMA, MMA and repair warps, 8 softmax war
 
 // ---- the scheduling warp
 
+// then(w, lane): what the scheduling warp does with an item once the others have it.
+struct Nothing {
+    __device__ bool operator()(const Item&, int) { return true; }
+};
+template <typename Then = Nothing>
 struct Publisher {
     uint8_t* items;
     uint64_t* bars;
     unsigned* status;
+    Then then{};
     int count = 0;
     __device__ bool put(const Item& w, int lane) {
         const int s = count % kItemSlots;
@@ -329,7 +336,7 @@ struct Publisher {
         }
         __syncwarp();
         ++count;
-        return true;
+        return then(w, lane);
     }
 };
 
@@ -341,7 +348,7 @@ struct Publisher {
 // heads run together even where their K and V are larger than L2: one group of
 // heads after another, each within L2, ends on heavy items several times (one
 // sequence of 64K tokens, 16/8 heads: 11.9 ms in groups, 10.8 this way).
-__device__ __forceinline__ void schedule_prompts(const Params& p, int2* seqs, Publisher& pub,
+__device__ __forceinline__ void schedule_prompts(const Params& p, int2* seqs, Publisher<>& pub,
                                                  int lane) {
     const int block = 2 * p.tok;
     bool bad = false;
@@ -510,7 +517,7 @@ constexpr int kItemCost = 2;
 // of the block (tokens x G), z the KV head, w the number of parts (0: nothing to
 // merge); the other parts are those of the same member of the next teams.
 template <int kMode>
-__device__ __forceinline__ void schedule_tree(const Params& p, Publisher& pub, int lane) {
+__device__ __forceinline__ void schedule_tree(const Params& p, Publisher<>& pub, int lane) {
     bool bad = false;
     const int team = blockIdx.x / p.team, member = blockIdx.x % p.team;
     struct Row {
@@ -630,22 +637,22 @@ __device__ __forceinline__ void schedule_tree(const Params& p, Publisher& pub, i
 // paged_attention. A unit is a block of tokens of a row against one KV head: tiles
 // 0 .. N - 1 of 128 keys, N from the keys that its last token sees. The units lie in
 // one line, rows one behind the other, their KV heads, their blocks; a unit is as long
-// as its keys, twice where it has two groups of rows (which take twice as long), and
-// kPagedItemCost. The line is cut into equal shares, one to a
+// as its keys and kPagedItemCost of them. (A tile of one group of rows takes as long as one
+// of two beside chunks: 1.8 us, for its loads, against 2.0.) The line is cut into equal shares, one to a
 // CTA, so that a step with chunks, drafts and single tokens at once is balanced
 // whatever its lengths. Where a cut falls inside a unit it moves to the nearest
 // boundary of tiles. The blocks' lengths in the line grow evenly (a causal limit) up
 // to the last, so sums over them have a closed form and nothing is stored.
 // When every row has one block only and the units can be cut into equal parts, one
 // part to a CTA at most, that is done instead (see schedule_tree).
-constexpr int kPagedItemCost = kItemCost * BN;
-constexpr int kPagedShare = 6 * BN;  // least length of a share: two tiles of any unit it crosses
+constexpr int kPagedItemCost = 4 * BN;
+constexpr int kPagedShare = 3 * BN;  // least length of a share: two tiles of any unit it crosses
 
 struct PagedRow {
     int q0, T, n, blocks;
     int64_t line;  // length of its blocks against one KV head
 };
-__device__ __forceinline__ int64_t paged_limit(const Params& p, const PagedRow& r, int i) {
+__device__ __forceinline__ int paged_limit(const Params& p, const PagedRow& r, int i) {
     if (!p.causal || i + 1 >= r.blocks) return r.n;
     return max(0, r.n - r.T + (i + 1) * 2 * p.tok);
 }
@@ -654,17 +661,18 @@ __device__ __forceinline__ bool paged_alt(const Params& p, const PagedRow& r, in
     return p.alt || r.T - i * 2 * p.tok <= p.tok;
 }
 // Length of the first k blocks of a row.
-__device__ __forceinline__ int64_t paged_line(const Params& p, const PagedRow& r, int k) {
-    int64_t sum = int64_t(k) * kPagedItemCost;
+template <typename I>
+__device__ __forceinline__ I paged_line(const Params& p, const PagedRow& r, int k) {
+    I sum = I(k) * kPagedItemCost;
+    if (!p.causal) return sum + I(k) * r.n;
     if (k == r.blocks && k > 0) {
         --k;
-        sum += paged_alt(p, r, k) ? int64_t(r.n) : 2 * int64_t(r.n);
+        sum += r.n;
     }
-    if (!p.causal) return sum + 2 * int64_t(k) * r.n;
-    const int64_t block = 2 * p.tok, off = r.n - r.T;
+    const int block = 2 * p.tok, off = r.n - r.T;
     // the blocks before `none` see no key
-    const int64_t none = off < 0 ? min(-off / block, int64_t(k)) : 0;
-    return sum + 2 * (k - none) * off + block * (int64_t(k) * (k + 1) - none * (none + 1));
+    const int none = off < 0 ? min(-off / block, k) : 0;
+    return sum + I(k - none) * off + p.tok * (I(k) * (k + 1) - I(none) * (none + 1));
 }
 __device__ __forceinline__ PagedRow paged_row(const Params& p, int b, bool& bad) {
     PagedRow r{0, 0, 0, 0, 0};
@@ -678,34 +686,27 @@ __device__ __forceinline__ PagedRow paged_row(const Params& p, int b, bool& bad)
     r.n = clampi(keys, 0, p.S_max);
     bad = bad || r.n != keys;
     r.blocks = cdiv(r.T, 2 * p.tok);
-    r.line = paged_line(p, r, r.blocks);
+    r.line = paged_line<int64_t>(p, r, r.blocks);
     return r;
 }
 
-__device__ __forceinline__ int64_t warp_sum64(int64_t x) {
-    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-    return x;
-}
-
-__device__ __forceinline__ void schedule_paged(const Params& p, Publisher& pub, int lane) {
-    bool bad = false;
+// I: an integer type that holds every position of the line (64-bit divisions cost a
+// microsecond before a CTA's first item).
+template <typename I, typename Pub>
+__device__ __forceinline__ void schedule_line(const Params& p, const PagedRow& row_0, I total,
+                                              Pub& pub, int lane) {
+    bool bad = false;  // (reported by the caller)
     const int ctas = gridDim.x, cta = blockIdx.x;
-    if (!p.whole && lane == 0) p.part_info[cta] = make_int4(0, 0, 0, 0);
-    const PagedRow row_0 = paged_row(p, lane, bad);  // the first 32 rows stay in registers
     auto row_of = [&](int b0) { return b0 == 0 ? row_0 : paged_row(p, b0 + lane, bad); };
-    int64_t total = 0;
-    int tiles = 0, units = 0;
-    for (int b0 = 0; b0 < p.B; b0 += 32) {
-        const PagedRow r = row_of(b0);
-        total += r.line * p.H_kv;
-        units += r.blocks * p.H_kv;
-        if (p.single) tiles += r.blocks * cdiv(r.n, BN) * p.H_kv;
-    }
-    total = warp_sum64(total);
-    if (bad && cta == 0) atomicOr(p.status, kStatusBadSeqlen);
     // Units in equal parts, at most one to a CTA?
     int even = 0;
-    if (p.single && !p.whole) {
+    if (p.single && !p.whole && sizeof(I) == 4) {
+        int tiles = 0, units = 0;
+        for (int b0 = 0; b0 < p.B; b0 += 32) {
+            const PagedRow r = row_of(b0);
+            units += r.blocks * p.H_kv;
+            tiles += r.blocks * cdiv(r.n, BN) * p.H_kv;
+        }
         tiles = __reduce_add_sync(0xffffffffu, tiles);
         units = __reduce_add_sync(0xffffffffu, units);
         if (units <= ctas) {
@@ -718,24 +719,22 @@ __device__ __forceinline__ void schedule_paged(const Params& p, Publisher& pub, 
             if (__reduce_add_sync(0xffffffffu, parts) <= ctas) even = most;
         }
     }
-    // This CTA's share [x, end) of the line (whole, even: of the numbered units or parts).
-    const int64_t shares = max(int64_t(1), min(int64_t(ctas), total / kPagedShare));
+    // This CTA's share [x0, x1) of the line (whole, even: of the numbered units or parts).
     const bool counted = p.whole || even;
-    const int64_t x0 = counted ? cta : cta < shares ? total * cta / shares : total;
-    const int64_t x1 = p.whole ? INT64_MAX : even ? cta + 1
-                       : cta < shares             ? total * (cta + 1) / shares
-                                                  : total;
-    int64_t x = x0, before = 0;  // length of the rows before b0
+    const I per = max((total + ctas - 1) / ctas, I(kPagedShare));
+    const I x0 = counted ? I(cta) : min(I(cta) * per, total);
+    const I x1 = p.whole ? (I(1) << (8 * sizeof(I) - 2)) : even ? x0 + 1 : min(x0 + per, total);
+    I x = x0, before = 0;  // length of the rows before b0
     for (int b0 = 0; b0 < p.B && x < x1; b0 += 32) {
         const PagedRow mine = row_of(b0);
         const int per_unit = even ? max(1, cdiv(cdiv(mine.n, BN), even)) : 1;  // parts
-        const int64_t len = counted ? int64_t(mine.blocks) * p.H_kv * per_unit : mine.line * p.H_kv;
-        int64_t sum = len;  // inclusive prefix sum over the lanes
+        const I len = counted ? I(mine.blocks) * p.H_kv * per_unit : I(mine.line) * p.H_kv;
+        I sum = len;  // inclusive prefix sum over the lanes
         for (int o = 1; o < 32; o <<= 1) {
-            const int64_t y = __shfl_up_sync(0xffffffffu, sum, o);
+            const I y = __shfl_up_sync(0xffffffffu, sum, o);
             if (lane >= o) sum += y;
         }
-        const int64_t all = __shfl_sync(0xffffffffu, sum, 31);
+        const I all = __shfl_sync(0xffffffffu, sum, 31);
         while (x < x1 && x < before + all) {
             const int src = __ffs(__ballot_sync(0xffffffffu, before + sum > x)) - 1;
             PagedRow r;
@@ -743,31 +742,31 @@ __device__ __forceinline__ void schedule_paged(const Params& p, Publisher& pub, 
             r.T = __shfl_sync(0xffffffffu, mine.T, src);
             r.n = __shfl_sync(0xffffffffu, mine.n, src);
             r.blocks = __shfl_sync(0xffffffffu, mine.blocks, src);
-            r.line = __shfl_sync(0xffffffffu, mine.line, src);
+            const I line = __shfl_sync(0xffffffffu, I(mine.line), src);
             const int cuts = __shfl_sync(0xffffffffu, per_unit, src);
-            const int64_t start = before + __shfl_sync(0xffffffffu, sum - len, src);
-            const int64_t at = x - start;
+            const I start = before + __shfl_sync(0xffffffffu, sum - len, src);
+            const I at = x - start;
             Item w{};
             w.b = b0 + src;
             int block, parts = 1;
-            int64_t s = 0;  // (line) start of the unit
+            I s = 0;  // (line) start of the unit
             if (counted) {
                 const int unit = int(at / cuts);
                 w.kvh = unit / r.blocks;
                 block = unit % r.blocks;
             } else {
-                w.kvh = int(at / r.line);
-                const int64_t rest = at - w.kvh * r.line;
+                w.kvh = int(at / line);
+                const I rest = at - w.kvh * line;
                 int lo = 0, hi = r.blocks;  // the block with line(lo) <= rest < line(lo + 1)
                 while (hi - lo > 1) {
                     const int mid = (lo + hi) >> 1;
-                    if (paged_line(p, r, mid) <= rest) lo = mid;
+                    if (paged_line<I>(p, r, mid) <= rest) lo = mid;
                     else hi = mid;
                 }
                 block = lo;
-                s = start + w.kvh * r.line + paged_line(p, r, block);
+                s = start + w.kvh * line + paged_line<I>(p, r, block);
             }
-            const int limit = int(paged_limit(p, r, block));
+            const int limit = paged_limit(p, r, block);
             const int tiles_of = cdiv(limit, BN);
             int j1 = tiles_of;
             bool take = true;
@@ -780,15 +779,13 @@ __device__ __forceinline__ void schedule_paged(const Params& p, Publisher& pub, 
                 parts = cuts;
                 ++x;
             } else {
-                const int twice = paged_alt(p, r, block) ? 0 : 1;
-                const int64_t keys_at = s + kPagedItemCost;
-                const int64_t stop = keys_at + (int64_t(limit) << twice);
-                const int64_t half = (BN / 2) << twice;  // of a tile
+                const I keys_at = s + kPagedItemCost, stop = keys_at + limit;
+                constexpr int half = BN / 2;  // of a tile
                 // tiles of the unit before a cut at y
-                auto before_cut = [&](int64_t y) {
+                auto before_cut = [&](I y) {
                     if (y >= stop) return tiles_of;
-                    const int64_t t = (y - keys_at + half) >> (7 + twice);
-                    return int(min(max(t, int64_t(0)), int64_t(tiles_of)));
+                    const I t = (y - keys_at + half) / BN;
+                    return y <= keys_at ? 0 : int(min(t, I(tiles_of)));
                 };
                 w.j0 = before_cut(x0);
                 j1 = before_cut(x1);
@@ -797,13 +794,9 @@ __device__ __forceinline__ void schedule_paged(const Params& p, Publisher& pub, 
                 } else {
                     take = j1 > w.j0;
                     // the shares that hold its first and its last tile: the first c
-                    // whose end, floor(total (c + 1) / shares), is not before the cut
-                    auto share_of = [&](int64_t y) {
-                        return (y * shares + total - 1) / total - 1;
-                    };
-                    const int64_t first = share_of(min(keys_at + half, stop));
-                    const int64_t last =
-                        share_of(min(keys_at + 2 * half * tiles_of - half, stop));
+                    // with (c + 1) per, its end, not before the cut
+                    const I first = (min(keys_at + half, stop) - 1) / per;
+                    const I last = (min(keys_at + I(tiles_of) * BN - half, stop) - 1) / per;
                     parts = int(last - first) + 1;
                 }
                 x = stop;  // the next unit of the line
@@ -832,6 +825,22 @@ __device__ __forceinline__ void schedule_paged(const Params& p, Publisher& pub, 
     pub.put(end, lane);
 }
 
+template <typename Pub>
+__device__ __forceinline__ void schedule_paged(const Params& p, Pub& pub, int lane) {
+    bool bad = false;
+    if (!p.whole && lane == 0) p.part_info[blockIdx.x] = make_int4(0, 0, 0, 0);
+    const PagedRow row_0 = paged_row(p, lane, bad);  // the first 32 rows stay in registers
+    int64_t total = 0;
+    for (int b0 = 0; b0 < p.B; b0 += 32) {
+        const PagedRow r = b0 == 0 ? row_0 : paged_row(p, b0 + lane, bad);
+        total += r.line * p.H_kv;
+    }
+    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+    if (bad && blockIdx.x == 0) atomicOr(p.status, kStatusBadSeqlen);
+    if (total < (1 << 30)) schedule_line(p, row_0, int(total), pub, lane);
+    else schedule_line(p, row_0, total, pub, lane);
+}
+
 // Ring position, counted from the item's first, of its V tile j, of n tiles. The tiles
 // are loaded in the order in which their slots come free: K_0 V_0 K_1 V_1 .. where two
 // groups share them, K_0 K_1 V_0 K_2 V_1 .. where the groups take turns (paged caches).
@@ -850,12 +859,18 @@ __device__ __forceinline__ int k_position(int j, bool alt) {
 // their use. Keys behind the row's last page are not read: what their place in the tile
 // holds gives scores that are masked, and the P V product does not reach them. A page
 // id out of range gives zeros and is reported.
+//
+// A warp issues a box every 52 cycles whatever its size, so small pages want a second
+// warp: `loader` of p.loaders copies every p.loaders-th page of a tile, and a slot's barrier
+// counts both. (A decode step of 32 rows from pages of 16 / 32 keys: 162 / 140 us, with
+// one loader 215 / 162; of 64 keys 140. Copied by the lanes of one warp, 16 bytes each,
+// 334 / 252.)
 template <int D, int kMode>
 __device__ __forceinline__ void load_pages(const Params& p, const Item& w, int n, bool alt,
                                            int lane, const CUtensorMap* tmap_k,
                                            const CUtensorMap* tmap_v, uint64_t policy,
-                                           uint64_t* bars, uint32_t ring, int r, int& issued,
-                                           bool& alive) {
+                                           uint64_t* bars, uint32_t ring, int loader, int r,
+                                           int& issued, bool& alive) {
     using Gm = Geo<D, kMode>;
     const int rows = min(p.page_size, BN);       // keys of a box
     const int per_tile = BN / rows;              // boxes of a tile and 64 columns
@@ -867,7 +882,8 @@ __device__ __forceinline__ void load_pages(const Params& p, const Item& w, int n
         const int i = first + window * 32 + lane;
         return i < pages ? table[i] : 0;
     };
-    const int box = lane % per_tile, half = lane / per_tile;
+    const int per_loader = per_tile / p.loaders;
+    const int box = lane % per_loader * p.loaders + loader, half = lane / per_loader;
     // The current window is that of the last V tile; K tiles run at most two tiles
     // (16 pages) ahead of it.
     int window = 0, ids = fetch(0), next = fetch(1);
@@ -903,7 +919,9 @@ __device__ __forceinline__ void load_pages(const Params& p, const Item& w, int n
             if (ri >= Gm::kRing)
                 alive = mbar_wait_bounded(smem_u32(&bars[bSlotEmpty + s]),
                                           ((ri / Gm::kRing) - 1) & 1, p.status);
-            if (alive) mbar_arrive_expect_tx(full, uint32_t(boxes * rows * 128 * Gm::kBoxes));
+            if (alive)
+                mbar_arrive_expect_tx(full, uint32_t((boxes - loader + p.loaders - 1) / p.loaders *
+                                                     rows * 128 * Gm::kBoxes));
         }
         alive = __all_sync(0xffffffffu, alive);
         if (!alive) break;
@@ -1047,7 +1065,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(bar(bQFull), 1);
         mbar_init(bar(bQEmpty), 1);
         for (int s = 0; s < kRing; ++s) {
-            mbar_init(bar(bSlotFull + s), 1);
+            mbar_init(bar(bSlotFull + s), kPages ? p.loaders : 1);
             mbar_init(bar(bSlotEmpty + s), 1);
         }
         for (int g = 0; g < 2; ++g) {
@@ -1169,7 +1187,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if constexpr (kPages) {
                 alive = __all_sync(0xffffffffu, alive);
                 load_pages<D, kMode>(p, w, n, alt_item(w), lane, &tmap_kc, &tmap_vc, once, bars,
-                                     smem_u32(smem + Gm::kRingOff), r, issued, alive);
+                                     smem_u32(smem + Gm::kRingOff), 0, r, issued, alive);
             }
             if (!withheld) ++q_loads;
             if (!__all_sync(0xffffffffu, alive) || withheld) break;
@@ -1411,12 +1429,29 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       } else if (warp == 2) {
         // --------------------------------------------------------- scheduler
-        Publisher pub{smem + Gm::kItemOff, bars, p.status};
+        if constexpr (kPages && kAlt) {
+            int r = 0, issued = 0;  // ring items before this item, and issued
+            const uint64_t policy = l2_policy_evict_first();
+            auto second_loader = [&](const Item& w, int) {
+                if (p.loaders == 1 || w.n <= 0) return true;
+                bool ok = true;
+                load_pages<D, kMode>(p, w, w.n, true, lane, &tmap_kc, &tmap_vc, policy, bars,
+                                     smem_u32(smem + Gm::kRingOff), 1, r, issued, ok);
+                r += 2 * w.n;
+                return ok;
+            };
+            Publisher<decltype(second_loader)> pub{smem + Gm::kItemOff, bars, p.status,
+                                                   second_loader};
+            schedule_paged(p, pub, lane);
+            if (lane == 0)
+                for (int i = max(0, issued - kRing); i < issued; ++i) ring_wait(i);
+        }
+        Publisher<> pub{smem + Gm::kItemOff, bars, p.status};
         if constexpr (kTree)
             schedule_tree<kMode>(p, pub, lane);
-        else if constexpr (kPages)
+        else if constexpr (kMode == kPaged)
             schedule_paged(p, pub, lane);
-        else
+        else if constexpr (kMode == kPrompts)
             schedule_prompts(p, reinterpret_cast<int2*>(smem + Gm::kSeqOff), pub, lane);
       } else {
         // ------------------------------------------------------------ repair
@@ -1846,8 +1881,9 @@ __global__ void __launch_bounds__(kMergeThreads, 2) merge_kernel(const Params p)
     constexpr int kPartWarps = kMergeThreads / 64;
     const int col_warp = warp & 1, part_warp = warp >> 1;
     for (int task = blockIdx.x; task < n * chunks * (D / 32); task += gridDim.x) {
-        const int nth = task / (chunks * (D / 32)), c = list[nth];
-        const int chunk = task / (D / 32) % chunks, quarter = task % (D / 32);
+        // (quarter 0 of all first: a unit of few parts has no other)
+        const int nth = task % (n * chunks) / chunks, c = list[nth];
+        const int chunk = task % chunks, quarter = task / (n * chunks);
         const int4 info = infos[nth];
         const int r = chunk * 32 + lane, parts = info.w;
         // (these are the same for the whole block)
@@ -2420,6 +2456,9 @@ extern "C" int gqa_attn_paged_attention(
     if (!p.status || sms <= 0) return GQA_ERR_CUDA;
     p.B = B; p.H_q = H_q; p.H_kv = H_kv; p.G = H_q / H_kv; p.total_q = total;
     p.table = block_table; p.table_width = table_width; p.page_size = page_size;
+    // (Beside several items of two groups a second loader costs more than it gives: the
+    // step of chunks and single tokens takes 110 us with it, 87 without.)
+    p.loaders = plan.alt && page_size < 64 ? 2 : 1;
     p.num_pages = num_pages; p.v_pages = v_pages; p.v_page = num_pages > 1 ? v_page_stride : 0;
     const int slots = num_pages > 0 ? table_width * page_size : 0;
     p.S_max = max_keys > 0 && max_keys < slots ? max_keys : slots;
