@@ -94,8 +94,9 @@ constexpr float kRescaleThreshold = 8.f;
 // 5 drafts, contexts of 64 to 9100: 19.0 us against 19.9 as kTreePair, whose
 // second group would be empty).
 // kPaged: items are blocks of 2 * tok tokens of a row, a range of the row's keys,
-// which all lie in pages. A block of up to tok tokens (a single token beside a chunk of
-// a prompt) runs as in kTreeAlt, the others as in kTreePair.
+// which all lie in pages. (Blocks of one group that took turns as in kTreeAlt beside the
+// others doubled the code that runs at a time: a step of chunks and single tokens took 93 us
+// for 77, many short prompts 363 for 310, with four times the stalls for instructions.)
 // kPagedAlt: the same where no row has more than tok tokens: with room for one group of
 // queries only, the ring of K/V tiles is deeper.
 // kPagedFew: and no more than kFewRows rows of the products (tokens x G).
@@ -131,7 +132,6 @@ struct Params {
     int table_width, page_size, num_pages;
     int loaders;      // warps that copy pages: 1, or 2 (the scheduling warp too)
     int single;       // no row has more than one block of tokens
-    int alt;          // nor more than one group of them
     int q_tok;        // tokens of a Q box: tok, or fewer where no row has as many
     float scale_log2;
     int inject_timeout;  // test hook: block 0 withholds its first Q copy
@@ -153,7 +153,7 @@ struct __align__(16) Item {
     int k_row;   // packed index of the row's first own key
     int off;     // own key of token 0 (keys minus queries)
     int n_own;   // own keys
-    int alt;     // kPaged: one group of rows, the tiles in turn
+    int pad;
 };
 static_assert(sizeof(Item) == 64, "four 16-byte copies");
 
@@ -264,6 +264,8 @@ struct Geo {
                                  : kMode == kPagedAlt ? (D == 128 ? 5 : 10)
                                                       : (D == 128 ? 4 : 10);
     static_assert(kRing <= kMaxRing, "barriers");
+    // V_1 may be repaired before K_0 has been seen (see ask): not into K_0's slot
+    static_assert(kQGroups == 2 || kRing > 4, "repair");
     static constexpr uint32_t kQOff = 0;
     static constexpr uint32_t kRingOff = kQGroups * kQBytes;
     static constexpr uint32_t kStageOff = kRingOff + kRing * kTileBytes;  // 8 warps
@@ -637,8 +639,8 @@ __device__ __forceinline__ void schedule_tree(const Params& p, Publisher<>& pub,
 // paged_attention. A unit is a block of tokens of a row against one KV head: tiles
 // 0 .. N - 1 of 128 keys, N from the keys that its last token sees. The units lie in
 // one line, rows one behind the other, their KV heads, their blocks; a unit is as long
-// as its keys and kPagedItemCost of them. (A tile of one group of rows takes as long as one
-// of two beside chunks: 1.8 us, for its loads, against 2.0.) The line is cut into equal shares, one to a
+// as its keys and kPagedItemCost of them. (A tile of one group of rows takes almost as long as
+// one of two.) The line is cut into equal shares, one to a
 // CTA, so that a step with chunks, drafts and single tokens at once is balanced
 // whatever its lengths. Where a cut falls inside a unit it moves to the nearest
 // boundary of tiles. The blocks' lengths in the line grow evenly (a causal limit) up
@@ -655,10 +657,6 @@ struct PagedRow {
 __device__ __forceinline__ int paged_limit(const Params& p, const PagedRow& r, int i) {
     if (!p.causal || i + 1 >= r.blocks) return r.n;
     return max(0, r.n - r.T + (i + 1) * 2 * p.tok);
-}
-// Block i has one group of rows only.
-__device__ __forceinline__ bool paged_alt(const Params& p, const PagedRow& r, int i) {
-    return p.alt || r.T - i * 2 * p.tok <= p.tok;
 }
 // Length of the first k blocks of a row.
 template <typename I>
@@ -725,100 +723,124 @@ __device__ __forceinline__ void schedule_line(const Params& p, const PagedRow& r
     const I x0 = counted ? I(cta) : min(I(cta) * per, total);
     const I x1 = p.whole ? (I(1) << (8 * sizeof(I) - 2)) : even ? x0 + 1 : min(x0 + per, total);
     I x = x0, before = 0;  // length of the rows before b0
-    for (int b0 = 0; b0 < p.B && x < x1; b0 += 32) {
-        const PagedRow mine = row_of(b0);
-        const int per_unit = even ? max(1, cdiv(cdiv(mine.n, BN), even)) : 1;  // parts
-        const I len = counted ? I(mine.blocks) * p.H_kv * per_unit : I(mine.line) * p.H_kv;
-        I sum = len;  // inclusive prefix sum over the lanes
+    int b0 = 0, cuts_of = 1;
+    PagedRow mine{};
+    I len = 0, sum = 0, all = 0;  // of the rows from b0 on: a lane's, up to it, all of them
+    auto look = [&] {
+        mine = row_of(b0);
+        cuts_of = even ? max(1, cdiv(cdiv(mine.n, BN), even)) : 1;
+        len = counted ? I(mine.blocks) * p.H_kv * cuts_of : I(mine.line) * p.H_kv;
+        sum = len;
         for (int o = 1; o < 32; o <<= 1) {
             const I y = __shfl_up_sync(0xffffffffu, sum, o);
             if (lane >= o) sum += y;
         }
-        const I all = __shfl_sync(0xffffffffu, sum, 31);
-        while (x < x1 && x < before + all) {
-            const int src = __ffs(__ballot_sync(0xffffffffu, before + sum > x)) - 1;
-            PagedRow r;
-            r.q0 = __shfl_sync(0xffffffffu, mine.q0, src);
-            r.T = __shfl_sync(0xffffffffu, mine.T, src);
-            r.n = __shfl_sync(0xffffffffu, mine.n, src);
-            r.blocks = __shfl_sync(0xffffffffu, mine.blocks, src);
+        all = __shfl_sync(0xffffffffu, sum, 31);
+    };
+    look();
+    while (x < x1) {
+        while (x >= before + all) {
+            before += all;
+            b0 += 32;
+            if (b0 >= p.B) break;
+            look();
+        }
+        if (b0 >= p.B) break;
+        // the row that holds x, and its unit
+        const int src = __ffs(__ballot_sync(0xffffffffu, before + sum > x)) - 1;
+        PagedRow r;
+        r.q0 = __shfl_sync(0xffffffffu, mine.q0, src);
+        r.T = __shfl_sync(0xffffffffu, mine.T, src);
+        r.n = __shfl_sync(0xffffffffu, mine.n, src);
+        r.blocks = __shfl_sync(0xffffffffu, mine.blocks, src);
+        const int cuts = __shfl_sync(0xffffffffu, cuts_of, src);
+        const I stop_row = before + __shfl_sync(0xffffffffu, sum, src);
+        const I start = stop_row - __shfl_sync(0xffffffffu, len, src);
+        int kvh, block;
+        I s = 0;  // (line) start of the unit
+        if (counted) {
+            const int unit = int((x - start) / cuts);
+            kvh = unit / r.blocks;
+            block = unit % r.blocks;
+        } else {
             const I line = __shfl_sync(0xffffffffu, I(mine.line), src);
-            const int cuts = __shfl_sync(0xffffffffu, per_unit, src);
-            const I start = before + __shfl_sync(0xffffffffu, sum - len, src);
-            const I at = x - start;
+            kvh = int((x - start) / line);
+            const I rest = x - start - kvh * line;
+            int lo = 0, hi = r.blocks;  // the block with line(lo) <= rest < line(lo + 1)
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) >> 1;
+                if (paged_line<I>(p, r, mid) <= rest) lo = mid;
+                else hi = mid;
+            }
+            block = lo;
+            s = start + kvh * line + paged_line<I>(p, r, block);
+        }
+        // the row's units from there on (few instructions: every one of this warp's that
+        // is run between two items takes the softmax warps' out of the cache)
+#pragma unroll 1
+        for (;;) {
             Item w{};
             w.b = b0 + src;
-            int block, parts = 1;
-            I s = 0;  // (line) start of the unit
-            if (counted) {
-                const int unit = int(at / cuts);
-                w.kvh = unit / r.blocks;
-                block = unit % r.blocks;
-            } else {
-                w.kvh = int(at / line);
-                const I rest = at - w.kvh * line;
-                int lo = 0, hi = r.blocks;  // the block with line(lo) <= rest < line(lo + 1)
-                while (hi - lo > 1) {
-                    const int mid = (lo + hi) >> 1;
-                    if (paged_line<I>(p, r, mid) <= rest) lo = mid;
-                    else hi = mid;
-                }
-                block = lo;
-                s = start + w.kvh * line + paged_line<I>(p, r, block);
-            }
-            const int limit = paged_limit(p, r, block);
-            const int tiles_of = cdiv(limit, BN);
-            int j1 = tiles_of;
-            bool take = true;
-            if (p.whole) {
-                x += ctas;
-            } else if (even) {
-                const int i = int(at % cuts);
-                w.j0 = int(int64_t(tiles_of) * i / cuts);
-                j1 = int(int64_t(tiles_of) * (i + 1) / cuts);
-                parts = cuts;
-                ++x;
-            } else {
-                const I keys_at = s + kPagedItemCost, stop = keys_at + limit;
-                constexpr int half = BN / 2;  // of a tile
-                // tiles of the unit before a cut at y
-                auto before_cut = [&](I y) {
-                    if (y >= stop) return tiles_of;
-                    const I t = (y - keys_at + half) / BN;
-                    return y <= keys_at ? 0 : int(min(t, I(tiles_of)));
-                };
-                w.j0 = before_cut(x0);
-                j1 = before_cut(x1);
-                if (tiles_of == 0) {
-                    take = s >= x0;  // the CTA in whose share it begins
-                } else {
-                    take = j1 > w.j0;
-                    // the shares that hold its first and its last tile: the first c
-                    // with (c + 1) per, its end, not before the cut
-                    const I first = (min(keys_at + half, stop) - 1) / per;
-                    const I last = (min(keys_at + I(tiles_of) * BN - half, stop) - 1) / per;
-                    parts = int(last - first) + 1;
-                }
-                x = stop;  // the next unit of the line
-            }
+            w.kvh = kvh;
             w.q_row = r.q0;
             w.T = r.T;
             w.n_own = r.n;
             w.off = r.n - r.T;
             w.tok0 = block * 2 * p.tok;
-            w.alt = paged_alt(p, r, block);
-            w.n = j1 - w.j0;
-            w.n0 = clampi(cdiv(group_last<kPaged>(p, w, 0), BN) - w.j0, 0, w.n);
-            w.n1 = w.tok0 + p.tok < w.T ? w.n : 0;
-            if (!take || (w.n == 0 && tiles_of > 0)) continue;
-            // slot 2c + 1 holds the first part of a unit, 2c another one
-            w.dst = parts == 1 ? -1 : 2 * cta + (w.j0 == 0);
-            if (parts > 1 && w.j0 == 0 && lane == 0)
-                p.part_info[cta] =
-                    make_int4(w.q_row + w.tok0, min(w.T - w.tok0, 2 * p.tok) * p.G, w.kvh, parts);
-            if (!pub.put(w, lane)) return;
+            const int limit = paged_limit(p, r, block), tiles_of = cdiv(limit, BN);
+            int j1 = tiles_of, parts = 1;
+            bool take = true;
+            if (even) {
+                const int i = int(x - start) - (kvh * r.blocks + block) * cuts;
+                w.j0 = int(int64_t(tiles_of) * i / cuts);
+                j1 = int(int64_t(tiles_of) * (i + 1) / cuts);
+                parts = cuts;
+            } else if (!p.whole) {
+                const I keys_at = s + kPagedItemCost;
+                s = keys_at + limit;  // its end
+                constexpr int half = BN / 2;  // of a tile
+                // tiles of the unit before a cut at y
+                auto before_cut = [&](I y) {
+                    if (y >= s) return tiles_of;
+                    return y <= keys_at ? 0 : min(int((y - keys_at + half) / BN), tiles_of);
+                };
+                w.j0 = before_cut(x0);
+                j1 = before_cut(x1);
+                if (tiles_of == 0) {
+                    take = keys_at - kPagedItemCost >= x0;  // the CTA in whose share it begins
+                } else {
+                    take = j1 > w.j0;
+                    // cut: the shares that hold its first and its last tile are the first
+                    // c with (c + 1) per, its end, not before the cut
+                    if (w.j0 > 0 || j1 < tiles_of) {
+                        const I first = (min(keys_at + half, s) - 1) / per;
+                        const I last = (min(keys_at + I(tiles_of) * BN - half, s) - 1) / per;
+                        parts = int(last - first) + 1;
+                    }
+                }
+            }
+            if (take) {
+                w.n = j1 - w.j0;
+                w.n0 = clampi(cdiv(group_last<kPaged>(p, w, 0), BN) - w.j0, 0, w.n);
+                w.n1 = w.tok0 + p.tok < w.T ? w.n : 0;
+                // slot 2c + 1 holds the first part of a unit, 2c another one
+                w.dst = parts == 1 ? -1 : 2 * cta + (w.j0 == 0);
+                if (parts > 1 && w.j0 == 0 && lane == 0)
+                    p.part_info[cta] = make_int4(w.q_row + w.tok0,
+                                                 min(w.T - w.tok0, 2 * p.tok) * p.G, w.kvh, parts);
+                if (!pub.put(w, lane)) return;
+            }
+            if (counted) {
+                x += even ? 1 : ctas;
+                break;
+            }
+            x = s;
+            if (x >= x1 || x >= stop_row) break;
+            if (++block == r.blocks) {
+                block = 0;
+                ++kvh;
+            }
         }
-        before += all;
     }
     Item end{};
     end.n = -1;
@@ -845,12 +867,8 @@ __device__ __forceinline__ void schedule_paged(const Params& p, Pub& pub, int la
 // are loaded in the order in which their slots come free: K_0 V_0 K_1 V_1 .. where two
 // groups share them, K_0 K_1 V_0 K_2 V_1 .. where the groups take turns (paged caches).
 template <int kMode>
-__device__ __forceinline__ int v_position(int j, int n, bool alt) {
-    return paged_mode(kMode) && alt ? min(2 * j + 2, 2 * n - 1) : 2 * j + 1;
-}
-template <int kMode>
-__device__ __forceinline__ int k_position(int j, bool alt) {
-    return paged_mode(kMode) && alt ? max(2 * j - 1, 0) : 2 * j;
+__device__ __forceinline__ int v_position(int j, int n) {
+    return paged_mode(kMode) && alt_mode(kMode) ? min(2 * j + 2, 2 * n - 1) : 2 * j + 1;
 }
 
 // Copies the K and V tiles of an item from their pages into the ring: a box of a page
@@ -866,8 +884,8 @@ __device__ __forceinline__ int k_position(int j, bool alt) {
 // one loader 215 / 162; of 64 keys 140. Copied by the lanes of one warp, 16 bytes each,
 // 334 / 252.)
 template <int D, int kMode>
-__device__ __forceinline__ void load_pages(const Params& p, const Item& w, int n, bool alt,
-                                           int lane, const CUtensorMap* tmap_k,
+__device__ __forceinline__ void load_pages(const Params& p, const Item& w, int n, int lane,
+                                           const CUtensorMap* tmap_k,
                                            const CUtensorMap* tmap_v, uint64_t policy,
                                            uint64_t* bars, uint32_t ring, int loader, int r,
                                            int& issued, bool& alive) {
@@ -890,7 +908,7 @@ __device__ __forceinline__ void load_pages(const Params& p, const Item& w, int n
 #pragma unroll 1
     for (int i = 0; i < 2 * n && alive; ++i) {
         int kv, j;
-        if (alt) {
+        if (alt_mode(kMode)) {
             j = i & 1 ? (i + 1) >> 1 : max(i - 2, 0) >> 1;
             kv = i & 1 ? j >= n : i > 0;
             j = min(j, n - 1);
@@ -1043,11 +1061,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr uint32_t kTileBytes = Gm::kTileBytes;
     constexpr int kRing = Gm::kRing;
     constexpr bool kTree = tree_mode(kMode), kPages = paged_mode(kMode), kAlt = alt_mode(kMode);
-    // items of one group, whose tiles the two softmax groups take in turn
-    auto alt_item = [](const Item& w) {
-        if constexpr (kMode == kPaged) return uniform(w.alt) != 0;
-        else return kAlt;
-    };
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                ~uintptr_t(1023));
@@ -1186,7 +1199,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if constexpr (kPages) {
                 alive = __all_sync(0xffffffffu, alive);
-                load_pages<D, kMode>(p, w, n, alt_item(w), lane, &tmap_kc, &tmap_vc, once, bars,
+                load_pages<D, kMode>(p, w, n, lane, &tmap_kc, &tmap_vc, once, bars,
                                      smem_u32(smem + Gm::kRingOff), 0, r, issued, alive);
             }
             if (!withheld) ++q_loads;
@@ -1208,8 +1221,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint64_t qdesc0 = tc::sdesc_sw128(smem_u32(smem + Gm::kQOff), 16, 1024);
         const uint64_t qdesc1 = tc::sdesc_sw128(smem_u32(smem + Gm::kQOff + kTileBytes), 16, 1024);
         // S_g = Q K^T with K in ring item ri (kTreeAlt: both groups hold the same rows)
-        auto issue_s = [&](int g, int ri, bool one_group = alt_mode(kMode)) {
-            const uint64_t qdesc = !one_group && g ? qdesc1 : qdesc0;
+        auto issue_s = [&](int g, int ri) {
+            const uint64_t qdesc = !kAlt && g ? qdesc1 : qdesc0;
             const uint64_t kdesc = tc::sdesc_sw128(slot_addr(ri), 16, 1024);
             const uint32_t qlo = uint32_t(qdesc), qhi = uint32_t(qdesc >> 32);
             const uint32_t klo = uint32_t(kdesc), khi = uint32_t(kdesc >> 32);
@@ -1245,19 +1258,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int n = uniform(w.n);
             if (n < 0) break;
             if (n == 0) continue;
-            const bool alt = alt_item(w);
-            const int n0 = alt ? (n + 1) >> 1 : uniform(w.n0), n1 = alt ? n >> 1 : uniform(w.n1);
+            const int n0 = kAlt ? (n + 1) >> 1 : uniform(w.n0), n1 = kAlt ? n >> 1 : uniform(w.n1);
             // tiles before `plain` need no repair and count with all their keys;
             // the last tile of a group (kPrompts), the context's last and the
             // drafted tokens' tile (decode_tree) may count with fewer
             const int plain = uniform(plain_tiles<kMode>(p, w, 0));
             const int j_own = uniform(w.c_t - w.j0);
             const int k0 = uniform(
-                kTree ? w.n_own : tile_keys<kMode>(p, w, w.j0 + (alt ? n : n0) - 1, 0));
+                kTree ? w.n_own : tile_keys<kMode>(p, w, w.j0 + (kAlt ? n : n0) - 1, 0));
             const int k1 = uniform(kTree ? w.ctx - (w.c_t - 1) * BN
                                          : tile_keys<kMode>(p, w, w.j0 + n1 - 1, 1));
             auto keys_of = [&](int j, int g) {
-                if (kPages && alt) return j + 1 < n ? BN : k0;
+                if (kPages && kAlt) return j + 1 < n ? BN : k0;
                 if (!kTree) return j + 1 < (g ? n1 : n0) ? BN : (g ? k1 : k0);
                 return j < plain ? BN : (j < j_own ? k1 : k0);
             };
@@ -1274,28 +1286,26 @@ __global__ void __launch_bounds__(kThreads, 1)
             bool alive = true;
             // Tiles that both groups run whole and that are not a group's last:
             // no conditions between the issues, which are on the critical path.
-            const int fast = alt ? 0 : min(plain, min(n0, n1) - 1);
+            const int fast = kAlt ? 0 : min(plain, min(n0, n1) - 1);
             if (lane == 0) {
                 if (fast <= 0) {
                     ask(0);
-                    // (a ring of four: K_0 has the slot of V_1 before it)
-                    if (!kPages || !alt) ask(1);
+                    ask(1);
                 }
                 alive = mbar_wait_bounded(bar(bQFull), qi & 1, p.status) && ring_wait(r);
-                if (kPages && alt && alive) ask(1);
             }
             if (lane == 0 && alive) {
               tc::fence_after_sync();
-              if (kPages && alt) {
+              if constexpr (kPages && kAlt) {
                 // Each product waits for its own operands only: K and V come from HBM at
                 // the pace of the whole GPU, and a slot given back early is loaded early.
-                issue_s(0, r, true);
+                issue_s(0, r);
                 tc::commit(bar(bSlotEmpty + r % kRing));
                 if (n > 1) {
                     alive = ring_wait(r + 1);
                     if (alive) {
                         tc::fence_after_sync();
-                        issue_s(1, r + 1, true);
+                        issue_s(1, r + 1);
                         tc::commit(bar(bSlotEmpty + (r + 1) % kRing));
                     }
                 }
@@ -1303,8 +1313,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
                 for (int j = 0; j < n && alive; ++j) {
                     const int g = j & 1;
-                    const int rv = r + v_position<kMode>(j, n, true);
-                    const int rk = r + k_position<kMode>(j + 2, true);
+                    const int rv = r + v_position<kMode>(j, n);
+                    const int rk = rv + 1;
                     alive = ring_wait(rv) && repaired(j);
                     if (!alive) break;
                     ask(j + 2);
@@ -1318,7 +1328,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         alive = ring_wait(rk);
                         if (!alive) break;
                         tc::fence_after_sync();
-                        issue_s(g, rk, true);  // K_{j+2}
+                        issue_s(g, rk);  // K_{j+2}
                         tc::commit(bar(bSlotEmpty + rk % kRing));
                         if (j + 3 == n) tc::commit(bar(bQEmpty));
                     } else {
@@ -1435,7 +1445,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             auto second_loader = [&](const Item& w, int) {
                 if (p.loaders == 1 || w.n <= 0) return true;
                 bool ok = true;
-                load_pages<D, kMode>(p, w, w.n, true, lane, &tmap_kc, &tmap_vc, policy, bars,
+                load_pages<D, kMode>(p, w, w.n, lane, &tmap_kc, &tmap_vc, policy, bars,
                                      smem_u32(smem + Gm::kRingOff), 1, r, issued, ok);
                 r += 2 * w.n;
                 return ok;
@@ -1467,7 +1477,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (w.n < 0) break;
             for (int j = plain_tiles<kMode>(p, w, 0); j < w.n && alive; ++j) {
                 const Repair fix = repair_of<kMode>(p, w, w.j0 + j);
-                const int ri = r + v_position<kMode>(j, w.n, alt_item(w));
+                const int ri = r + v_position<kMode>(j, w.n);
                 alive = __all_sync(0xffffffffu,
                                    mbar_wait_bounded(bar(bFixAsk + (f & 1)), (f >> 1) & 1,
                                                      p.status)) &&
@@ -1547,12 +1557,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool alive = true;
         int tt = 0;              // tiles this group finished: its S phases
         int done0 = 0, done1 = 0;  // O_0, O_1 phases (kTreeAlt reads both, else its own)
-        auto done_phases = [&](const Item& w) {  // kPaged: an item's, for both
-            if constexpr (kMode == kPaged) {
-                done0 += alt_item(w) ? w.n > 0 : w.n0 > 0;
-                done1 += alt_item(w) ? w.n > 1 : w.n1 > 0;
-            }
-        };
         int xk = 0;
         auto wait_all = [&](int b, int phase) {
             return bool(__all_sync(0xffffffffu, mbar_wait_bounded(bar(b), phase & 1, p.status)));
@@ -1569,18 +1573,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                 smem_u32(smem + Gm::kItemOff + (it % kItemSlots) * sizeof(Item));
             const Item w = read_item(item_addr);
             if (uniform(w.n) < 0) break;
-            const bool alt = alt_item(w);
-            const int tok0 = alt ? w.tok0 : w.tok0 + g * p.tok;
+            const int tok0 = kAlt ? w.tok0 : w.tok0 + g * p.tok;
             const int count = uniform(min(p.tok, w.T - tok0));  // tokens of this group
             if (count <= 0) {
-                done_phases(w);
                 done_with_item();
                 continue;
             }
-            const int ng = uniform(alt ? (w.n + 1 - g) >> 1 : (g ? w.n1 : w.n0));
+            const int ng = uniform(kAlt ? (w.n + 1 - g) >> 1 : (g ? w.n1 : w.n0));
             // some row of this warp is valid
             const bool act = __any_sync(0xffffffffu, row_tok < count);
-            if (kPages && !alt && ng == 0 && w.dst >= 0) {  // ... in this part of the keys
+            if (kPages && !kAlt && ng == 0 && w.dst >= 0) {  // ... in this part of the keys
                 if (row_tok < count) {
                     const int prow = (g * p.tok + row_tok) * p.G + row_head;
                     float4* dst = reinterpret_cast<float4*>(p.part_o) +
@@ -1590,12 +1592,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                         dst[size_t(i) * p.part_rows] = make_float4(0.f, 0.f, 0.f, 0.f);
                     p.part_lse[size_t(w.dst) * p.part_rows + prow] = -INFINITY;
                 }
-                done_phases(w);
                 done_with_item();
                 continue;
             }
-            if (!kTree && (alt ? w.n : ng) == 0) {  // queries that see no key
-                if (row_tok < count && (!alt || g == 0)) {
+            if (!kTree && (kAlt ? w.n : ng) == 0) {  // queries that see no key
+                if (row_tok < count && (!kAlt || g == 0)) {
                     const size_t orow = (size_t(w.q_row) + tok0 + row_tok) * p.H_q +
                                         w.kvh * p.G + row_head;
                     uint4* dst = reinterpret_cast<uint4*>(p.o + orow * D);
@@ -1603,13 +1604,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int i = 0; i < D / 8; ++i) dst[i] = make_uint4(0, 0, 0, 0);
                     if (p.lse) p.lse[orow] = -INFINITY;
                 }
-                done_phases(w);
                 done_with_item();
                 continue;
             }
             // Keys of tile i that this row sees, for the tiles from `plain` on:
             // c < last - 128 i. The drafted tokens' tile goes by the bits.
-            const int plain = uniform(plain_tiles<kMode>(p, w, kTree || alt ? 0 : g));
+            const int plain = uniform(plain_tiles<kMode>(p, w, kTree || kAlt ? 0 : g));
             const int last = (kTree ? w.ctx : token_limit(p, w, tok0 + row_tok)) - w.j0 * BN;
             const int own_tile = kTree ? uniform(w.c_t - w.j0) : 0;
             uint32_t bits[4] = {0, 0, 0, 0};  // drafted tokens this row sees
@@ -1631,7 +1631,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t pk[2][32];  // the last tile's P, not in lb yet
 #pragma unroll 1
             for (int i = 0; i < ng && alive; ++i) {
-                if (!alt && act && i > 0) st.lb += rounded_sum(pk);
+                if (!kAlt && act && i > 0) st.lb += rounded_sum(pk);
                 alive = wait_all(bSFull + g, tt + i);
                 if (!alive) break;
                 if (act) {
@@ -1645,7 +1645,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int e = 0; e < 32; ++e) sv[c * 32 + e] = __uint_as_float(x[e]);
                     }
                     tc::tmem_wait_ld();
-                    const int j = alt ? 2 * i + g : i;
+                    const int j = kAlt ? 2 * i + g : i;
                     if (j >= plain) {
                         if (kTree && j >= own_tile) {
 #pragma unroll
@@ -1685,18 +1685,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(bPFull + g));
-                if (alt && act) st.lb += rounded_sum(pk);
+                if (kAlt && act) st.lb += rounded_sum(pk);
             }
             if (!alive) break;
-            if (!alt && act && ng > 0) st.lb += rounded_sum(pk);
+            if (!kAlt && act && ng > 0) st.lb += rounded_sum(pk);
             tt += ng;
 
             // ---- epilogue. Every read of O completes before this warp's next
             // P arrive, which is what lets the next item overwrite O.
             float f0 = 1.f, f1 = 0.f;  // weights of O_0 and O_1 (kTreeAlt)
             const Item e = read_item(item_addr);
-            const bool two = alt && uniform(e.n) > 1;
-            if (alt) {
+            const bool two = kAlt && uniform(e.n) > 1;
+            if constexpr (kAlt) {
                 xch[g * BM + row] = make_float4(st.m, st.l, st.lb, 0.f);
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(bXch));
@@ -1711,7 +1711,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 st.lb = f0 * a.z + f1 * b.z;
             }
             // (what does not need O comes before the wait for it)
-            const int t = (alt ? e.tok0 : e.tok0 + g * p.tok) + row_tok;
+            const int t = (kAlt ? e.tok0 : e.tok0 + g * p.tok) + row_tok;
             const bool valid = row_tok < p.tok && t < e.T;
             const bool own = kPages || e.j0 + e.n > e.c_t;  // the item has the row's own tokens
             const size_t orow = (size_t(e.q_row) + t) * p.H_q + e.kvh * p.G + row_head;
@@ -1722,31 +1722,31 @@ __global__ void __launch_bounds__(kThreads, 1)
                 valid && direct ? reinterpret_cast<uint8_t*>(p.o + orow * D) : nullptr, lane);
             // the sums are 0 only for a row that saw no key (and NaN stays NaN)
             const float inv = st.lb == 0.f ? 0.f : 1.f / st.lb;
-            if (valid && (!alt || g == 0)) {
+            if (valid && (!kAlt || g == 0)) {
                 const float lse = st.l == 0.f ? -INFINITY : (st.m + log2f(st.l)) * kLn2;
                 if (!direct)
                     p.part_lse[size_t(e.dst) * p.part_rows + prow] = lse;
                 else if (p.lse)
                     p.lse[orow] = lse;
             }
-            if (alt) {
+            if constexpr (kAlt) {
                 alive = wait_all(bODone, done0) && (!two || wait_all(bODone + 1, done1));
-                if (kMode != kPaged) done1 += two;
+                done1 += two;
             } else {
-                alive = wait_all(bODone + g, kMode == kPaged && g ? done1 : done0);
+                alive = wait_all(bODone + g, done0);
             }
             if (!alive) break;
-            if (kMode != kPaged) ++done0;
+            ++done0;
             if (act) {
                 tc::fence_after_sync();
                 const bool odd = *odd_values != 0 && own;
-                const int c_begin = alt ? g * (D / 64) : 0;
-                const int c_end = alt ? (g + 1) * (D / 64) : D / 32;
+                const int c_begin = kAlt ? g * (D / 64) : 0;
+                const int c_end = kAlt ? (g + 1) * (D / 64) : D / 32;
 #pragma unroll 1
                 for (int c = c_begin; c < c_end; ++c) {
                     uint32_t x[32];
-                    tc::tmem_ld32(lane_base + (alt ? col_o_of(0) : col_o) + c * 32, x);
-                    if (alt) {
+                    tc::tmem_ld32(lane_base + (kAlt ? col_o_of(0) : col_o) + c * 32, x);
+                    if constexpr (kAlt) {
                         if (two) {
                             uint32_t y[32];
                             tc::tmem_ld32(lane_base + col_o_of(1) + c * 32, y);
@@ -1815,7 +1815,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
             }
-            if (alt) {
+            if constexpr (kAlt) {
                 // both groups have read O_0, O_1 and xch
                 tc::fence_before_sync();
                 __syncwarp();
@@ -1824,7 +1824,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!alive) break;
                 ++xk;
             }
-            done_phases(e);
             done_with_item();
         }
     }
@@ -2466,7 +2465,6 @@ extern "C" int gqa_attn_paged_attention(
     p.causal = causal != 0;
     p.tok = plan.tok; p.team = 1; p.part_rows = plan.part_rows;
     p.single = max_tokens <= 2 * plan.tok;
-    p.alt = plan.alt;
     p.q_tok = plan.alt ? max_tokens : plan.tok;
     p.scale_log2 = scale * kLog2e;
     p.inject_timeout = take_injected_timeout() ? 1 : 0;

@@ -353,7 +353,7 @@ __device__ __forceinline__ void st_dsmem_f64(uint32_t addr, double v) {
     asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(addr), "d"(v) : "memory");
 }
 
-__global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyParams p) {
+__global__ void __launch_bounds__(kVerifyThreads, 2) verify_kernel(const VerifyParams p) {
     static_assert(kVerifyWarps == 16 && kMaxCluster == 16, "inclusive16");
     __shared__ int first_fall;
     __shared__ float2 warp_sum[kVerifyWarps];
