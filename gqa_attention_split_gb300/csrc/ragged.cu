@@ -1248,6 +1248,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tc::mma_ts_lo(dst, src + ks * 8, vlo + uint32_t((ks * 2048) >> 4), vhi,
                                   idesc_pv, 1u);
         };
+        // the same in a loop: few instructions (see kPaged)
+        auto issue_pv_loop = [&](int g, int ri, bool first, int keys) {
+            const uint64_t vdesc = tc::sdesc_sw128(slot_addr(ri), kBoxBytes, 1024);
+            uint32_t vlo = uint32_t(vdesc), src = tmem + col_s_of(g), add = first ? 0u : 1u;
+#pragma unroll 1
+            for (int k = 0; k < keys; k += 16, vlo += 2048 >> 4, src += 8, add = 1u)
+                tc::mma_ts_lo(tmem + col_o_of(g), src, vlo, uint32_t(vdesc >> 32), idesc_pv, add);
+        };
         constexpr std::integral_constant<int, BN> kAllKeys{};
         int r = 0, qi = 0;   // ring items and items with tiles before this item
         int t0 = 0, t1 = 0;  // tiles of group 0 and 1 before this item (their S and P phases)
@@ -1402,16 +1410,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int rv = r + 2 * j + 1;
                     alive = ring_wait(rv) && (j + 1 == n || ring_wait(rv + 1)) && repaired(j);
                     if (alive) ask(j + 2);
-#pragma unroll
-                    for (int g = 0; g < 2; ++g) {
-                        if (!alive) break;
+                    auto tile_of = [&](int g) {
                         const int n_g = g ? n1 : n0;
-                        if (j >= n_g) continue;
+                        if (j >= n_g) return;
                         alive = mbar_wait_bounded(bar(bPFull + g), ((g ? t1 : t0) + j) & 1,
                                                   p.status);
-                        if (!alive) break;
+                        if (!alive) return;
                         tc::fence_after_sync();
-                        issue_pv(g, rv, j == 0, keys_of(j, g));
+                        if constexpr (kPages) issue_pv_loop(g, rv, j == 0, keys_of(j, g));
+                        else issue_pv(g, rv, j == 0, keys_of(j, g));
                         if (g == last_user(j)) tc::commit(bar(bSlotEmpty + rv % kRing));
                         if (j + 1 < n_g) {
                             issue_s(g, rv + 1);
@@ -1422,6 +1429,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                         } else {
                             tc::commit(bar(bODone + g));
                         }
+                    };
+                    if constexpr (kPages) {
+#pragma unroll 1
+                        for (int g = 0; g < 2 && alive; ++g) tile_of(g);
+                    } else {
+                        if (alive) tile_of(0);
+                        if (alive) tile_of(1);
                     }
                 }
               }
@@ -1630,8 +1644,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             RowState st{-INFINITY, 0.f, 0.f};
             uint32_t pk[2][32];  // the last tile's P, not in lb yet
 #pragma unroll 1
-            for (int i = 0; i < ng && alive; ++i) {
+            for (int i = 0;; ++i) {
                 if (!kAlt && act && i > 0) st.lb += rounded_sum(pk);
+                if (i >= ng) break;
                 alive = wait_all(bSFull + g, tt + i);
                 if (!alive) break;
                 if (act) {
@@ -1688,7 +1703,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (kAlt && act) st.lb += rounded_sum(pk);
             }
             if (!alive) break;
-            if (!kAlt && act && ng > 0) st.lb += rounded_sum(pk);
             tt += ng;
 
             // ---- epilogue. Every read of O completes before this warp's next
