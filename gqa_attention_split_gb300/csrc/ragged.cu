@@ -1,13 +1,14 @@
 // Attention over ragged batches on the 5th-generation tensor cores: packed
-// prompts, and drafted token trees on top of the KV cache; and appending
-// packed tokens to the cache.
+// prompts, drafted token trees on top of the KV cache, and new tokens over a
+// paged cache; and appending packed tokens to a cache.
 //
 //   O = softmax(scale * Q K^T over the visible keys) V,   lse = ln sum exp(.)
 //
-// Both calls stream the same two sources of keys per row of the batch: the
+// The calls stream two sources of keys per row of the batch: the
 // context in the cache (decode_tree only; every slot below context_lens[b] is
 // visible), then the row's own packed tokens (prefill_packed: a causal limit
-// or all of them; decode_tree: the bits of a mask, or a line). A key that a
+// or all of them; decode_tree: the bits of a mask, or a line). paged_attention has
+// the second source only, and finds it through the row's block table. A key that a
 // query does not see never reaches its result, whatever K and V hold there.
 //
 // Layout of the work. The G query heads of a KV head are folded into the rows
@@ -94,12 +95,19 @@ constexpr float kRescaleThreshold = 8.f;
 // 5 drafts, contexts of 64 to 9100: 19.0 us against 19.9 as kTreePair, whose
 // second group would be empty).
 // kPaged: items are blocks of 2 * tok tokens of a row, a range of the row's keys,
-// which all lie in pages. (Blocks of one group that took turns as in kTreeAlt beside the
-// others doubled the code that runs at a time: a step of chunks and single tokens took 93 us
-// for 77, many short prompts 363 for 310, with four times the stalls for instructions.)
-// kPagedAlt: the same where no row has more than tok tokens: with room for one group of
-// queries only, the ring of K/V tiles is deeper.
-// kPagedFew: and no more than kFewRows rows of the products (tokens x G).
+// which all lie in pages. (Letting its blocks of one group take turns as in kTreeAlt put
+// more code to work at a time than the instruction caches hold: two chunks and eight other
+// rows 93 us for 77, 32 short prompts 363 for 310.) What bounds it beside the products: a
+// chunk of 2048 tokens on 30K, 64/8 heads, runs at 1.45 to 1.58 PFLOP/s; short prompts wait
+// for instructions (3.1 stalls to an issue, prefill_packed 0.7) and take up to 1.5 times
+// prefill_packed's time.
+// kPagedAlt: no row has more than tok tokens, and the groups take turns: with room for one
+// group of queries only, the ring of K/V tiles is deeper.
+// kPagedFew: and no more than kFewRows rows of the products (tokens x G). Bound by HBM at
+// d = 128 (32 rows of 1000 to 16000 keys, 64/8 heads: 141 us, 6.4 TB/s, 0.95 of the copy
+// rate; with four ring slots, K and V in the order of their use and not of their release,
+// 220), by the thread that issues the products at 64 (the same keys, 32/8 heads, 127 us:
+// 1400 cycles a tile for 12 products of 128 rows, whatever rows are used).
 enum Mode { kPrompts, kTreePair, kTreeAlt, kPaged, kPagedAlt, kPagedFew };
 constexpr int kFewRows = 32;
 constexpr bool tree_mode(int m) { return m == kTreePair || m == kTreeAlt; }
@@ -639,21 +647,22 @@ __device__ __forceinline__ void schedule_tree(const Params& p, Publisher<>& pub,
 // paged_attention. A unit is a block of tokens of a row against one KV head: tiles
 // 0 .. N - 1 of 128 keys, N from the keys that its last token sees. The units lie in
 // one line, rows one behind the other, their KV heads, their blocks; a unit is as long
-// as its keys and kPagedItemCost of them. (A tile of one group of rows takes almost as long as
-// one of two.) The line is cut into equal shares, one to a
-// CTA, so that a step with chunks, drafts and single tokens at once is balanced
-// whatever its lengths. Where a cut falls inside a unit it moves to the nearest
-// boundary of tiles. The blocks' lengths in the line grow evenly (a causal limit) up
-// to the last, so sums over them have a closed form and nothing is stored.
+// as its keys and kPagedItemCost, about what its first loads and its end cost. (A tile of
+// one group of rows takes almost as long as one of two.) The line is cut into equal
+// shares, one to a CTA, so that a step with chunks, drafts and single tokens at once is
+// balanced whatever its lengths. Where a cut falls inside a unit it moves to the nearest
+// boundary of tiles. The blocks' lengths in the line grow evenly (a causal limit) up to
+// the last, so sums over them have a closed form and nothing is stored. (Two chunks, eight
+// other rows, 28/4 heads, with an item cost of 2 / 4 / 10 tiles: 100 / 92 / 98 us at that point.)
 // When every row has one block only and the units can be cut into equal parts, one
 // part to a CTA at most, that is done instead (see schedule_tree). And when a share is
 // longer than kPagedWhole of the longest units, they are dealt out whole, unit u to CTA
-// u mod ctas: nothing is left to merge, and CTAs that run items of one length at a time run the
-// same code at a time, which their common instruction caches reward (32 prompts of 16 to
-// 900 tokens: 287 us cut, 267 dealt out; one prompt of 8192, 64/8 heads, 756 and 760; a chunk
-// of 2048 on 30K tokens 1410 and 1372).
+// u mod ctas: nothing is left to merge, and CTAs that run items of one length at a time
+// run the same code at a time, which suits the instruction caches (32 prompts of 16 to 900
+// tokens, 64/8 heads, 13 of the longest units to a share: 287 us cut, 267 dealt out; one prompt
+// of 12000 tokens, 10 to a share: 1567 and 1706, waiting for the last units).
 constexpr int kPagedItemCost = 4 * BN;
-constexpr int kPagedWhole = 8;
+constexpr int kPagedWhole = 12;
 constexpr int kPagedShare = 3 * BN;  // least length of a share: two tiles of any unit it crosses
 
 struct PagedRow {
@@ -868,7 +877,7 @@ __device__ __forceinline__ void schedule_paged(const Params& p, Pub& pub, int la
     for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
     longest = __reduce_max_sync(0xffffffffu, longest);
     if (bad && blockIdx.x == 0) atomicOr(p.status, kStatusBadSeqlen);
-    const bool whole = p.whole || (longest + kPagedItemCost) * int64_t(kPagedWhole) <=
+    const bool whole = p.whole || (int64_t(longest) + kPagedItemCost) * kPagedWhole <=
                                       total / int(gridDim.x);
     if (total < (1 << 30)) schedule_line(p, row_0, int(total), whole, pub, lane);
     else schedule_line(p, row_0, total, whole, pub, lane);

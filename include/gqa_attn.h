@@ -446,8 +446,8 @@ GQA_API int gqa_attn_cache_append(uint16_t* k_cache, uint16_t* v_cache, const ui
  * channels (i, i + pairs), or (2i, 2i + 1) with interleaved != 0. Channels from
  * 2 * pairs on are not rotated. Rounded to bf16 once, at the end.
  *   positions : device int32 [axes, tokens], any values; the angle is exact to
- *               about 2^-22 turns over their whole range.
- *   inv_freq  : device fp32 [pairs], finite.
+ *               about 2^-25 turns over their whole range (frequencies up to 1).
+ *   inv_freq  : device fp32 [pairs], finite, below 2^24 in magnitude.
  *   axes      : 1, or up to 4 (time, height, width of images and video), where
  *               axis a turns the next sections[a] pairs (host int32 [axes],
  *               summing to pairs; read during the call).

@@ -698,3 +698,91 @@ def test_serving_step_with_drafts():
         _check(o, lse, q, kp, vp, table, tokens, cap, True, 1 / math.sqrt(d))
         want = _verify_want(probs, None, x, ua, us, drafts)
         assert (acc.tolist(), nxt.tolist()) == want
+
+
+# ------------------------------------------------------------------- limits
+
+
+def test_pages_far_behind_32_bits():
+    # a pool of more than 2^32 elements, most of which nobody uses
+    H_q, H_kv, d, page, pages = 8, 8, 128, 64, 70000
+    kp = torch.empty(pages, H_kv, page, d, dtype=torch.bfloat16, device="cuda")
+    vp = torch.empty_like(kp)
+    starts, counts = [0, 60], [130, 70]
+    lens = [130, 130]
+    table = np.array([[pages - 1, 5, pages - 2], [pages - 3, 66000, 65999]], np.int32)
+    for b in range(2):
+        for g in range(3):
+            kp[table[b, g]], vp[table[b, g]] = _randn(10 + b, H_kv, page, d), _randn(20 + g, H_kv,
+                                                                                    page, d)
+    kn, vn = _randn(1, 200, H_kv, d), _randn(2, 200, H_kv, d)
+    api.paged_append(kp, vp, kn, vn, _i32(table), _i32(starts), cu_seqlens=_cu(counts))
+    q = _randn(3, 70, H_q, d)
+    vp[pages - 1, 0, 3, 4] = float("inf")
+    args = dict(cu_seqlens=_cu([1, 69]), max_tokens=69)
+    o, lse = api.paged_attention(q, kp, vp, _i32(table), _i32(lens), **args)
+    api.check()
+    assert torch.isinf(o[0, 0, 4])
+    vp[pages - 1, 0, 3, 4] = 1.0
+    o, lse = api.paged_attention(q, kp, vp, _i32(table), _i32(lens), **args)
+    api.check()
+    _check(o, lse, q, kp, vp, table, [1, 69], lens, True, 1 / math.sqrt(d))
+    assert torch.equal(kp[pages - 1, :, 0], kn[0]) and torch.equal(vp[66000, :, 63], vn[197])
+
+
+@pytest.mark.parametrize("tokens,page", [(1, 16), (6, 128), (40, 32), (40, 128)])
+def test_a_withheld_copy_is_reported(tokens, page):
+    # (rows so long that the first block has keys to wait for)
+    H_q, H_kv, d = 16, 2, 128
+    lens = [30000, 500]
+    table, pages = _table(lens, page)
+    q = _randn(1, 2 * tokens, H_q, d)
+    kp, vp = _randn(2, pages, H_kv, page, d), _randn(3, pages, H_kv, page, d)
+    api.check()
+    assert api.gqa_attn_debug_inject_timeout(1) == api.GQA_OK
+    api.paged_attention(q, kp, vp, _i32(table), _i32(lens))
+    with pytest.raises(api.GqaError) as e:
+        api.check()
+    assert e.value.code == api.GQA_ERR_DEVICE_TIMEOUT
+    o, lse = api.paged_attention(q, kp, vp, _i32(table), _i32(lens))
+    api.check()
+    _check(o, lse, q, kp, vp, table, [tokens] * 2, lens, True, 1 / math.sqrt(d))
+
+
+def test_large_batch():
+    # more rows than a scheduling warp keeps in registers, by far; most of them short
+    B, page = 20000, 16
+    rng = np.random.RandomState(1)
+    lens = rng.randint(0, 40, B)
+    lens[[7, 15000]] = [3000, 5000]
+    table, pages = _table(list(lens), page, 5)
+    q = _randn(1, B, 3, 64)
+    kp, vp = _randn(2, pages, 1, page, 64), _randn(3, pages, 1, page, 64)
+    o, lse = api.paged_attention(q, kp, vp, _i32(table), _i32(lens.tolist()))
+    api.check()
+    for b in [0, 1, 7, 31, 32, 9999, 15000, B - 1] + list(rng.randint(0, B, 40)):
+        _check(o[b:b + 1], lse[b:b + 1], q[b:b + 1], kp, vp, table[b:b + 1], [1], [int(lens[b])],
+               True, 1 / 8, f"row {b}")
+    assert torch.equal(torch.isneginf(lse).all(1).cpu(), torch.from_numpy(lens == 0))
+
+
+@pytest.mark.parametrize("causal", [True, False], ids=["causal", "full"])
+def test_many_short_prompts_are_dealt_out_whole(causal):
+    # more than a dozen units to every CTA, none cut; against rows on their own, which are cut or
+    # not in other ways, and in 64 bits
+    H_q, H_kv, d, page = 16, 1, 128, 32
+    rng = np.random.RandomState(2)
+    tokens = [int(t) for t in rng.randint(0, 80, 800)]
+    lens = [t + int(rng.randint(0, 30)) for t in tokens]
+    table, pages = _table(lens, page, 6, junk=BIG)
+    q = _randn(1, sum(tokens), H_q, d)
+    kp, vp = _randn(2, pages, H_kv, page, d), _randn(3, pages, H_kv, page, d)
+    o, lse = api.paged_attention(q, kp, vp, _i32(table), _i32(lens), cu_seqlens=_cu(tokens),
+                                 max_tokens=80, causal=causal)
+    api.check()
+    first = np.cumsum([0] + tokens)
+    for b in [0, 1, 31, 32, 33, 798, 799] + list(rng.randint(0, 800, 60)):
+        a, e = first[b], first[b + 1]
+        _check(o[a:e], lse[a:e], q[a:e], kp, vp, table[b:b + 1], tokens[b:b + 1], lens[b:b + 1],
+               causal, 1 / math.sqrt(d), f"row {b}")
+    assert torch.isfinite(o).all()
