@@ -1132,7 +1132,7 @@ def paged_attention(q, k_pages, v_pages, block_table, kv_lens, *, cu_seqlens=Non
     sums cu_seqlens int32 [B+1]; None: total / B per row). Token t sees the keys
     j <= kv_lens[b] - T + t (causal) or all of them. A call may mix single tokens, drafted tokens in
     a line and chunks of prompts. max_tokens bounds T; it is needed with cu_seqlens, whose values
-    stay on the device. max_keys bounds kv_lens (None: what the table holds); up to 512 saves a
+    stay on the device. max_keys bounds kv_lens (None: what the table holds); up to 640 saves a
     kernel.
 
     Returns (o [total,H_q,d] bf16, lse [total,H_q] fp32). ``workspace``: a uint8 CUDA tensor of

@@ -79,7 +79,9 @@ constexpr int kSchedSeqs = 1024;     // sequences whose schedule is kept in shar
 constexpr int kTreeCtas = 152;       // most CTAs of a decode_tree launch (workspace size)
 // decode_tree: rows are not cut where the cache holds at most this many tiles with the drafts' own
 // (512 slots), which saves the merge (8 units of 2 tiles 8.1 us against 10.2 cut, 4 tiles 10.5
-// against 11.0, 5 tiles 12.0 against 11.2, 9 tiles 18.4 against 11.7). The host goes by the size
+// against 11.0, 5 tiles 12.0 against 11.2, 9 tiles 18.4 against 11.7). paged_attention: rows of
+// at most 5 tiles, whose merge would have to be launched too (single tokens on 533 keys, 1 / 8 /
+// 32 rows of 64/8 heads: 11.9 / 18.4 / 37 us cut, 13.1 / 14.3 / 26 whole). The host goes by the size
 // of the cache, since the lengths are on the device: short contexts in a larger cache are cut.
 constexpr int kWholeTiles = 5;
 constexpr uint32_t kBoxBytes = BM * 128;       // 128 rows x 64 bf16
@@ -660,9 +662,13 @@ __device__ __forceinline__ void schedule_tree(const Params& p, Publisher<>& pub,
 // u mod ctas: nothing is left to merge, and CTAs that run items of one length at a time
 // run the same code at a time, which suits the instruction caches (32 prompts of 16 to 900
 // tokens, 64/8 heads, 13 of the longest units to a share: 287 us cut, 267 dealt out; one prompt
-// of 12000 tokens, 10 to a share: 1567 and 1706, waiting for the last units).
+// of 12000 tokens, 10 to a share: 1567 and 1706, waiting for the last units). So they are
+// when even the CTA with the most of the longest units is done before cuts would be
+// merged, kPagedMergeCost (single tokens of 8 / 32 rows of 1000 keys, 64/8 heads: 18.5 / 46 us
+// cut, 22 / 37 dealt out, the merge kernel finding nothing to do).
 constexpr int kPagedItemCost = 4 * BN;
 constexpr int kPagedWhole = 12;
+constexpr int kPagedMergeCost = 4 * BN;
 constexpr int kPagedShare = 3 * BN;  // least length of a share: two tiles of any unit it crosses
 
 struct PagedRow {
@@ -868,17 +874,22 @@ __device__ __forceinline__ void schedule_paged(const Params& p, Pub& pub, int la
     if (!p.whole && lane == 0) p.part_info[blockIdx.x] = make_int4(0, 0, 0, 0);
     const PagedRow row_0 = paged_row(p, lane, bad);  // the first 32 rows stay in registers
     int64_t total = 0;
-    int longest = 0;
+    int longest = 0, units = 0;
     for (int b0 = 0; b0 < p.B; b0 += 32) {
         const PagedRow r = b0 == 0 ? row_0 : paged_row(p, b0 + lane, bad);
         total += r.line * p.H_kv;
         if (r.blocks > 0) longest = max(longest, r.n);
+        units += r.blocks * p.H_kv;
     }
     for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
     longest = __reduce_max_sync(0xffffffffu, longest);
     if (bad && blockIdx.x == 0) atomicOr(p.status, kStatusBadSeqlen);
-    const bool whole = p.whole || (int64_t(longest) + kPagedItemCost) * kPagedWhole <=
-                                      total / int(gridDim.x);
+    units = __reduce_add_sync(0xffffffffu, units);
+    const int ctas = gridDim.x;
+    const int64_t unit = int64_t(longest) + kPagedItemCost;
+    const bool whole = p.whole || unit * kPagedWhole * ctas <= total ||
+                       (total < (1 << 30) &&
+                        cdiv(units, ctas) * unit <= total / ctas + kPagedMergeCost);
     if (total < (1 << 30)) schedule_line(p, row_0, int(total), whole, pub, lane);
     else schedule_line(p, row_0, total, whole, pub, lane);
 }
@@ -2547,7 +2558,7 @@ extern "C" int gqa_attn_paged_attention(
     p.scale_log2 = scale * kLog2e;
     p.inject_timeout = take_injected_timeout() ? 1 : 0;
     // no more CTAs than there can be tiles, or units that are not cut
-    const int64_t row_tiles = (int64_t(p.S_max) + BN - 1) / BN + 1;
+    const int64_t row_tiles = (int64_t(p.S_max) + BN - 1) / BN;
     p.whole = row_tiles <= kWholeTiles;
     const int64_t blocks = int64_t(total) / (2 * plan.tok) + (B < total ? B : total);
     const int64_t shares = blocks * H_kv * (p.whole ? 1 : row_tiles);

@@ -498,7 +498,7 @@ GQA_API int gqa_attn_paged_append(
  *                per row with max_tokens = 1 runs fastest.
  *   max_keys   : no row has more keys, or 0: table_width * page_size. A length
  *                outside [0, max_keys] is clamped and reported. Small values
- *                (512 and fewer) save the merge.
+ *                (640 and fewer) save the merge and its launch.
  *   workspace  : 256-byte aligned device memory of at least
  *                gqa_attn_paged_attention_workspace_size() bytes, as for
  *                gqa_attn_decode_tree.
