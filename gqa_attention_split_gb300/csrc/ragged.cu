@@ -2194,12 +2194,13 @@ struct AppendParams {
 
 // One warp per entry: K and V of one token, every head, four 16-byte pieces of
 // each a lane at a time with all their loads in flight. A copy, bound by HBM (a
-// packed step of 7205 tokens, 59 MB: 11.5 us against 8.7 at the copy rate) or,
-// for a few tokens, by the chain launch, prefix sums, start, copy (2.7 us in a graph).
-constexpr int kAppendWarps = 8;
+// packed step of 7205 tokens, 59 MB: 11.5 us against 8.8 at the copy rate; blocks of
+// eight warps 11.8, with the pieces loaded behind the search for their place 12.3) or,
+// for a few tokens, by the chain launch, prefix sums, start, copy (2.6 us in a graph).
+constexpr int kAppendWarps = 4;
 
 template <int D, bool kPaged>
-__global__ void __launch_bounds__(kAppendWarps * 32) append_kernel(const AppendParams p) {
+__global__ void __launch_bounds__(kAppendWarps * 32, 8) append_kernel(const AppendParams p) {
     grid_launch_dependents();
     grid_wait_primary();
     const int lane = threadIdx.x & 31;
@@ -2212,6 +2213,26 @@ __global__ void __launch_bounds__(kAppendWarps * 32) append_kernel(const AppendP
             row_range(p.cu, p.B, p.total, b, first, n, bad);
         }
     }
+    // What goes where is three dependent loads away, what goes is at hand: the first pieces
+    // are on their way meanwhile.
+    constexpr int kPieces = D / 8, kBatch = 4;
+    const int n_pieces = p.H_kv * kPieces;
+    const int src = e < p.total ? (p.index ? p.index[e] : e) : -1;
+    const bool there = src >= 0 && src < p.total_new;
+    const uint16_t* k_src = p.k + (there ? src * p.k_st : 0);
+    const uint16_t* v_src = p.v + (there ? src * p.v_st : 0);
+    uint4 kx[kBatch], vx[kBatch];
+    auto load = [&](int v0) {
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+            const int v = v0 + 32 * u;
+            if (v >= n_pieces) break;
+            const int h = v / kPieces, c = v % kPieces * 8;
+            kx[u] = *reinterpret_cast<const uint4*>(k_src + h * p.k_sh + c);
+            vx[u] = *reinterpret_cast<const uint4*>(v_src + h * p.v_sh + c);
+        }
+    };
+    if (there) load(lane);
     // the entry's row: the last b with cu[b] <= e, by 32 probes at a time
     int b = 0, i = 0;
     bool mine = e < p.total;
@@ -2240,8 +2261,7 @@ __global__ void __launch_bounds__(kAppendWarps * 32) append_kernel(const AppendP
     }
     if (mine) {
         const int64_t slot = int64_t(p.starts[b]) + i;
-        const int src = p.index ? p.index[e] : e;
-        bool fits = slot >= 0 && slot < p.S_max && src >= 0 && src < p.total_new;
+        bool fits = slot >= 0 && slot < p.S_max && there;
         int page = 0;
         if (kPaged && fits) {
             page = p.table[size_t(b) * p.table_width + slot / p.page_size];
@@ -2250,31 +2270,19 @@ __global__ void __launch_bounds__(kAppendWarps * 32) append_kernel(const AppendP
         if (!fits) {
             bad = true;
         } else {
-            constexpr int kPieces = D / 8, kBatch = 4;
-            const uint16_t* k_src = p.k + src * p.k_st;
-            const uint16_t* v_src = p.v + src * p.v_st;
             const size_t base = kPaged ? size_t(slot % p.page_size) * D
                                        : (size_t(b) * p.H_kv * p.S_max + slot) * D;
             const size_t head = size_t(kPaged ? p.page_size : p.S_max) * D;
-            uint16_t* const kc = p.kc + (kPaged ? page * p.k_page : 0);
-            uint16_t* const vc = p.vc + (kPaged ? page * p.v_page : 0);
-            const int n = p.H_kv * kPieces;
+            uint16_t* const kc = p.kc + (kPaged ? page * p.k_page : 0) + base;
+            uint16_t* const vc = p.vc + (kPaged ? page * p.v_page : 0) + base;
 #pragma unroll 1
-            for (int v0 = lane; v0 < n; v0 += 32 * kBatch) {
-                uint4 kx[kBatch], vx[kBatch];
+            for (int v0 = lane; v0 < n_pieces; v0 += 32 * kBatch) {
+                if (v0 != lane) load(v0);
 #pragma unroll
                 for (int u = 0; u < kBatch; ++u) {
                     const int v = v0 + 32 * u;
-                    if (v >= n) break;
-                    const int h = v / kPieces, c = v % kPieces * 8;
-                    kx[u] = *reinterpret_cast<const uint4*>(k_src + h * p.k_sh + c);
-                    vx[u] = *reinterpret_cast<const uint4*>(v_src + h * p.v_sh + c);
-                }
-#pragma unroll
-                for (int u = 0; u < kBatch; ++u) {
-                    const int v = v0 + 32 * u;
-                    if (v >= n) break;
-                    const size_t dst = base + v / kPieces * head + v % kPieces * 8;
+                    if (v >= n_pieces) break;
+                    const size_t dst = v / kPieces * head + v % kPieces * 8;
                     *reinterpret_cast<uint4*>(kc + dst) = kx[u];
                     *reinterpret_cast<uint4*>(vc + dst) = vx[u];
                 }
