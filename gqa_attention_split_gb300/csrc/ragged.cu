@@ -281,7 +281,8 @@ struct Geo {
     static constexpr uint32_t kStageOff = kRingOff + kRing * kTileBytes;  // 8 warps
     static constexpr uint32_t kXchOff = kStageOff + 8 * kStageBytes;  // float4 [2][128]
     static constexpr uint32_t kSeqOff = kXchOff + 2 * BM * 16;        // int2 [kSchedSeqs]
-    static constexpr uint32_t kItemOff = kSeqOff + (paged_mode(kMode) ? 0 : kSchedSeqs * 8);
+    static constexpr uint32_t kItemOff =
+        kSeqOff + (kMode == kPagedAlt || kMode == kPagedFew ? 0 : kSchedSeqs * 8);
     static constexpr uint32_t kBarOff = kItemOff + kItemSlots * 64;
     static constexpr int kSmemBytes = 1024 + kBarOff + 512;
     static_assert(kSmemBytes <= 232448, "more dynamic shared memory than one CTA may have");
@@ -352,6 +353,51 @@ struct Publisher {
     }
 };
 
+// ---- rows of paged_attention
+
+constexpr int kPagedItemCost = 4 * BN;
+constexpr int kPagedWhole = 12;
+constexpr int kPagedMergeCost = 8 * BN;
+constexpr int kPagedShare = 3 * BN;  // least length of a share: two tiles of any unit it crosses
+
+struct PagedRow {
+    int q0, T, n, blocks;
+    int64_t line;  // length of its blocks against one KV head
+};
+__device__ __forceinline__ int paged_limit(const Params& p, const PagedRow& r, int i) {
+    if (!p.causal || i + 1 >= r.blocks) return r.n;
+    return max(0, r.n - r.T + (i + 1) * 2 * p.tok);
+}
+// Length of the first k blocks of a row.
+template <typename I>
+__device__ __forceinline__ I paged_line(const Params& p, const PagedRow& r, int k) {
+    I sum = I(k) * kPagedItemCost;
+    if (!p.causal) return sum + I(k) * r.n;
+    if (k == r.blocks && k > 0) {
+        --k;
+        sum += r.n;
+    }
+    const int block = 2 * p.tok, off = r.n - r.T;
+    // the blocks before `none` see no key
+    const int none = off < 0 ? min(-off / block, k) : 0;
+    return sum + I(k - none) * off + p.tok * (I(k) * (k + 1) - I(none) * (none + 1));
+}
+__device__ __forceinline__ PagedRow paged_row(const Params& p, int b, bool& bad) {
+    PagedRow r{0, 0, 0, 0, 0};
+    if (b >= p.B) return r;
+    const int keys = p.ctx[b];
+    row_range(p.cu_q, p.B, p.total_q, b, r.q0, r.T, bad);
+    if (r.T > p.max_tokens) {
+        r.T = p.max_tokens;
+        bad = true;
+    }
+    r.n = clampi(keys, 0, p.S_max);
+    bad = bad || r.n != keys;
+    r.blocks = cdiv(r.T, 2 * p.tok);
+    r.line = paged_line<int64_t>(p, r, r.blocks);
+    return r;
+}
+
 // kPrompts. A block's cost is the number of keys it sees, so a sequence's
 // blocks are numbered by levels (key position of the block / block length) and
 // the launch runs the levels from the highest down over all sequences, in
@@ -360,15 +406,22 @@ struct Publisher {
 // heads run together even where their K and V are larger than L2: one group of
 // heads after another, each within L2, ends on heavy items several times (one
 // sequence of 64K tokens, 16/8 heads: 11.9 ms in groups, 10.8 this way).
+template <int kMode>
 __device__ __forceinline__ void schedule_prompts(const Params& p, int2* seqs, Publisher<>& pub,
                                                  int lane) {
     const int block = 2 * p.tok;
     bool bad = false;
     auto levels = [&](int b) {  // x: lowest level, y: blocks
         int q0, T, k0, n;
-        row_range(p.cu_q, p.B, p.total_q, b, q0, T, bad);
-        if (p.cu_k) row_range(p.cu_k, p.B, p.total_k, b, k0, n, bad);
-        else n = T;
+        if constexpr (kMode == kPaged) {
+            const PagedRow r = paged_row(p, b, bad);
+            T = r.T;
+            n = r.n;
+        } else {
+            row_range(p.cu_q, p.B, p.total_q, b, q0, T, bad);
+            if (p.cu_k) row_range(p.cu_k, p.B, p.total_k, b, k0, n, bad);
+            else n = T;
+        }
         return make_int2((p.causal ? max(n - T, 0) : n) / block, cdiv(T, block));
     };
     // More sequences than the table holds: the blocks run in the sequences'
@@ -490,14 +543,21 @@ __device__ __forceinline__ void schedule_prompts(const Params& p, int2* seqs, Pu
         w.kvh = int(R % p.H_kv);
         w.b = b;
         w.dst = -1;
-        row_range(p.cu_q, p.B, p.total_q, b, w.q_row, w.T, bad);
-        w.k_row = w.q_row;
-        w.n_own = w.T;
-        if (p.cu_k) row_range(p.cu_k, p.B, p.total_k, b, w.k_row, w.n_own, bad);
+        if constexpr (kMode == kPaged) {
+            const PagedRow r = paged_row(p, b, bad);
+            w.q_row = r.q0;
+            w.T = r.T;
+            w.n_own = r.n;
+        } else {
+            row_range(p.cu_q, p.B, p.total_q, b, w.q_row, w.T, bad);
+            w.k_row = w.q_row;
+            w.n_own = w.T;
+            if (p.cu_k) row_range(p.cu_k, p.B, p.total_k, b, w.k_row, w.n_own, bad);
+        }
         w.off = w.n_own - w.T;
         w.tok0 = i * block;
-        w.n0 = cdiv(group_last<kPrompts>(p, w, 0), BN);
-        w.n1 = w.tok0 + p.tok < w.T ? cdiv(group_last<kPrompts>(p, w, 1), BN) : 0;
+        w.n0 = cdiv(group_last<kMode>(p, w, 0), BN);
+        w.n1 = w.tok0 + p.tok < w.T ? cdiv(group_last<kMode>(p, w, 1), BN) : 0;
         w.n = max(w.n0, w.n1);
         if (!pub.put(w, lane)) return;
     }
@@ -657,58 +717,16 @@ __device__ __forceinline__ void schedule_tree(const Params& p, Publisher<>& pub,
 // the last, so sums over them have a closed form and nothing is stored. (Two chunks, eight
 // other rows, 28/4 heads, with an item cost of 2 / 4 / 10 tiles: 100 / 92 / 98 us at that point.)
 // When every row has one block only and the units can be cut into equal parts, one
-// part to a CTA at most, that is done instead (see schedule_tree). And when a share is
-// longer than kPagedWhole of the longest units, they are dealt out whole, unit u to CTA
-// u mod ctas: nothing is left to merge, and CTAs that run items of one length at a time
-// run the same code at a time, which suits the instruction caches (32 prompts of 16 to 900
-// tokens, 64/8 heads, 13 of the longest units to a share: 287 us cut, 267 dealt out; one prompt
-// of 12000 tokens, 10 to a share: 1567 and 1706, waiting for the last units). So they are
-// when even the CTA with the most of the longest units is done before cuts would be
-// merged, kPagedMergeCost (single tokens of 8 / 32 rows of 1000 keys, 64/8 heads: 18.5 / 46 us
-// cut, 22 / 37 dealt out, the merge kernel finding nothing to do).
-constexpr int kPagedItemCost = 4 * BN;
-constexpr int kPagedWhole = 12;
-constexpr int kPagedMergeCost = 4 * BN;
-constexpr int kPagedShare = 3 * BN;  // least length of a share: two tiles of any unit it crosses
-
-struct PagedRow {
-    int q0, T, n, blocks;
-    int64_t line;  // length of its blocks against one KV head
-};
-__device__ __forceinline__ int paged_limit(const Params& p, const PagedRow& r, int i) {
-    if (!p.causal || i + 1 >= r.blocks) return r.n;
-    return max(0, r.n - r.T + (i + 1) * 2 * p.tok);
-}
-// Length of the first k blocks of a row.
-template <typename I>
-__device__ __forceinline__ I paged_line(const Params& p, const PagedRow& r, int k) {
-    I sum = I(k) * kPagedItemCost;
-    if (!p.causal) return sum + I(k) * r.n;
-    if (k == r.blocks && k > 0) {
-        --k;
-        sum += r.n;
-    }
-    const int block = 2 * p.tok, off = r.n - r.T;
-    // the blocks before `none` see no key
-    const int none = off < 0 ? min(-off / block, k) : 0;
-    return sum + I(k - none) * off + p.tok * (I(k) * (k + 1) - I(none) * (none + 1));
-}
-__device__ __forceinline__ PagedRow paged_row(const Params& p, int b, bool& bad) {
-    PagedRow r{0, 0, 0, 0, 0};
-    if (b >= p.B) return r;
-    const int keys = p.ctx[b];
-    row_range(p.cu_q, p.B, p.total_q, b, r.q0, r.T, bad);
-    if (r.T > p.max_tokens) {
-        r.T = p.max_tokens;
-        bad = true;
-    }
-    r.n = clampi(keys, 0, p.S_max);
-    bad = bad || r.n != keys;
-    r.blocks = cdiv(r.T, 2 * p.tok);
-    r.line = paged_line<int64_t>(p, r, r.blocks);
-    return r;
-}
-
+// part to a CTA at most, that is done instead (see schedule_tree).
+// And units are not cut at all when the last CTA would be done about as early without:
+// nothing is left to merge then (kPagedMergeCost). kPaged runs them as prompts, in levels,
+// long ones first: CTAs that run items of one length at a time run the same code at a
+// time, and neighbouring SMs share instruction caches (12 prompts of 900 tokens, 64/8 heads:
+// cut 290 us; whole units dealt out in the order of the line 257, in levels 206; 32 prompts of 16
+// to 900 tokens 287, 262 and 188; one of 8192 757 cut and 727 in levels; one of 2304, 28/4
+// heads, 58 and 46). The others deal unit u to CTA u mod ctas (single tokens of 8 / 32 rows
+// of 1000 keys, 64/8 heads: 18.5 / 46 us cut, 22 / 37 dealt out, the merge kernel finding
+// nothing to do), also when a share is longer than kPagedWhole of the longest units.
 // I: an integer type that holds every position of the line (64-bit divisions cost a
 // microsecond before a CTA's first item).
 template <typename I, typename Pub>
@@ -868,30 +886,47 @@ __device__ __forceinline__ void schedule_line(const Params& p, const PagedRow& r
     pub.put(end, lane);
 }
 
-template <typename Pub>
-__device__ __forceinline__ void schedule_paged(const Params& p, Pub& pub, int lane) {
+template <int kMode, typename Pub>
+__device__ __forceinline__ void schedule_paged(const Params& p, int2* seqs, Pub& pub, int lane) {
     bool bad = false;
     if (!p.whole && lane == 0) p.part_info[blockIdx.x] = make_int4(0, 0, 0, 0);
     const PagedRow row_0 = paged_row(p, lane, bad);  // the first 32 rows stay in registers
     int64_t total = 0;
-    int longest = 0, units = 0;
+    int longest = 0, shortest = 0x7fffffff, units = 0;
     for (int b0 = 0; b0 < p.B; b0 += 32) {
         const PagedRow r = b0 == 0 ? row_0 : paged_row(p, b0 + lane, bad);
         total += r.line * p.H_kv;
-        if (r.blocks > 0) longest = max(longest, r.n);
         units += r.blocks * p.H_kv;
+        if (r.blocks > 0) {
+            longest = max(longest, r.n);
+            shortest = min(shortest, paged_limit(p, r, 0));
+        }
     }
     for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
     longest = __reduce_max_sync(0xffffffffu, longest);
     if (bad && blockIdx.x == 0) atomicOr(p.status, kStatusBadSeqlen);
-    units = __reduce_add_sync(0xffffffffu, units);
+    units = __reduce_add_sync(0xffffffffu, units);  // (used below 2^30 only)
     const int ctas = gridDim.x;
-    const int64_t unit = int64_t(longest) + kPagedItemCost;
-    const bool whole = p.whole || unit * kPagedWhole * ctas <= total ||
-                       (total < (1 << 30) &&
-                        cdiv(units, ctas) * unit <= total / ctas + kPagedMergeCost);
-    if (total < (1 << 30)) schedule_line(p, row_0, int(total), whole, pub, lane);
-    else schedule_line(p, row_0, total, whole, pub, lane);
+    const int64_t unit = int64_t(longest) + kPagedItemCost, share = total / ctas;
+    if constexpr (kMode == kPaged) {
+        shortest = __reduce_min_sync(0xffffffffu, shortest);
+        // when the last CTA is done: after the rounds of the longest units at most, or, long
+        // ones first, about one of the shortest units after the others
+        int64_t end = max(unit, share + shortest + kPagedItemCost);
+        if (total < (1 << 30)) end = min(end, cdiv(units, ctas) * unit);
+        if (p.whole || end <= share + share / 10 + kPagedMergeCost) {
+            schedule_prompts<kPaged>(p, seqs, pub, lane);
+            return;
+        }
+        if (total < (1 << 30)) schedule_line(p, row_0, int(total), false, pub, lane);
+        else schedule_line(p, row_0, total, false, pub, lane);
+    } else {
+        const bool whole = p.whole || unit * kPagedWhole <= share ||
+                           (total < (1 << 30) &&
+                            cdiv(units, ctas) * unit <= share + kPagedMergeCost / 2);
+        if (total < (1 << 30)) schedule_line(p, row_0, int(total), whole, pub, lane);
+        else schedule_line(p, row_0, total, whole, pub, lane);
+    }
 }
 
 // Ring position, counted from the item's first, of its V tile j, of n tiles. The tiles
@@ -1541,7 +1576,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             };
             Publisher<decltype(second_loader)> pub{smem + Gm::kItemOff, bars, p.status,
                                                    second_loader};
-            schedule_paged(p, pub, lane);
+            schedule_paged<kMode>(p, nullptr, pub, lane);
             if (lane == 0)
                 for (int i = max(0, issued - kRing); i < issued; ++i) ring_wait(i);
         }
@@ -1549,9 +1584,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         if constexpr (kTree)
             schedule_tree<kMode>(p, pub, lane);
         else if constexpr (kMode == kPaged)
-            schedule_paged(p, pub, lane);
+            schedule_paged<kMode>(p, reinterpret_cast<int2*>(smem + Gm::kSeqOff), pub, lane);
         else if constexpr (kMode == kPrompts)
-            schedule_prompts(p, reinterpret_cast<int2*>(smem + Gm::kSeqOff), pub, lane);
+            schedule_prompts<kMode>(p, reinterpret_cast<int2*>(smem + Gm::kSeqOff), pub, lane);
       } else {
         // ------------------------------------------------------------ repair
         // P is 0 at a key that a row does not see, but 0 * NaN is not: in the
@@ -2572,6 +2607,7 @@ extern "C" int gqa_attn_paged_attention(
     const int64_t shares = blocks * H_kv * (p.whole ? 1 : row_tiles);
     const int most = sms < kTreeCtas ? sms : kTreeCtas;
     const int ctas = int(shares < most ? shares : most);
+    p.max_blocks = int(blocks);  // (below 2^31: total / 2 + 65535 at most)
     p.n_teams = ctas;
     p.part_info = static_cast<int4*>(workspace);
     p.part_o = reinterpret_cast<float*>(p.part_info + kTreeCtas);
