@@ -99,10 +99,9 @@ constexpr float kRescaleThreshold = 8.f;
 // kPaged: items are blocks of 2 * tok tokens of a row, a range of the row's keys,
 // which all lie in pages. (Letting its blocks of one group take turns as in kTreeAlt put
 // more code to work at a time than the instruction caches hold: two chunks and eight other
-// rows 93 us for 77, 32 short prompts 363 for 310.) What bounds it beside the products: a
-// chunk of 2048 tokens on 30K, 64/8 heads, runs at 1.45 to 1.58 PFLOP/s; short prompts wait
-// for instructions (3.1 stalls to an issue, prefill_packed 0.7) and take up to 1.5 times
-// prefill_packed's time.
+// rows 93 us for 77, 32 short prompts 363 for 310.) A chunk of 2048 tokens on 30K, 64/8
+// heads, runs at 1.45 to 1.58 PFLOP/s, prompts in prefill_packed's time or up to 1.15 of it
+// (the step above 72 us, bound by loads, instruction fetch and the merge).
 // kPagedAlt: no row has more than tok tokens, and the groups take turns: with room for one
 // group of queries only, the ring of K/V tiles is deeper.
 // kPagedFew: and no more than kFewRows rows of the products (tokens x G). Bound by HBM at
@@ -814,8 +813,7 @@ __device__ __forceinline__ void schedule_line(const Params& p, const PagedRow& r
             block = lo;
             s = start + kvh * line + paged_line<I>(p, r, block);
         }
-        // the row's units from there on (few instructions: every one of this warp's that
-        // is run between two items takes the softmax warps' out of the cache)
+        // the row's units from there on, without another search
 #pragma unroll 1
         for (;;) {
             Item w{};
@@ -1017,7 +1015,7 @@ __device__ __forceinline__ void load_pages(const Params& p, const Item& w, int n
 }
 
 // The same for kPaged where a tile lies in one page: one lane copies, and there is less
-// code (32 prompts of 16 to 900 tokens 287 -> 263 us).
+// code (32 prompts of 16 to 900 tokens, cut, 263 us against 287).
 template <int D>
 __device__ __forceinline__ void load_whole_tiles(const Params& p, const Item& w, int n,
                                                  const CUtensorMap* tmap_k,
