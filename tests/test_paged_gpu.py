@@ -786,3 +786,39 @@ def test_many_short_prompts_are_dealt_out_whole(causal):
         _check(o[a:e], lse[a:e], q[a:e], kp, vp, table[b:b + 1], tokens[b:b + 1], lens[b:b + 1],
                causal, 1 / math.sqrt(d), f"row {b}")
     assert torch.isfinite(o).all()
+
+
+def test_calls_on_two_streams_at_once():
+    # each stream its own rows, workspaces and outputs; the same bits as one call at a time
+    H_q, H_kv, d, page = 16, 2, 128, 16
+    f = torch.from_numpy(_freq(64)).cuda()
+    sets = []
+    for s, (tokens, lens) in enumerate([([1] * 20, list(range(50, 4050, 200))),
+                                        ([200, 1, 30], [900, 5000, 30])]):
+        table, pages = _table(lens, page, s)
+        n = sum(tokens)
+        sets.append(dict(q=_randn(s, n, H_q, d), kp=_randn(s + 5, pages, H_kv, page, d),
+                         vp=_randn(s + 9, pages, H_kv, page, d), table=_i32(table),
+                         lens=_i32(lens), cu=_cu(tokens), most=max(tokens),
+                         pos=_i32(list(range(n))), p=_dists(s, 8, 3000), u=torch.full(
+                             (4,), 0.37 + 0.2 * s, device="cuda")))
+
+    def run(x, stream=None):
+        q, _ = api.qk_norm_rope(x["q"], None, x["pos"], f, stream=stream)
+        o, lse = api.paged_attention(q, x["kp"], x["vp"], x["table"], x["lens"],
+                                     cu_seqlens=x["cu"], max_tokens=x["most"], stream=stream)
+        a, t = api.verify_drafts(x["p"], _i32([3, 5, 7, 9]), x["u"], x["u"], stream=stream)
+        return o, lse, a, t
+
+    want = [run(x) for x in sets]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [[], []]
+    for _ in range(15):
+        for i in range(2):
+            got[i].append(run(sets[i], streams[i]))
+    torch.cuda.synchronize()
+    api.check()
+    for i in range(2):
+        for r in got[i]:
+            assert all(torch.equal(a, b) for a, b in zip(r, want[i]))
