@@ -962,11 +962,12 @@ def _counts(torch, name, t, given, n):
 
 
 def _weight(torch, name, t, d, device):
-    if not isinstance(t, torch.Tensor) or t.dtype not in (torch.bfloat16, torch.float32):
+    wide = isinstance(t, torch.Tensor) and t.dtype is torch.float32
+    if not wide and not (isinstance(t, torch.Tensor) and t.dtype is torch.bfloat16):
         raise TypeError(f"{name} must be a bfloat16 or float32 CUDA tensor")
-    if t.get_device() != device or t.shape != (d,) or t.stride(0) != 1:
+    if t.get_device() != device or t.dim() != 1 or t.numel() != d or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous [{d}] tensor on cuda:{device}")
-    return t.dtype is torch.float32
+    return wide
 
 
 @functools.lru_cache(maxsize=256)
@@ -986,26 +987,28 @@ def _floats(torch, name, t, n, device):
 
 def _pages(torch, k_pages, v_pages, block_table, H_kv, d, device):
     """Checks pages [num_pages, H_kv, page_size, d] and the block table [B, width]; returns
-    (B, num_pages, page_size, width, K page stride, V page stride)."""
+    (B, num_pages, page_size, width, K page stride, V page stride, H_kv, table pointer)."""
     for name, t in (("k_pages", k_pages), ("v_pages", v_pages)):
-        if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype is not torch.bfloat16:
+        if not isinstance(t, torch.Tensor) or t.dtype is not torch.bfloat16 or not t.is_cuda:
             raise TypeError(f"{name} must be a bfloat16 CUDA tensor")
         if t.get_device() != device:
             raise ValueError(f"{name} must be on cuda:{device}, got {t.device}")
     shape = k_pages.shape
-    if (len(shape) != 4 or v_pages.shape != shape or (H_kv is not None and shape[1] != H_kv)
-            or shape[3] != d):
+    if len(shape) != 4 or v_pages.shape != shape:
         raise ValueError(f"k_pages, v_pages must be [num_pages, {H_kv or 'H_kv'}, page_size, {d}]")
-    n, heads, size, _ = shape
-    for name, t in (("k_pages", k_pages), ("v_pages", v_pages)):
-        _, sh, ss, sd = t.stride()
-        if sd != 1 or (size > 1 and ss != d) or (heads > 1 and sh != size * d):
-            raise ValueError(f"every page of {name} must be contiguous")
+    n, heads, size, width = shape
+    if width != d or (H_kv is not None and heads != H_kv):
+        raise ValueError(f"k_pages, v_pages must be [num_pages, {H_kv or 'H_kv'}, page_size, {d}]")
+    kp, kh, ks, kd = k_pages.stride()
+    vp, vh, vs, vd = v_pages.stride()
+    if (kd != 1 or vd != 1 or (size > 1 and (ks != d or vs != d))
+            or (heads > 1 and (kh != size * d or vh != size * d))):
+        raise ValueError("every page of k_pages and v_pages must be contiguous")
     if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
         raise TypeError("block_table must be a contiguous int32 [B, width] CUDA tensor")
     B, width = block_table.shape
-    _ints(torch, "block_table", block_table, B * width, device)
-    return B, n, size, width, k_pages.stride(0), v_pages.stride(0)
+    return B, n, size, width, kp, vp, heads, _ints(torch, "block_table", block_table, B * width,
+                                                   device)
 
 
 def qk_norm_rope(q, k, positions, inv_freq, *, q_weight=None, k_weight=None,
@@ -1025,14 +1028,14 @@ def qk_norm_rope(q, k, positions, inv_freq, *, q_weight=None, k_weight=None,
     import torch
 
     qs, qh = _packed(torch, "q", q, None, None, None)
-    n, H_q, d = q.shape
+    n, H_q, d = q_shape = q.shape
     dev = q.get_device()
     ks = kh = kos = koh = 8
     H_kv = 0
     if k is not None:
         ks, kh = _packed(torch, "k", k, None, d, dev)
-        H_kv = k.shape[1]
-        if k.shape[0] != n:
+        n_k, H_kv, _ = k_shape = k.shape
+        if n_k != n:
             raise ValueError("q and k must have the same tokens")
         if H_kv == 0:
             raise ValueError("k has no heads")
@@ -1041,12 +1044,12 @@ def qk_norm_rope(q, k, positions, inv_freq, *, q_weight=None, k_weight=None,
     pairs = inv_freq.numel() if isinstance(inv_freq, torch.Tensor) else 0
     freq = _floats(torch, "inv_freq", inv_freq, pairs, dev)
     if sections is None:
-        axes, sec, want = 1, None, (n,)
+        axes, sec = 1, None
     else:
         axes = len(sections)
-        sec, want = (ctypes.c_int32 * axes)(*sections), (axes, n)
+        sec = (ctypes.c_int32 * axes)(*sections)
     pos = _ints(torch, "positions", positions, axes * n, dev)
-    if positions.shape != want:
+    if positions.dim() != (1 if sections is None else 2) or positions.shape[-1] != n:
         raise ValueError(f"positions must be {'[tokens]' if sections is None else '[axes, tokens]'}"
                          f", got {tuple(positions.shape)}")
     qw = kw = wide = None
@@ -1061,19 +1064,19 @@ def qk_norm_rope(q, k, positions, inv_freq, *, q_weight=None, k_weight=None,
     if eps is None and wide is not None:
         raise ValueError("weights need the norm (eps)")
     if q_out is None:
-        q_out = _empty(torch, q, q.shape, torch.bfloat16, stream)
+        q_out = _empty(torch, q, q_shape, torch.bfloat16, stream)
         qos, qoh = H_q * d, d
     else:
-        if q_out.shape != q.shape:
+        if q_out.shape != q_shape:
             raise ValueError("q_out must be shaped like q")
         qos, qoh = _packed(torch, "q_out", q_out, H_q, d, dev)
     k_ptr = ko_ptr = None
     if k is not None:
         if k_out is None:
-            k_out = _empty(torch, k, k.shape, torch.bfloat16, stream)
+            k_out = _empty(torch, k, k_shape, torch.bfloat16, stream)
             kos, koh = H_kv * d, d
         else:
-            if k_out.shape != k.shape:
+            if k_out.shape != k_shape:
                 raise ValueError("k_out must be shaped like k")
             kos, koh = _packed(torch, "k_out", k_out, H_kv, d, dev)
         k_ptr, ko_ptr = k.data_ptr(), k_out.data_ptr()
@@ -1102,7 +1105,8 @@ def paged_append(k_pages, v_pages, k_new, v_new, block_table, starts, *, cu_seql
     vs, vh = _packed(torch, "v_new", v_new, H_kv, d, dev)
     if v_new.shape[0] != total_new:
         raise ValueError("k_new and v_new must have the same shape")
-    B, n, size, width, kp, vp = _pages(torch, k_pages, v_pages, block_table, H_kv, d, dev)
+    B, n, size, width, kp, vp, _, table = _pages(torch, k_pages, v_pages, block_table, H_kv, d,
+                                                 dev)
     first = _ints(torch, "starts", starts, B, dev)
     total, idx, cu = total_new, None, None
     if index is not None:
@@ -1114,7 +1118,7 @@ def paged_append(k_pages, v_pages, k_new, v_new, block_table, starts, *, cu_seql
         raise ValueError("without cu_seqlens every row has the same number of entries")
     rc = _on_device(torch, dev, lambda: lib().gqa_attn_paged_append(
         k_pages.data_ptr(), v_pages.data_ptr(), k_new.data_ptr(), v_new.data_ptr(), cu, first, idx,
-        block_table.data_ptr(), B, H_kv, d, total, total_new, n, size, width, ks, kh, vs, vh, kp,
+        table, B, H_kv, d, total, total_new, n, size, width, ks, kh, vs, vh, kp,
         vp, _raw_stream(torch, dev, stream)))
     if rc != GQA_OK:
         raise GqaError(rc, "gqa_attn_paged_append")
@@ -1143,8 +1147,8 @@ def paged_attention(q, k_pages, v_pages, block_table, kv_lens, *, cu_seqlens=Non
     qs, qh = _packed(torch, "q", q, None, None, None)
     total, H_q, d = q.shape
     dev = q.get_device()
-    B, n, size, width, kp, vp = _pages(torch, k_pages, v_pages, block_table, None, d, dev)
-    H_kv = k_pages.shape[1]
+    B, n, size, width, kp, vp, H_kv, table = _pages(torch, k_pages, v_pages, block_table, None,
+                                                    d, dev)
     lens = _ints(torch, "kv_lens", kv_lens, B, dev)
     cu = None
     if cu_seqlens is not None:
@@ -1168,7 +1172,7 @@ def paged_attention(q, k_pages, v_pages, block_table, kv_lens, *, cu_seqlens=Non
         raise ValueError(f"workspace must be contiguous and on cuda:{dev}")
     rc = _on_device(torch, dev, lambda: lib().gqa_attn_paged_attention(
         q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), out.data_ptr(), lse.data_ptr(), cu,
-        lens, block_table.data_ptr(), B, H_q, H_kv, d, total, max_tokens, max_keys or 0, n, size,
+        lens, table, B, H_q, H_kv, d, total, max_tokens, max_keys or 0, n, size,
         width, qs, qh, kp, vp, 1 if causal else 0, sc, workspace.data_ptr(),
         workspace.numel() * workspace.element_size(), _raw_stream(torch, dev, stream)))
     if rc != GQA_OK:
@@ -1193,17 +1197,25 @@ def verify_drafts(target_probs, draft_tokens, u_accept, u_sample, cu_seqlens=Non
     Returns (accepted, next_tokens), int32 [B]. ``stream`` as prefill_packed."""
     import torch
 
-    for name, t in (("target_probs", target_probs), ("draft_probs", draft_probs)):
-        if t is None and name == "draft_probs":
-            continue
+    def table(name, t):
         if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype is not torch.float32:
             raise TypeError(f"{name} must be a float32 CUDA tensor")
-        if t.dim() != 2 or t.shape[1] != target_probs.shape[1]:
+        if t.dim() != 2:
             raise ValueError("target_probs and draft_probs must be [rows, V]")
-        if t.stride(1) != 1 and t.shape[1] > 1:
+        n, V = t.shape
+        st, sv = t.stride()
+        if sv != 1 and V > 1:
             raise ValueError(f"the last dimension of {name} must be contiguous")
+        return n, V, st
+
+    rows, V, target_stride = table("target_probs", target_probs)
     dev = target_probs.get_device()
-    rows, V = target_probs.shape
+    q_ptr, draft_stride = None, V
+    if draft_probs is not None:
+        n_q, V_q, draft_stride = table("draft_probs", draft_probs)
+        if V_q != V:
+            raise ValueError("target_probs and draft_probs must be [rows, V]")
+        q_ptr = draft_probs.data_ptr()
     total = draft_tokens.numel() if isinstance(draft_tokens, torch.Tensor) else 0
     toks = _ints(torch, "draft_tokens", draft_tokens, total, dev)
     B = rows - total
@@ -1216,17 +1228,16 @@ def verify_drafts(target_probs, draft_tokens, u_accept, u_sample, cu_seqlens=Non
         cu = _ints(torch, "cu_seqlens", cu_seqlens, B + 1, dev)
     elif B == 0 or total % B:
         raise ValueError("without cu_seqlens every row has the same number of drafted tokens")
-    if draft_probs is not None and (draft_probs.shape[0] != total
-                                    or draft_probs.get_device() != dev):
+    if draft_probs is not None and (n_q != total or draft_probs.get_device() != dev):
         raise ValueError(f"draft_probs must have {total} rows and be on cuda:{dev}")
     accepted = (_empty(torch, target_probs, B, torch.int32, stream) if accepted is None
                 else _counts(torch, "accepted", target_probs, accepted, B))
     next_tokens = (_empty(torch, target_probs, B, torch.int32, stream) if next_tokens is None
                    else _counts(torch, "next_tokens", target_probs, next_tokens, B))
     rc = _on_device(torch, dev, lambda: lib().gqa_attn_verify_drafts(
-        target_probs.data_ptr(), _ptr(draft_probs), toks, ua, us, cu, accepted.data_ptr(),
-        next_tokens.data_ptr(), B, total, V, target_probs.stride(0),
-        draft_probs.stride(0) if draft_probs is not None else V, _raw_stream(torch, dev, stream)))
+        target_probs.data_ptr(), q_ptr, toks, ua, us, cu, accepted.data_ptr(),
+        next_tokens.data_ptr(), B, total, V, target_stride, draft_stride,
+        _raw_stream(torch, dev, stream)))
     if rc != GQA_OK:
         raise GqaError(rc, "gqa_attn_verify_drafts")
     if stream is not None:
