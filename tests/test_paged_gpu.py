@@ -766,13 +766,13 @@ def test_large_batch():
     assert torch.equal(torch.isneginf(lse).all(1).cpu(), torch.from_numpy(lens == 0))
 
 
+@pytest.mark.parametrize("rows", [800, 1300])
 @pytest.mark.parametrize("causal", [True, False], ids=["causal", "full"])
-def test_many_short_prompts_are_dealt_out_whole(causal):
-    # more than a dozen units to every CTA, none cut; against rows on their own, which are cut or
-    # not in other ways, and in 64 bits
+def test_many_short_prompts_are_not_cut(causal, rows):
+    # a dozen units and more to every CTA; 1300 rows are more than the schedule's table holds
     H_q, H_kv, d, page = 16, 1, 128, 32
     rng = np.random.RandomState(2)
-    tokens = [int(t) for t in rng.randint(0, 80, 800)]
+    tokens = [int(t) for t in rng.randint(0, 80, rows)]
     lens = [t + int(rng.randint(0, 30)) for t in tokens]
     table, pages = _table(lens, page, 6, junk=BIG)
     q = _randn(1, sum(tokens), H_q, d)
@@ -781,7 +781,7 @@ def test_many_short_prompts_are_dealt_out_whole(causal):
                                  max_tokens=80, causal=causal)
     api.check()
     first = np.cumsum([0] + tokens)
-    for b in [0, 1, 31, 32, 33, 798, 799] + list(rng.randint(0, 800, 60)):
+    for b in [0, 1, 31, 32, 33, rows - 2, rows - 1] + list(rng.randint(0, rows, 60)):
         a, e = first[b], first[b + 1]
         _check(o[a:e], lse[a:e], q[a:e], kp, vp, table[b:b + 1], tokens[b:b + 1], lens[b:b + 1],
                causal, 1 / math.sqrt(d), f"row {b}")
@@ -822,3 +822,11 @@ def test_calls_on_two_streams_at_once():
     for i in range(2):
         for r in got[i]:
             assert all(torch.equal(a, b) for a, b in zip(r, want[i]))
+
+
+@pytest.mark.parametrize("page", [128, 384, 1024])
+@pytest.mark.parametrize("heads", ["g8x2", "g3d64"])
+def test_pages_of_several_tiles(page, heads):
+    _attend(heads, [1, 1], [3000, 385], page)
+    _attend(heads, [1, 150, 7], [2500, 1000, 385], page)
+    _attend(heads, [400, 40, 200] * 2, [400, 385, 1030] * 2, page)
