@@ -162,7 +162,7 @@ struct __align__(16) Item {
     int k_row;   // packed index of the row's first own key
     int off;     // own key of token 0 (keys minus queries)
     int n_own;   // own keys
-    int pad;
+    int loaders; // paged_attention: warps that copy its pages, up to p.loaders
 };
 static_assert(sizeof(Item) == 64, "four 16-byte copies");
 
@@ -359,6 +359,8 @@ constexpr int kPagedWhole = 12;
 constexpr int kPagedMergeCost = 8 * BN;
 constexpr int kPagedShare = 3 * BN;  // least length of a share: two tiles of any unit it crosses
 
+constexpr int kLongItem = 16;  // tiles of an item of kPaged whose pages two warps copy
+
 struct PagedRow {
     int q0, T, n, blocks;
     int64_t line;  // length of its blocks against one KV head
@@ -405,8 +407,8 @@ __device__ __forceinline__ PagedRow paged_row(const Params& p, int b, bool& bad)
 // heads run together even where their K and V are larger than L2: one group of
 // heads after another, each within L2, ends on heavy items several times (one
 // sequence of 64K tokens, 16/8 heads: 11.9 ms in groups, 10.8 this way).
-template <int kMode>
-__device__ __forceinline__ void schedule_prompts(const Params& p, int2* seqs, Publisher<>& pub,
+template <int kMode, typename Pub>
+__device__ __forceinline__ void schedule_prompts(const Params& p, int2* seqs, Pub& pub,
                                                  int lane) {
     const int block = 2 * p.tok;
     bool bad = false;
@@ -558,6 +560,8 @@ __device__ __forceinline__ void schedule_prompts(const Params& p, int2* seqs, Pu
         w.n0 = cdiv(group_last<kMode>(p, w, 0), BN);
         w.n1 = w.tok0 + p.tok < w.T ? cdiv(group_last<kMode>(p, w, 1), BN) : 0;
         w.n = max(w.n0, w.n1);
+        // (small pages: a second loader, which keeps this warp from the next item meanwhile)
+        if (kMode == kPaged) w.loaders = w.n >= kLongItem ? p.loaders : 1;
         if (!pub.put(w, lane)) return;
     }
     Item end{};
@@ -728,7 +732,7 @@ __device__ __forceinline__ void schedule_tree(const Params& p, Publisher<>& pub,
 // nothing to do), also when a share is longer than kPagedWhole of the longest units.
 // I: an integer type that holds every position of the line (64-bit divisions cost a
 // microsecond before a CTA's first item).
-template <typename I, typename Pub>
+template <int kMode, typename I, typename Pub>
 __device__ __forceinline__ void schedule_line(const Params& p, const PagedRow& row_0, I total,
                                               bool whole, Pub& pub, int lane) {
     bool bad = false;  // (reported by the caller)
@@ -824,6 +828,7 @@ __device__ __forceinline__ void schedule_line(const Params& p, const PagedRow& r
             w.n_own = r.n;
             w.off = r.n - r.T;
             w.tok0 = block * 2 * p.tok;
+            w.loaders = alt_mode(kMode) ? p.loaders : 1;
             const int limit = paged_limit(p, r, block), tiles_of = cdiv(limit, BN);
             int j1 = tiles_of, parts = 1;
             bool take = true;
@@ -916,14 +921,14 @@ __device__ __forceinline__ void schedule_paged(const Params& p, int2* seqs, Pub&
             schedule_prompts<kPaged>(p, seqs, pub, lane);
             return;
         }
-        if (total < (1 << 30)) schedule_line(p, row_0, int(total), false, pub, lane);
-        else schedule_line(p, row_0, total, false, pub, lane);
+        if (total < (1 << 30)) schedule_line<kMode>(p, row_0, int(total), false, pub, lane);
+        else schedule_line<kMode>(p, row_0, total, false, pub, lane);
     } else {
         const bool whole = p.whole || unit * kPagedWhole <= share ||
                            (total < (1 << 30) &&
                             cdiv(units, ctas) * unit <= share + kPagedMergeCost / 2);
-        if (total < (1 << 30)) schedule_line(p, row_0, int(total), whole, pub, lane);
-        else schedule_line(p, row_0, total, whole, pub, lane);
+        if (total < (1 << 30)) schedule_line<kMode>(p, row_0, int(total), whole, pub, lane);
+        else schedule_line<kMode>(p, row_0, total, whole, pub, lane);
     }
 }
 
@@ -946,7 +951,9 @@ __device__ __forceinline__ int v_position(int j, int n) {
 // warp: `loader` of p.loaders copies every p.loaders-th page of a tile, and a slot's barrier
 // counts both. (A decode step of 32 rows from pages of 16 / 32 keys: 162 / 140 us, with
 // one loader 215 / 162; of 64 keys 140. Copied by the lanes of one warp, 16 bytes each,
-// 334 / 252.)
+// 334 / 252.) kPaged has a second loader for long items that are not cut (a prompt of 8192
+// tokens, 64/8 heads, pages of 16 / 32 keys: 822 / 755 us, without 1042 / 814; in short items, as
+// the prompts of 0 to 2047 tokens, it holds the schedule up, 228 / 202 without and 231 / 228 with).
 template <int D, int kMode>
 __device__ __forceinline__ void load_pages(const Params& p, const Item& w, int n, int lane,
                                            const CUtensorMap* tmap_k,
@@ -964,8 +971,8 @@ __device__ __forceinline__ void load_pages(const Params& p, const Item& w, int n
         const int i = first + window * 32 + lane;
         return i < pages ? table[i] : 0;
     };
-    const int per_loader = per_tile / p.loaders;
-    const int box = lane % per_loader * p.loaders + loader, half = lane / per_loader;
+    const int per_loader = per_tile / w.loaders;
+    const int box = lane % per_loader * w.loaders + loader, half = lane / per_loader;
     // The current window is that of the last V tile; K tiles run at most two tiles
     // (16 pages) ahead of it.
     int window = 0, ids = fetch(0), next = fetch(1);
@@ -1001,9 +1008,11 @@ __device__ __forceinline__ void load_pages(const Params& p, const Item& w, int n
             if (ri >= Gm::kRing)
                 alive = mbar_wait_bounded(smem_u32(&bars[bSlotEmpty + s]),
                                           ((ri / Gm::kRing) - 1) & 1, p.status);
-            if (alive)
-                mbar_arrive_expect_tx(full, uint32_t((boxes - loader + p.loaders - 1) / p.loaders *
+            if (alive) {
+                mbar_arrive_expect_tx(full, uint32_t((boxes - loader + w.loaders - 1) / w.loaders *
                                                      rows * 128 * Gm::kBoxes));
+                if (w.loaders < p.loaders) mbar_arrive(full);
+            }
         }
         alive = __all_sync(0xffffffffu, alive);
         if (!alive) break;
@@ -1561,28 +1570,28 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       } else if (warp == 2) {
         // --------------------------------------------------------- scheduler
-        if constexpr (kPages && kAlt) {
+        if constexpr (kPages) {
             int r = 0, issued = 0;  // ring items before this item, and issued
-            const uint64_t policy = l2_policy_evict_first();
+            const uint64_t policy = p.single ? l2_policy_evict_first() : l2_policy_evict_normal();
             auto second_loader = [&](const Item& w, int) {
-                if (p.loaders == 1 || w.n <= 0) return true;
+                if (w.n <= 0) return true;
                 bool ok = true;
-                load_pages<D, kMode>(p, w, w.n, lane, &tmap_kc, &tmap_vc, policy, bars,
-                                     smem_u32(smem + Gm::kRingOff), 1, r, issued, ok);
+                if (w.loaders == 2)
+                    load_pages<D, kMode>(p, w, w.n, lane, &tmap_kc, &tmap_vc, policy, bars,
+                                         smem_u32(smem + Gm::kRingOff), 1, r, issued, ok);
                 r += 2 * w.n;
                 return ok;
             };
             Publisher<decltype(second_loader)> pub{smem + Gm::kItemOff, bars, p.status,
                                                    second_loader};
-            schedule_paged<kMode>(p, nullptr, pub, lane);
+            schedule_paged<kMode>(p, reinterpret_cast<int2*>(smem + Gm::kSeqOff), pub, lane);
+            // (a slot that the other loader has filled again held a copy that landed)
             if (lane == 0)
-                for (int i = max(0, issued - kRing); i < issued; ++i) ring_wait(i);
+                for (int i = max(0, max(issued, r) - kRing); i < issued; ++i) ring_wait(i);
         }
         Publisher<> pub{smem + Gm::kItemOff, bars, p.status};
         if constexpr (kTree)
             schedule_tree<kMode>(p, pub, lane);
-        else if constexpr (kMode == kPaged)
-            schedule_paged<kMode>(p, reinterpret_cast<int2*>(smem + Gm::kSeqOff), pub, lane);
         else if constexpr (kMode == kPrompts)
             schedule_prompts<kMode>(p, reinterpret_cast<int2*>(smem + Gm::kSeqOff), pub, lane);
       } else {
@@ -2585,9 +2594,7 @@ extern "C" int gqa_attn_paged_attention(
     if (!p.status || sms <= 0) return GQA_ERR_CUDA;
     p.B = B; p.H_q = H_q; p.H_kv = H_kv; p.G = H_q / H_kv; p.total_q = total;
     p.table = block_table; p.table_width = table_width; p.page_size = page_size;
-    // (Beside several items of two groups a second loader costs more than it gives: the
-    // step of chunks and single tokens takes 110 us with it, 87 without.)
-    p.loaders = plan.alt && page_size < 64 ? 2 : 1;
+    p.loaders = page_size < 64 ? 2 : 1;
     p.num_pages = num_pages; p.v_pages = v_pages; p.v_page = num_pages > 1 ? v_page_stride : 0;
     const int slots = num_pages > 0 ? table_width * page_size : 0;
     p.S_max = max_keys > 0 && max_keys < slots ? max_keys : slots;

@@ -830,3 +830,25 @@ def test_pages_of_several_tiles(page, heads):
     _attend(heads, [1, 1], [3000, 385], page)
     _attend(heads, [1, 150, 7], [2500, 1000, 385], page)
     _attend(heads, [400, 40, 200] * 2, [400, 385, 1030] * 2, page)
+
+
+@pytest.mark.parametrize("heads", ["g8x2", "g3d64"])
+def test_the_page_size_does_not_change_a_bit(heads):
+    # long and short prompts, whole and cut rows, single tokens: pages are copied by one warp or
+    # two, box by box or tile by tile, and hold the same keys
+    H_q, H_kv, d = HEADS[heads]
+    for tokens, lens in (([3000, 100, 2500, 40], [3000, 100, 2500, 40]),
+                         ([300, 1, 1], [9000, 5000, 77]), ([1] * 5, [9000, 5000, 77, 1, 640])):
+        n = sum(lens)
+        q, k, v = _randn(1, sum(tokens), H_q, d), _randn(2, n, H_kv, d), _randn(3, n, H_kv, d)
+        want = None
+        for page in (128, 16, 32, 64, 256):
+            table, pages = _table(lens, page, page)
+            kp = torch.zeros(pages, H_kv, page, d, dtype=torch.bfloat16, device="cuda")
+            vp = torch.zeros_like(kp)
+            api.paged_append(kp, vp, k, v, _i32(table), _i32([0] * len(lens)), cu_seqlens=_cu(lens))
+            got = api.paged_attention(q, kp, vp, _i32(table), _i32(lens), cu_seqlens=_cu(tokens),
+                                      max_tokens=max(tokens), max_keys=max(lens))
+            api.check()
+            want = want or got
+            assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]), page
